@@ -13,6 +13,12 @@
  *     [ceil(N/128), K/128], each scale folded once per 128-K block onto an
  *     fp32 outer accumulator.
  *
+ * and, for MXFP4 weights (4-bit codes with an E8M0 scale per 32 values, the
+ * OCP microscaling layout), products of any number of rows with activations in
+ * BF16, MXFP8 or MXFP4, the pair of products of a gated feed-forward block,
+ * and what makes their operands: quantisation, its inverse, and the residual
+ * addition with a root-mean-square norm whose rows leave in MXFP8.
+ *
  * Conventions for every GPU entry point:
  *   - A, B/W, S and C are DEVICE pointers owned by the caller; the library
  *     never frees or keeps them, and allocates nothing per call.
@@ -196,6 +202,126 @@ int w8a16_gemv_batch16_strided(const void *A, const void *W, const float *S, voi
                                uint32_t M, uint32_t N, uint32_t K,
                                uint32_t a_row_stride, uint32_t c_row_stride,
                                hipStream_t stream);
+
+/* ------------------------------------------------ microscaled operators */
+
+/*
+ * A microscaled row of K values (K a multiple of 32) is K element codes and
+ * K/32 scale bytes.  Scale byte s of values 32b .. 32b+31 stands for
+ * 2^(s - 127), 255 for NaN (E8M0).
+ *   WQD_MXFP4  codes uint8 [rows][K/2]: E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3
+ *              the sign), value 2i in the low and 2i+1 in the high nibble of
+ *              byte i
+ *   WQD_MXFP8  codes uint8 [rows][K]: E4M3FN
+ *   scales     uint8 [rows][K/32], for both
+ */
+#define WQD_MXFP4      4
+#define WQD_MXFP8      8
+#define WQD_TYPE_BF16  0
+#define WQD_TYPE_FP16  1
+#define WQD_TYPE_FP32  2
+#define WQD_MX_BLOCK        32          /* values that share a scale */
+#define WQD_MX_MAX_K        (1u << 20)  /* largest K of the products */
+#define WQD_MX_MAX_STRIDE   (1u << 21)  /* largest BF16 activation pitch of the products */
+#define WQD_MX_MAX_ROWS     (1u << 24)  /* largest M and N of the products */
+#define WQD_MX_NORM_MAX_K   (1u << 15)  /* largest K of add_rmsnorm_mx8 */
+#define WQD_MX_NORM_MAX_M   (1u << 21)  /* largest M of add_rmsnorm_mx8 */
+#define WQD_MX_MAX_VALUES   (1ull << 36) /* largest M * K of mx_quantize and mx_dequantize */
+
+/*
+ * mx_quantize - rows of BF16, FP16 or FP32 values to MXFP4 or MXFP8.  Per
+ * block of 32: e = max(floor(log2 max|x|) - emax, -127), emax 2 (MXFP4) or 8
+ * (MXFP8); s = e + 127; code = x / 2^e rounded to nearest even and saturated at
+ * the format's largest value (6, 448); the sign of a zero is kept.  A block of
+ * zeros has s = 0; a block that holds an infinity or NaN has s = 255 and codes
+ * 0, so that all of it reads back as NaN.
+ *
+ *   X             device, row m at X + m * x_row_stride elements, 16-byte aligned
+ *   x_type        WQD_TYPE_BF16, WQD_TYPE_FP16 or WQD_TYPE_FP32
+ *   Q, S          device, codes (16-byte aligned) and scales of M rows
+ *   format        WQD_MXFP4 or WQD_MXFP8
+ *   M             rows; M = 0 returns WQD_OK and launches nothing
+ *   K             a positive multiple of 32, at most WQD_Q2_0_MAX_K; M * K at
+ *                 most WQD_MX_MAX_VALUES
+ *   x_row_stride  >= K, whole 16-byte pieces (a multiple of 8, FP32: of 4)
+ */
+int mx_quantize(const void *X, uint32_t x_type, void *Q, void *S, uint32_t format,
+                uint32_t M, uint32_t K, uint32_t x_row_stride, hipStream_t stream);
+
+/*
+ * mx_dequantize - the values of MXFP4 or MXFP8 rows: code * 2^(s - 127) in
+ * fp32, rounded to nearest even to y_type (exact in FP32, and in BF16 but for
+ * values beyond its range).  Arguments as for mx_quantize; Y is 16-byte
+ * aligned and its pitch whole 16-byte pieces; padding is not written.
+ */
+int mx_dequantize(const void *Q, const void *S, uint32_t format, void *Y, uint32_t y_type,
+                  uint32_t M, uint32_t K, uint32_t y_row_stride, hipStream_t stream);
+
+/*
+ * add_rmsnorm_mx8 - residual addition, root-mean-square norm and MXFP8 rows:
+ *   h = bf16(x + r);  y = h / sqrt(mean_k(h^2) + eps) * g  (fp32);
+ *   (Q, S) = y in MXFP8, as mx_quantize rounds it;  Y = bf16(y).
+ * The mean is that of the BF16 h; its sum is held in fp32.
+ *
+ *   X  device, BF16, row m at X + m * x_row_stride, 16-byte aligned
+ *   R  device, BF16 residual rows, pitch r_row_stride, 16-byte aligned; or NULL:
+ *      h = x, and H must be NULL too
+ *   G  device, BF16 [K], 16-byte aligned
+ *   H  device, BF16, pitch r_row_stride, 16-byte aligned; may be R (the
+ *      residual is updated in place), or X where the pitches are equal
+ *   Y  device, BF16 [M][K], 16-byte aligned; or NULL where only MXFP8 is wanted
+ *   Q, S  device, MXFP8 codes (16-byte aligned) and scales of M rows
+ *   M  rows (0: nothing is launched), at most WQD_MX_NORM_MAX_M;  K  a
+ *      positive multiple of 32, at most WQD_MX_NORM_MAX_K;  strides >= K and multiples of 8;  eps finite, >= 0
+ */
+int add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *Y, void *Q, void *S,
+                    uint32_t M, uint32_t K, uint32_t x_row_stride, uint32_t r_row_stride, float eps,
+                    hipStream_t stream);
+
+/*
+ * w4a16_gemm, w4a8_gemm, w4a4_gemm - products with MXFP4 weights:
+ *   C[m,n] = bf16( sum_k a[m,k] * w[n,k] ),  sums in fp32,
+ * with activations in BF16, MXFP8 and MXFP4.
+ *
+ *   A   device, BF16, row m at A + m * a_row_stride, 16-byte aligned (w4a16);
+ *       MXFP8 or MXFP4 codes [M][K] or [M][K/2], 16-byte aligned
+ *   AS  device, scales [M][K/32], 4-byte aligned
+ *   W   device, MXFP4 codes [N][K/2], 16-byte aligned
+ *   WS  device, scales [N][K/32], 4-byte aligned
+ *   C   device, BF16, row m at C + m * c_row_stride, 2-byte aligned; only
+ *       columns < N of rows < M are written
+ *   M   rows, from one to a long prompt (0: nothing is launched)
+ *   N   >= 1;  K  a positive multiple of 128, at most WQD_MX_MAX_K
+ *   a_row_stride  >= K, a multiple of 8, at most WQD_MX_MAX_STRIDE
+ *   c_row_stride  >= N
+ *   M and N at most WQD_MX_MAX_ROWS (else WQD_EUNSUPPORTED)
+ *
+ * A NaN or infinity in an activation row, or a scale of 255, reaches that
+ * row's (column's) outputs only.  The same call gives the same bits each time;
+ * the order of the sums depends on M, N and K.
+ */
+int w4a16_gemm(const void *A, const void *W, const void *WS, void *C, uint32_t M, uint32_t N, uint32_t K,
+               uint32_t a_row_stride, uint32_t c_row_stride, hipStream_t stream);
+int w4a8_gemm(const void *A, const void *AS, const void *W, const void *WS, void *C,
+              uint32_t M, uint32_t N, uint32_t K, uint32_t c_row_stride, hipStream_t stream);
+int w4a4_gemm(const void *A, const void *AS, const void *W, const void *WS, void *C,
+              uint32_t M, uint32_t N, uint32_t K, uint32_t c_row_stride, hipStream_t stream);
+
+/*
+ * w4a16_gated, w4a8_gated, w4a4_gated - both projections of a gated
+ * feed-forward block and its activation in one launch:
+ *   C[m,n] = bf16( silu(sum_k a[m,k] wg[n,k]) * sum_k a[m,k] wu[n,k] ),
+ * silu(x) = x / (1 + exp(-x)), sums and activation in fp32.  WG, WGS and WU,
+ * WUS are the gate and up matrices [N][K/2] and their scales; the rest is as
+ * for the products above.
+ */
+int w4a16_gated(const void *A, const void *WG, const void *WGS, const void *WU, const void *WUS, void *C,
+                uint32_t M, uint32_t N, uint32_t K, uint32_t a_row_stride, uint32_t c_row_stride,
+                hipStream_t stream);
+int w4a8_gated(const void *A, const void *AS, const void *WG, const void *WGS, const void *WU, const void *WUS,
+               void *C, uint32_t M, uint32_t N, uint32_t K, uint32_t c_row_stride, hipStream_t stream);
+int w4a4_gated(const void *A, const void *AS, const void *WG, const void *WGS, const void *WU, const void *WUS,
+               void *C, uint32_t M, uint32_t N, uint32_t K, uint32_t c_row_stride, hipStream_t stream);
 
 /* ----------------------------------------------------------- host helpers */
 

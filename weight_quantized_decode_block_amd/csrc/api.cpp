@@ -8,6 +8,7 @@
 // w8a16_gemm_m16 and its _n64 and _strided variants).
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -130,6 +131,63 @@ int validate_pitches(const char *fn, uint32_t M, uint32_t N, uint32_t K, uint32_
       static_cast<uint64_t>(M - 1) * c_row_stride + N > 0xFFFFFFFFull)
     return fail(WQD_EINVAL, "%s: row pitches too large (the strided span exceeds 2^32 elements)", fn);
   return WQD_OK;
+}
+
+// Rows of a microscaled quantisation or its inverse: the values' type and
+// pitch, the format, and sizes that one launch covers.
+int validate_mx_rows(const char *fn, const void *V, const char *v_name, uint32_t type, const void *Q, const void *S,
+                     uint32_t format, uint32_t M, uint32_t K, uint32_t row_stride) {
+  if (!V || !Q || !S) return fail(WQD_ENULL, "%s: %s, Q and S must be non-NULL", fn, v_name);
+  if (type != WQD_TYPE_BF16 && type != WQD_TYPE_FP16 && type != WQD_TYPE_FP32)
+    return fail(WQD_EINVAL, "%s: type %u of %s is not BF16, FP16 or FP32", fn, type, v_name);
+  if (format != WQD_MXFP4 && format != WQD_MXFP8)
+    return fail(WQD_EINVAL, "%s: format %u is neither MXFP4 nor MXFP8", fn, format);
+  if (K == 0 || K % WQD_MX_BLOCK != 0) return fail(WQD_EINVAL, "%s: K=%u is not a positive multiple of 32", fn, K);
+  if (K > WQD_Q2_0_MAX_K) return fail(WQD_EUNSUPPORTED, "%s: K=%u above %u", fn, K, (unsigned)WQD_Q2_0_MAX_K);
+  const uint32_t piece = type == WQD_TYPE_FP32 ? 4u : 8u;
+  if (row_stride < K || row_stride % piece != 0)
+    return fail(WQD_EINVAL, "%s: row stride %u must be at least K=%u and a multiple of %u (16-byte rows)", fn,
+                row_stride, K, piece);
+  if (static_cast<uint64_t>(M) * K > WQD_MX_MAX_VALUES)
+    return fail(WQD_EUNSUPPORTED, "%s: %u rows of %u values are too many for one call", fn, M, K);
+  if (!aligned(V, 16)) return fail(WQD_EALIGN, "%s: %s must be 16-byte aligned", fn, v_name);
+  if (!aligned(Q, 16)) return fail(WQD_EALIGN, "%s: Q must be 16-byte aligned", fn);
+  return WQD_OK;
+}
+
+// One product or gated pair of products with MXFP4 weights: checks, then the
+// kernel.  A BF16 call has no activation scales; a quantised one has pitch K.
+int run_mx_product(const char *fn, wqd::MxOperands op, wqd::MxFormat fmt, bool gated, hipStream_t stream) {
+  const bool bf16 = fmt == wqd::MxFormat::kBf16;
+  if (!op.A || !op.W || !op.WS || !op.C || (!bf16 && !op.AS) || (gated && (!op.WU || !op.WUS)))
+    return fail(WQD_ENULL, "%s: operands must be non-NULL", fn);
+  if (op.N == 0) return fail(WQD_EINVAL, "%s: N must be >= 1", fn);
+  if (op.K == 0 || op.K % 128u != 0) return fail(WQD_EINVAL, "%s: K=%u is not a positive multiple of 128", fn, op.K);
+  if (op.K > WQD_MX_MAX_K) return fail(WQD_EUNSUPPORTED, "%s: K=%u above %u", fn, op.K, (unsigned)WQD_MX_MAX_K);
+  if (op.lda < op.K || op.ldc < op.N)
+    return fail(WQD_EINVAL, "%s: row strides must cover the rows (a_row_stride=%u < K=%u or c_row_stride=%u < N=%u)",
+                fn, op.lda, op.K, op.ldc, op.N);
+  if (op.lda % 8u != 0)
+    return fail(WQD_EINVAL, "%s: a_row_stride=%u is not a multiple of 8 (16-byte activation rows)", fn, op.lda);
+  if (op.lda > WQD_MX_MAX_STRIDE)
+    return fail(WQD_EUNSUPPORTED, "%s: a_row_stride=%u above %u", fn, op.lda, (unsigned)WQD_MX_MAX_STRIDE);
+  if (op.M > WQD_MX_MAX_ROWS || op.N > WQD_MX_MAX_ROWS)
+    return fail(WQD_EUNSUPPORTED, "%s: M=%u or N=%u above %u", fn, op.M, op.N, (unsigned)WQD_MX_MAX_ROWS);
+  if (!aligned(op.A, 16)) return fail(WQD_EALIGN, "%s: A must be 16-byte aligned", fn);
+  if (!aligned(op.W, 16) || !aligned(op.WU, 16)) return fail(WQD_EALIGN, "%s: weights must be 16-byte aligned", fn);
+  if (!aligned(op.AS, 4) || !aligned(op.WS, 4) || !aligned(op.WUS, 4))
+    return fail(WQD_EALIGN, "%s: scales must be 4-byte aligned", fn);
+  if (!aligned(op.C, 2)) return fail(WQD_EALIGN, "%s: C must be 2-byte aligned", fn);
+  if (op.M == 0) return WQD_OK;  // no rows: nothing to launch
+  if (int rc = check_device(fn)) return rc;
+  op.c_wide = aligned(op.C, 8) && op.ldc % 4u == 0;
+  (void)hipGetLastError();
+  return check_launch(fn, wqd::launch_mx_skinny(op, fmt, gated, stream));
+}
+
+wqd::MxOperands mx_operands(const void *A, const void *AS, const void *W, const void *WS, const void *WU,
+                            const void *WUS, void *C, uint32_t M, uint32_t N, uint32_t K, uint32_t lda, uint32_t ldc) {
+  return {A, AS, W, WS, WU, WUS, static_cast<uint16_t *>(C), M, N, K, lda, ldc, 0u};
 }
 
 // 16-row tiles per workgroup in w8a16_gemm_m16_n64: 64 weight rows each.
@@ -262,6 +320,87 @@ int w8a16_gemv_batch16_strided(const void *A, const void *W, const float *S, voi
 int w8a16_gemv_batch16(const void *A, const void *W, const float *S, void *C, uint32_t M, uint32_t N, uint32_t K,
                        hipStream_t stream) {
   return w8a16_gemv_batch16_strided(A, W, S, C, M, N, K, K, N, stream);
+}
+
+int mx_quantize(const void *X, uint32_t x_type, void *Q, void *S, uint32_t format, uint32_t M, uint32_t K,
+                uint32_t x_row_stride, hipStream_t stream) {
+  static const char fn[] = "mx_quantize";
+  int rc = validate_mx_rows(fn, X, "X", x_type, Q, S, format, M, K, x_row_stride);
+  if (rc) return rc;
+  if (M == 0) return WQD_OK;  // no rows: nothing to launch
+  if ((rc = check_device(fn))) return rc;
+  (void)hipGetLastError();
+  return check_launch(fn, wqd::launch_mx_quantize(X, x_type, Q, S, format == WQD_MXFP4, M, K, x_row_stride, stream));
+}
+
+int mx_dequantize(const void *Q, const void *S, uint32_t format, void *Y, uint32_t y_type, uint32_t M, uint32_t K,
+                  uint32_t y_row_stride, hipStream_t stream) {
+  static const char fn[] = "mx_dequantize";
+  int rc = validate_mx_rows(fn, Y, "Y", y_type, Q, S, format, M, K, y_row_stride);
+  if (rc) return rc;
+  if (M == 0) return WQD_OK;
+  if ((rc = check_device(fn))) return rc;
+  (void)hipGetLastError();
+  return check_launch(fn, wqd::launch_mx_dequantize(Q, S, format == WQD_MXFP4, Y, y_type, M, K, y_row_stride, stream));
+}
+
+int add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *Y, void *Q, void *S, uint32_t M,
+                    uint32_t K, uint32_t x_row_stride, uint32_t r_row_stride, float eps, hipStream_t stream) {
+  static const char fn[] = "add_rmsnorm_mx8";
+  if (!X || !G || !Q || !S) return fail(WQD_ENULL, "%s: X, G, Q and S must be non-NULL", fn);
+  if (!R != !H) return fail(WQD_ENULL, "%s: R and H must both be given or both be NULL", fn);
+  if (K == 0 || K % WQD_MX_BLOCK != 0) return fail(WQD_EINVAL, "%s: K=%u is not a positive multiple of 32", fn, K);
+  if (K > WQD_MX_NORM_MAX_K) return fail(WQD_EUNSUPPORTED, "%s: K=%u above %u", fn, K, (unsigned)WQD_MX_NORM_MAX_K);
+  if (M > WQD_MX_NORM_MAX_M) return fail(WQD_EUNSUPPORTED, "%s: M=%u rows are too many for one call", fn, M);
+  if (x_row_stride < K || x_row_stride % 8u != 0 || (R && (r_row_stride < K || r_row_stride % 8u != 0)))
+    return fail(WQD_EINVAL, "%s: row strides %u, %u must be at least K=%u and multiples of 8 (16-byte rows)", fn,
+                x_row_stride, r_row_stride, K);
+  if (H == X && x_row_stride != r_row_stride)
+    return fail(WQD_EINVAL, "%s: H may be X only where their row strides are equal (%u, %u)", fn, x_row_stride,
+                r_row_stride);
+  if (!std::isfinite(eps) || eps < 0.0f) return fail(WQD_EINVAL, "%s: eps must be finite and not negative", fn);
+  if (!aligned(X, 16) || !aligned(R, 16) || !aligned(G, 16) || !aligned(H, 16) || !aligned(Y, 16) || !aligned(Q, 16))
+    return fail(WQD_EALIGN, "%s: X, R, G, H, Y and Q must be 16-byte aligned", fn);
+  if (M == 0) return WQD_OK;
+  if (int rc = check_device(fn)) return rc;
+  (void)hipGetLastError();
+  return check_launch(fn, wqd::launch_add_rmsnorm_mx8(X, R, G, H, Y, Q, S, M, K, x_row_stride, r_row_stride, eps, stream));
+}
+
+int w4a16_gemm(const void *A, const void *W, const void *WS, void *C, uint32_t M, uint32_t N, uint32_t K,
+               uint32_t a_row_stride, uint32_t c_row_stride, hipStream_t stream) {
+  return run_mx_product("w4a16_gemm", mx_operands(A, nullptr, W, WS, nullptr, nullptr, C, M, N, K, a_row_stride, c_row_stride),
+                        wqd::MxFormat::kBf16, false, stream);
+}
+
+int w4a8_gemm(const void *A, const void *AS, const void *W, const void *WS, void *C, uint32_t M, uint32_t N, uint32_t K,
+              uint32_t c_row_stride, hipStream_t stream) {
+  return run_mx_product("w4a8_gemm", mx_operands(A, AS, W, WS, nullptr, nullptr, C, M, N, K, K, c_row_stride),
+                        wqd::MxFormat::kFp8, false, stream);
+}
+
+int w4a4_gemm(const void *A, const void *AS, const void *W, const void *WS, void *C, uint32_t M, uint32_t N, uint32_t K,
+              uint32_t c_row_stride, hipStream_t stream) {
+  return run_mx_product("w4a4_gemm", mx_operands(A, AS, W, WS, nullptr, nullptr, C, M, N, K, K, c_row_stride),
+                        wqd::MxFormat::kFp4, false, stream);
+}
+
+int w4a16_gated(const void *A, const void *WG, const void *WGS, const void *WU, const void *WUS, void *C, uint32_t M,
+                uint32_t N, uint32_t K, uint32_t a_row_stride, uint32_t c_row_stride, hipStream_t stream) {
+  return run_mx_product("w4a16_gated", mx_operands(A, nullptr, WG, WGS, WU, WUS, C, M, N, K, a_row_stride, c_row_stride),
+                        wqd::MxFormat::kBf16, true, stream);
+}
+
+int w4a8_gated(const void *A, const void *AS, const void *WG, const void *WGS, const void *WU, const void *WUS, void *C,
+               uint32_t M, uint32_t N, uint32_t K, uint32_t c_row_stride, hipStream_t stream) {
+  return run_mx_product("w4a8_gated", mx_operands(A, AS, WG, WGS, WU, WUS, C, M, N, K, K, c_row_stride),
+                        wqd::MxFormat::kFp8, true, stream);
+}
+
+int w4a4_gated(const void *A, const void *AS, const void *WG, const void *WGS, const void *WU, const void *WUS, void *C,
+               uint32_t M, uint32_t N, uint32_t K, uint32_t c_row_stride, hipStream_t stream) {
+  return run_mx_product("w4a4_gated", mx_operands(A, AS, WG, WGS, WU, WUS, C, M, N, K, K, c_row_stride),
+                        wqd::MxFormat::kFp4, true, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,98 @@
+// What the kernels of products with MXFP4 weights share: the operands of a
+// lane, the matrix instructions on them and the output store.
+#pragma once
+
+#include "mx_common.h"
+#include "wqd_internal.h"
+
+namespace wqd {
+
+// One lane's activations of a 128-k step: 32 BF16 values, 32 8-bit or 32
+// 4-bit codes, and the scale byte of its k block.
+template <MxFormat FMT>
+struct ActRegs {
+  u32x4_t v[FMT == MxFormat::kBf16 ? 4 : (FMT == MxFormat::kFp8 ? 2 : 1)];
+  uint32_t s;
+};
+
+// One lane's 32 weights of a step: BF16 (converted and scaled) or as stored.
+template <MxFormat FMT>
+struct WeightRegs {
+  u32x4_t v[FMT == MxFormat::kBf16 ? 4 : 1];
+  uint32_t s;
+  WeightRegs() = default;
+  __device__ __forceinline__ WeightRegs(const u32x4_t &codes, uint32_t scale) {
+    if constexpr (FMT == MxFormat::kBf16) {
+      const float f = e8m0_value(scale);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j].x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j], f, 0));
+        v[j].y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j], f, 1));
+        v[j].z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j], f, 2));
+        v[j].w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j], f, 3));
+      }
+      s = 0;
+    } else {
+      v[0] = codes;
+      s = scale;
+    }
+  }
+};
+
+// acc[n,m] += sum over the step's 128 k of w[n,k] a[m,k]; lane l ends with
+// n = 4 (l / 16) + i in element i and m = l % 16.
+template <MxFormat FMT>
+__device__ __forceinline__ f32x4_t mx_mfma(const WeightRegs<FMT> &w, const ActRegs<FMT> &a, f32x4_t acc) {
+  if constexpr (FMT == MxFormat::kBf16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w.v[j]),
+                                                    __builtin_bit_cast(bf16x8_t, a.v[j]), acc, 0, 0, 0);
+    return acc;
+  } else {
+    const i32x8_t wv = {(int)w.v[0].x, (int)w.v[0].y, (int)w.v[0].z, (int)w.v[0].w, 0, 0, 0, 0};
+    if constexpr (FMT == MxFormat::kFp8) {
+      const i32x8_t av = {(int)a.v[0].x, (int)a.v[0].y, (int)a.v[0].z, (int)a.v[0].w,
+                          (int)a.v[1].x, (int)a.v[1].y, (int)a.v[1].z, (int)a.v[1].w};
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, acc, 4, 0, 0, (int)w.s, 0, (int)a.s);
+    } else {
+      const i32x8_t av = {(int)a.v[0].x, (int)a.v[0].y, (int)a.v[0].z, (int)a.v[0].w, 0, 0, 0, 0};
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, acc, 4, 4, 0, (int)w.s, 0, (int)a.s);
+    }
+  }
+}
+
+// Bytes of n activation values
+template <MxFormat FMT>
+__device__ __forceinline__ uint32_t act_bytes(uint32_t n) {
+  return FMT == MxFormat::kBf16 ? 2u * n : (FMT == MxFormat::kFp8 ? n : n >> 1);
+}
+
+// A buffer over `rows` rows of `bytes` bytes from row r0 on, `pitch` bytes
+// apart; everything past the last row's end reads as zero.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *p, uint32_t r0, uint32_t rows, uint32_t pitch,
+                                                            uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t *>(static_cast<const uint8_t *>(p) + (uint64_t)r0 * pitch), (short)0,
+      (int)((rows - 1u) * pitch + bytes), 0x00020000);
+}
+
+// silu(g) * u.  exp(-g) overflows to infinity for g below -88, where the
+// quotient is the correct -0.
+__device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+
+// Four consecutive outputs of row m: one 8-byte store where C and its pitch
+// allow it, else one by one; columns past N are not written.
+__device__ __forceinline__ void store4(const MxOperands &op, uint32_t m, uint32_t n, const f32x4_t &c) {
+  uint16_t *p = op.C + (uint64_t)m * op.ldc + n;
+  const u32x2_t v = {bf16x2_rne(c[0], c[1]), bf16x2_rne(c[2], c[3])};
+  if (op.c_wide && n + 4u <= op.N) {
+    *reinterpret_cast<u32x2_t *>(p) = v;
+  } else {
+#pragma unroll
+    for (uint32_t i = 0; i < 4u; ++i)
+      if (n + i < op.N) p[i] = (uint16_t)(v[i >> 1] >> (16u * (i & 1u)));
+  }
+}
+
+}  // namespace wqd

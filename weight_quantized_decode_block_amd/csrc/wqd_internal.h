@@ -62,4 +62,33 @@ hipError_t launch_w8a16_gemv(const void *A, const void *W, const float *S,
 // row of K does not fit).
 uint32_t w8a16_gemv_rows_per_launch(uint32_t K);
 
+// Activation formats of the products with MXFP4 weights.
+enum class MxFormat : int { kBf16, kFp8, kFp4 };
+
+// Operands of one product (or gated pair of products) with MXFP4 weights.
+// Scales are E8M0 bytes [rows][K/32]; the codes of quantised activations have
+// pitch K.  Shapes validated by the caller.
+struct MxOperands {
+  const void *A, *AS;    // activations, their scales (unused for BF16)
+  const void *W, *WS;    // weights [N][K/2]; the gate matrix of a gated product
+  const void *WU, *WUS;  // the up matrix of a gated product
+  uint16_t *C;           // BF16, row pitch ldc
+  uint32_t M, N, K, lda, ldc;
+  uint32_t c_wide;       // every 4 columns of C start on an 8-byte boundary
+};
+
+// Enqueue a product (gated: silu of the first times the second) on the kernel
+// for few rows, which takes any M.
+hipError_t launch_mx_skinny(const MxOperands &op, MxFormat fmt, bool gated, hipStream_t stream);
+
+// Enqueue quantisation of M rows to MXFP4 or MXFP8, its inverse, and the
+// residual addition with a root-mean-square norm (R and H, and Y, may be
+// null).  `type` is one of WQD_TYPE_*; pitches in elements.
+hipError_t launch_mx_quantize(const void *X, uint32_t type, void *Q, void *S, bool fp4, uint32_t M, uint32_t K,
+                              uint32_t ldx, hipStream_t stream);
+hipError_t launch_mx_dequantize(const void *Q, const void *S, bool fp4, void *Y, uint32_t type, uint32_t M, uint32_t K,
+                                uint32_t ldy, hipStream_t stream);
+hipError_t launch_add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *Y, void *Q, void *S,
+                                  uint32_t M, uint32_t K, uint32_t ldx, uint32_t ldr, float eps, hipStream_t stream);
+
 }  // namespace wqd

@@ -24,6 +24,8 @@ Q2_0_GROUP = 128
 Q2_0_BLOCK_BYTES = 34
 Q2_0_BATCHM_MAX_M = 8
 W8A16_MAX_M = 16
+MXFP4, MXFP8 = 4, 8  # WQD_MXFP4, WQD_MXFP8
+TYPE_BF16, TYPE_FP16, TYPE_FP32 = range(3)  # WQD_TYPE_*
 Q2_0_TIER_WIDTHS = (1, 2, 4, 6, 8)  # WQD_Q2_0_TIER_WIDTHS, narrowest first
 
 _lib = None
@@ -54,6 +56,18 @@ def lib() -> ctypes.CDLL:
     L.w8a16_gemv_batch16_strided.argtypes = [vp, vp, vp, vp, u32, u32, u32, u32, u32, vp]
     for f in (L.q2_0_gemv, L.q2_0_gemv_batchm, L.w8a16_gemm_m16, L.w8a16_gemm_m16_n64,
               L.w8a16_gemm_m16_strided, L.w8a16_gemv_batch16, L.w8a16_gemv_batch16_strided):
+        f.restype = ctypes.c_int
+    L.mx_quantize.argtypes = [vp, u32, vp, vp, u32, u32, u32, u32, vp]
+    L.mx_dequantize.argtypes = [vp, vp, u32, vp, u32, u32, u32, u32, vp]
+    L.add_rmsnorm_mx8.argtypes = [vp, vp, vp, vp, vp, vp, vp, u32, u32, u32, u32, ctypes.c_float, vp]
+    L.w4a16_gemm.argtypes = [vp, vp, vp, vp, u32, u32, u32, u32, u32, vp]
+    L.w4a16_gated.argtypes = [vp, vp, vp, vp, vp, vp, u32, u32, u32, u32, u32, vp]
+    for f in (L.w4a8_gemm, L.w4a4_gemm):
+        f.argtypes = [vp, vp, vp, vp, vp, u32, u32, u32, u32, vp]
+    for f in (L.w4a8_gated, L.w4a4_gated):
+        f.argtypes = [vp, vp, vp, vp, vp, vp, vp, u32, u32, u32, u32, vp]
+    for f in (L.mx_quantize, L.mx_dequantize, L.add_rmsnorm_mx8, L.w4a16_gemm, L.w4a8_gemm, L.w4a4_gemm,
+              L.w4a16_gated, L.w4a8_gated, L.w4a4_gated):
         f.restype = ctypes.c_int
     L.q2_0_packed_bytes.argtypes = [u32, u32]
     L.q2_0_packed_bytes.restype = sz
@@ -153,6 +167,156 @@ def w8a16_gemv_batch16_strided(A, W, S, C, M: int, N: int, K: int, a_row_stride:
     _check("w8a16_gemv_batch16_strided",
            lib().w8a16_gemv_batch16_strided(_ptr(A), _ptr(W), _ptr(S), _ptr(C), M, N, K, a_row_stride,
                                             c_row_stride, _stream(stream)))
+
+
+# ---------------------------------------------------- microscaled operators
+_MX_FORMATS = {"mxfp4": MXFP4, "mxfp8": MXFP8, MXFP4: MXFP4, MXFP8: MXFP8}
+_types = None
+
+
+def _sizes(fn: str, bits: int) -> None:
+    """`bits`: the sizes and pitches of a call or-ed together; each must fit the C ABI's 32 bits."""
+    if bits >> 32:
+        raise ValueError(f"{fn}: sizes and strides must be from 0 to 2^32 - 1")
+
+
+def _span(rows: int, pitch: int, width: int, size: int) -> int:
+    """Bytes from the first row's start to the last row's end."""
+    return ((rows - 1) * pitch + width) * size if rows > 0 else 0
+
+
+def _arg(fn: str, name: str, x, nbytes: int) -> int | None:
+    """Device address of an operand.  A tensor must live on the current device
+    (its stream is the one the call goes to), with rows packed as the call says
+    (the last dimension contiguous), and reach `nbytes` from its first element;
+    an integer is taken as it is."""
+    if x is None or isinstance(x, int):
+        return x
+    device = x.get_device()
+    if device < 0 or device != _current_device():
+        raise ValueError(f"{fn}: {name} is not on the current GPU")
+    if x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
+        raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
+    if x.untyped_storage().nbytes() - x.storage_offset() * x.element_size() < nbytes:
+        raise ValueError(f"{fn}: {name} holds fewer than the {nbytes} bytes the call reaches")
+    return x.data_ptr()
+
+
+_current_device_raw = None
+
+
+def _current_device() -> int:
+    global _current_device_raw
+    if _current_device_raw is None:
+        import torch
+        _current_device_raw = torch.cuda.current_device
+    return _current_device_raw()
+
+
+def _type_of(fn: str, x, given: int | None) -> int:
+    """WQD_TYPE_* of a tensor's values (an address comes with its type)."""
+    global _types
+    if isinstance(x, int) or x is None:
+        return TYPE_BF16 if given is None else given
+    if _types is None:
+        import torch
+        _types = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}
+    t = _types.get(x.dtype)
+    if t is None or given not in (None, t):
+        raise ValueError(f"{fn}: values must be BF16, FP16 or FP32, as their tensor is ({x.dtype})")
+    return t
+
+
+def _mx_format(fn: str, fmt) -> int:
+    try:
+        return _MX_FORMATS[fmt]
+    except (KeyError, TypeError):
+        raise ValueError(f"{fn}: format {fmt!r} is neither 'mxfp4' nor 'mxfp8'") from None
+
+
+def _code_bytes(fmt: int, n: int) -> int:
+    return n // 2 if fmt == MXFP4 else n
+
+
+def mx_quantize(X, Q, S, fmt, M: int, K: int, x_row_stride: int | None = None, x_type: int | None = None,
+                stream=None) -> None:
+    """Rows of X to `fmt` ("mxfp4" or "mxfp8") codes Q and scale bytes S.  The
+    type is the tensor's; with an address pass `x_type` (default BF16)."""
+    fn, ld = "mx_quantize", K if x_row_stride is None else x_row_stride
+    _sizes(fn, M | K | ld)
+    f, t = _mx_format(fn, fmt), _type_of(fn, X, x_type)
+    _check(fn, lib().mx_quantize(_arg(fn, "X", X, _span(M, ld, K, 4 if t == TYPE_FP32 else 2)), t,
+                                 _arg(fn, "Q", Q, _code_bytes(f, M * K)), _arg(fn, "S", S, M * K // 32), f, M, K, ld,
+                                 _stream(stream)))
+
+
+def mx_dequantize(Q, S, Y, fmt, M: int, K: int, y_row_stride: int | None = None, y_type: int | None = None,
+                  stream=None) -> None:
+    """The values of `fmt` rows, in Y's type."""
+    fn, ld = "mx_dequantize", K if y_row_stride is None else y_row_stride
+    _sizes(fn, M | K | ld)
+    f, t = _mx_format(fn, fmt), _type_of(fn, Y, y_type)
+    _check(fn, lib().mx_dequantize(_arg(fn, "Q", Q, _code_bytes(f, M * K)), _arg(fn, "S", S, M * K // 32), f,
+                                   _arg(fn, "Y", Y, _span(M, ld, K, 4 if t == TYPE_FP32 else 2)), t, M, K, ld,
+                                   _stream(stream)))
+
+
+def add_rmsnorm_mx8(X, R, G, H, Y, Q, S, M: int, K: int, eps: float, x_row_stride: int | None = None,
+                    r_row_stride: int | None = None, stream=None) -> None:
+    """h = X + R (R and H may be None), its root-mean-square norm times G in
+    MXFP8 (Q, S) and, unless Y is None, in BF16."""
+    fn = "add_rmsnorm_mx8"
+    lx, lr = K if x_row_stride is None else x_row_stride, K if r_row_stride is None else r_row_stride
+    _sizes(fn, M | K | lx | lr)
+    rows = _span(M, lr, K, 2)
+    _check(fn, lib().add_rmsnorm_mx8(_arg(fn, "X", X, _span(M, lx, K, 2)), _arg(fn, "R", R, rows),
+                                     _arg(fn, "G", G, 2 * K), _arg(fn, "H", H, rows), _arg(fn, "Y", Y, 2 * M * K),
+                                     _arg(fn, "Q", Q, M * K), _arg(fn, "S", S, M * K // 32), M, K, lx, lr, eps,
+                                     _stream(stream)))
+
+
+def _a16(fn: str, M: int, N: int, K: int, A, weights, C, a_row_stride, c_row_stride, stream) -> None:
+    lda, ldc = K if a_row_stride is None else a_row_stride, N if c_row_stride is None else c_row_stride
+    _sizes(fn, M | N | K | lda | ldc)
+    w = [_arg(fn, "weights", x, N * K // (32 if i & 1 else 2)) for i, x in enumerate(weights)]
+    _check(fn, getattr(lib(), fn)(_arg(fn, "A", A, _span(M, lda, K, 2)), *w, _arg(fn, "C", C, _span(M, ldc, N, 2)),
+                                  M, N, K, lda, ldc, _stream(stream)))
+
+
+def _quantised(fn: str, fmt: int, M: int, N: int, K: int, A, AS, weights, C, c_row_stride, stream) -> None:
+    ldc = N if c_row_stride is None else c_row_stride
+    _sizes(fn, M | N | K | ldc)
+    w = [_arg(fn, "weights", x, N * K // (32 if i & 1 else 2)) for i, x in enumerate(weights)]
+    _check(fn, getattr(lib(), fn)(_arg(fn, "A", A, _code_bytes(fmt, M * K)), _arg(fn, "AS", AS, M * K // 32), *w,
+                                  _arg(fn, "C", C, _span(M, ldc, N, 2)), M, N, K, ldc, _stream(stream)))
+
+
+def w4a16_gemm(A, W, WS, C, M: int, N: int, K: int, a_row_stride: int | None = None,
+               c_row_stride: int | None = None, stream=None) -> None:
+    _a16("w4a16_gemm", M, N, K, A, (W, WS), C, a_row_stride, c_row_stride, stream)
+
+
+def w4a8_gemm(A, AS, W, WS, C, M: int, N: int, K: int, c_row_stride: int | None = None, stream=None) -> None:
+    _quantised("w4a8_gemm", MXFP8, M, N, K, A, AS, (W, WS), C, c_row_stride, stream)
+
+
+def w4a4_gemm(A, AS, W, WS, C, M: int, N: int, K: int, c_row_stride: int | None = None, stream=None) -> None:
+    _quantised("w4a4_gemm", MXFP4, M, N, K, A, AS, (W, WS), C, c_row_stride, stream)
+
+
+def w4a16_gated(A, WG, WGS, WU, WUS, C, M: int, N: int, K: int, a_row_stride: int | None = None,
+                c_row_stride: int | None = None, stream=None) -> None:
+    _a16("w4a16_gated", M, N, K, A, (WG, WGS, WU, WUS), C, a_row_stride, c_row_stride, stream)
+
+
+def w4a8_gated(A, AS, WG, WGS, WU, WUS, C, M: int, N: int, K: int, c_row_stride: int | None = None,
+               stream=None) -> None:
+    _quantised("w4a8_gated", MXFP8, M, N, K, A, AS, (WG, WGS, WU, WUS), C, c_row_stride, stream)
+
+
+def w4a4_gated(A, AS, WG, WGS, WU, WUS, C, M: int, N: int, K: int, c_row_stride: int | None = None,
+               stream=None) -> None:
+    _quantised("w4a4_gated", MXFP4, M, N, K, A, AS, (WG, WGS, WU, WUS), C, c_row_stride, stream)
 
 
 # ------------------------------------------------------------ host helpers
