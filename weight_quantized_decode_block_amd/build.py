@@ -15,7 +15,7 @@ LIB = os.path.join(PKG, "libwqd.so")
 # bench-only helper (a plain read of a buffer: the read ceiling bench.py reports)
 BENCH_LIB = os.path.join(PKG, "libwqd_bench.so")
 SOURCES = ["api.cpp", "pack.cpp", "q2_0_mfma.hip", "q2_0_valu.hip", "w8a16_gemm_m16.hip", "w8a16_gemv.hip",
-           "mx_quant.hip", "mx_skinny.hip"]
+           "mx_quant.hip", "mx_skinny.hip", "mx_tile.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -40,8 +40,9 @@ struct WeightRegs {
 };
 
 // acc[n,m] += sum over the step's 128 k of w[n,k] a[m,k]; lane l ends with
-// n = 4 (l / 16) + i in element i and m = l % 16.
-template <MxFormat FMT>
+// n = 4 (l / 16) + i in element i and m = l % 16.  B: the byte of the scale
+// registers to use.
+template <MxFormat FMT, int B = 0>
 __device__ __forceinline__ f32x4_t mx_mfma(const WeightRegs<FMT> &w, const ActRegs<FMT> &a, f32x4_t acc) {
   if constexpr (FMT == MxFormat::kBf16) {
 #pragma unroll
@@ -54,12 +55,26 @@ __device__ __forceinline__ f32x4_t mx_mfma(const WeightRegs<FMT> &w, const ActRe
     if constexpr (FMT == MxFormat::kFp8) {
       const i32x8_t av = {(int)a.v[0].x, (int)a.v[0].y, (int)a.v[0].z, (int)a.v[0].w,
                           (int)a.v[1].x, (int)a.v[1].y, (int)a.v[1].z, (int)a.v[1].w};
-      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, acc, 4, 0, 0, (int)w.s, 0, (int)a.s);
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, acc, 4, 0, B, (int)w.s, B, (int)a.s);
     } else {
       const i32x8_t av = {(int)a.v[0].x, (int)a.v[0].y, (int)a.v[0].z, (int)a.v[0].w, 0, 0, 0, 0};
-      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, acc, 4, 4, 0, (int)w.s, 0, (int)a.s);
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, acc, 4, 4, B, (int)w.s, B, (int)a.s);
     }
   }
+}
+
+constexpr uint32_t kMxMaxGrid = 1u << 22;  // workgroups of one launch, which holds fewer than 2^32 threads
+
+// Rows [m, m + rows) of a product.
+inline MxOperands mx_rows(const MxOperands &op, MxFormat fmt, uint32_t m, uint32_t rows) {
+  MxOperands part = op;
+  const uint64_t values = (uint64_t)m * op.lda;
+  part.A = static_cast<const uint8_t *>(op.A) +
+           (fmt == MxFormat::kBf16 ? values * 2u : (fmt == MxFormat::kFp8 ? values : values / 2u));
+  if (fmt != MxFormat::kBf16) part.AS = static_cast<const uint8_t *>(op.AS) + (uint64_t)m * (op.K / 32u);
+  part.C = op.C + (uint64_t)m * op.ldc;
+  part.M = op.M - m < rows ? op.M - m : rows;
+  return part;
 }
 
 // Bytes of n activation values

@@ -35,7 +35,6 @@ namespace {
 constexpr uint32_t kWaves = 8;
 constexpr uint32_t kThreads = 64 * kWaves;
 constexpr uint32_t kPastEnd = 0x80000000u;
-constexpr uint32_t kMaxGrid = 1u << 22;  // workgroups of one launch
 
 template <MxFormat FMT, int MT>
 struct StepRegs {
@@ -150,15 +149,10 @@ __global__ __launch_bounds__(kThreads) void mx_skinny_kernel(MxOperands op) {
 
 template <MxFormat FMT, int MT, bool GATED, int DEPTH>
 hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
-  // a launch holds fewer than 2^32 threads, so very many outputs take several
   const uint32_t tiles = (op.N + 15u) / 16u;
-  const uint32_t rows = kMaxGrid / tiles * 16u * MT;  // N <= 2^24, so at least one chunk
-  MxOperands part = op;
+  const uint32_t rows = kMxMaxGrid / tiles * 16u * MT;  // N <= 2^24, so at least one chunk
   for (uint32_t m = 0; m < op.M; m += rows) {
-    part.A = static_cast<const uint8_t *>(op.A) + (FMT == MxFormat::kFp4 ? (uint64_t)m * op.lda / 2u : (uint64_t)m * op.lda * (FMT == MxFormat::kBf16 ? 2u : 1u));
-    if (FMT != MxFormat::kBf16) part.AS = static_cast<const uint8_t *>(op.AS) + (uint64_t)m * (op.K / 32u);
-    part.C = op.C + (uint64_t)m * op.ldc;
-    part.M = op.M - m < rows ? op.M - m : rows;
+    const MxOperands part = mx_rows(op, FMT, m, rows);
     const uint32_t chunks = (part.M + 16u * MT - 1u) / (16u * MT);
     hipLaunchKernelGGL((mx_skinny_kernel<FMT, MT, GATED, DEPTH>), dim3(tiles * chunks), dim3(kThreads), 0, stream, part);
     const hipError_t e = hipGetLastError();

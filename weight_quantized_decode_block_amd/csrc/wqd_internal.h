@@ -81,6 +81,10 @@ struct MxOperands {
 // for few rows, which takes any M.
 hipError_t launch_mx_skinny(const MxOperands &op, MxFormat fmt, bool gated, hipStream_t stream);
 
+// The same on the kernel for many rows, for K of at least 512.
+bool mx_tile_supports(const MxOperands &op);
+hipError_t launch_mx_tile(const MxOperands &op, MxFormat fmt, bool gated, hipStream_t stream);
+
 // Enqueue quantisation of M rows to MXFP4 or MXFP8, its inverse, and the
 // residual addition with a root-mean-square norm (R and H, and Y, may be
 // null).  `type` is one of WQD_TYPE_*; pitches in elements.
