@@ -159,14 +159,14 @@ int validate_mx_rows(const char *fn, const void *V, const char *v_name, uint32_t
 // kernel.  A BF16 call has no activation scales; a quantised one has pitch K.
 int run_mx_product(const char *fn, wqd::MxOperands op, wqd::MxFormat fmt, bool gated, hipStream_t stream) {
   const bool bf16 = fmt == wqd::MxFormat::kBf16;
-  if (!op.A || !op.W || !op.WS || !op.C || (!bf16 && !op.AS) || (gated && (!op.WU || !op.WUS)))
+  if (!op.A || !op.W || !op.WS || !op.out.C || (!bf16 && !op.AS) || (gated && (!op.WU || !op.WUS)))
     return fail(WQD_ENULL, "%s: operands must be non-NULL", fn);
   if (op.N == 0) return fail(WQD_EINVAL, "%s: N must be >= 1", fn);
   if (op.K == 0 || op.K % 128u != 0) return fail(WQD_EINVAL, "%s: K=%u is not a positive multiple of 128", fn, op.K);
   if (op.K > WQD_MX_MAX_K) return fail(WQD_EUNSUPPORTED, "%s: K=%u above %u", fn, op.K, (unsigned)WQD_MX_MAX_K);
-  if (op.lda < op.K || op.ldc < op.N)
+  if (op.lda < op.K || op.out.ldc < op.N)
     return fail(WQD_EINVAL, "%s: row strides must cover the rows (a_row_stride=%u < K=%u or c_row_stride=%u < N=%u)",
-                fn, op.lda, op.K, op.ldc, op.N);
+                fn, op.lda, op.K, op.out.ldc, op.N);
   if (op.lda % 8u != 0)
     return fail(WQD_EINVAL, "%s: a_row_stride=%u is not a multiple of 8 (16-byte activation rows)", fn, op.lda);
   if (op.lda > WQD_MX_MAX_STRIDE)
@@ -177,10 +177,10 @@ int run_mx_product(const char *fn, wqd::MxOperands op, wqd::MxFormat fmt, bool g
   if (!aligned(op.W, 16) || !aligned(op.WU, 16)) return fail(WQD_EALIGN, "%s: weights must be 16-byte aligned", fn);
   if (!aligned(op.AS, 4) || !aligned(op.WS, 4) || !aligned(op.WUS, 4))
     return fail(WQD_EALIGN, "%s: scales must be 4-byte aligned", fn);
-  if (!aligned(op.C, 2)) return fail(WQD_EALIGN, "%s: C must be 2-byte aligned", fn);
+  if (!aligned(op.out.C, 2)) return fail(WQD_EALIGN, "%s: C must be 2-byte aligned", fn);
   if (op.M == 0) return WQD_OK;  // no rows: nothing to launch
   if (int rc = check_device(fn)) return rc;
-  op.c_wide = aligned(op.C, 8) && op.ldc % 4u == 0;
+  op.out.wide = aligned(op.out.C, 8) && op.out.ldc % 4u == 0;
   (void)hipGetLastError();
   const bool tile = op.M > 64u && wqd::mx_tile_supports(op);
   return check_launch(fn, tile ? wqd::launch_mx_tile(op, fmt, gated, stream) : wqd::launch_mx_skinny(op, fmt, gated, stream));
@@ -188,7 +188,7 @@ int run_mx_product(const char *fn, wqd::MxOperands op, wqd::MxFormat fmt, bool g
 
 wqd::MxOperands mx_operands(const void *A, const void *AS, const void *W, const void *WS, const void *WU,
                             const void *WUS, void *C, uint32_t M, uint32_t N, uint32_t K, uint32_t lda, uint32_t ldc) {
-  return {A, AS, W, WS, WU, WUS, static_cast<uint16_t *>(C), M, N, K, lda, ldc, 0u};
+  return {A, AS, W, WS, WU, WUS, M, N, K, lda, {static_cast<uint16_t *>(C), ldc, 0u}};
 }
 
 // 16-row tiles per workgroup in w8a16_gemm_m16_n64: 64 weight rows each.

@@ -72,7 +72,7 @@ inline MxOperands mx_rows(const MxOperands &op, MxFormat fmt, uint32_t m, uint32
   part.A = static_cast<const uint8_t *>(op.A) +
            (fmt == MxFormat::kBf16 ? values * 2u : (fmt == MxFormat::kFp8 ? values : values / 2u));
   if (fmt != MxFormat::kBf16) part.AS = static_cast<const uint8_t *>(op.AS) + (uint64_t)m * (op.K / 32u);
-  part.C = op.C + (uint64_t)m * op.ldc;
+  part.out.C = op.out.C + (uint64_t)m * op.out.ldc;
   part.M = op.M - m < rows ? op.M - m : rows;
   return part;
 }
@@ -98,15 +98,15 @@ __device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f
 
 // Four consecutive outputs of row m: one 8-byte store where C and its pitch
 // allow it, else one by one; columns past N are not written.
-__device__ __forceinline__ void store4(const MxOperands &op, uint32_t m, uint32_t n, const f32x4_t &c) {
-  uint16_t *p = op.C + (uint64_t)m * op.ldc + n;
+__device__ __forceinline__ void store4(const MxOut &out, uint32_t N, uint32_t m, uint32_t n, const f32x4_t &c) {
+  uint16_t *p = out.C + (uint64_t)m * out.ldc + n;
   const u32x2_t v = {bf16x2_rne(c[0], c[1]), bf16x2_rne(c[2], c[3])};
-  if (op.c_wide && n + 4u <= op.N) {
+  if (out.wide && n + 4u <= N) {
     *reinterpret_cast<u32x2_t *>(p) = v;
   } else {
 #pragma unroll
     for (uint32_t i = 0; i < 4u; ++i)
-      if (n + i < op.N) p[i] = (uint16_t)(v[i >> 1] >> (16u * (i & 1u)));
+      if (n + i < N) p[i] = (uint16_t)(v[i >> 1] >> (16u * (i & 1u)));
   }
 }
 

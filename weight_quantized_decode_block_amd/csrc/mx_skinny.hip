@@ -6,11 +6,22 @@
 // a in BF16, MXFP8 or MXFP4 and w in MXFP4 (scale per 32 k on both sides),
 // all sums in fp32.  The weights' bytes bound it: each is read once.
 //
-// A workgroup of 8 waves owns 16 weight rows (of both matrices in the gated
-// form) and 16 * MT activation rows; its waves take the 128-k steps in turn and
-// add their partial tiles in LDS, in wave order, at the end.  In a step lane
-// (r, g) = (lane % 16, lane / 16) loads the 16 bytes of weight block g (32
-// codes) of row r straight from memory and its scale byte:
+// A workgroup of 8 waves owns 16 * NT weight rows (of both matrices in the
+// gated form) and up to MMAX activation rows, and walks K in segments of 1024:
+// wave w takes the segment's w-th 128-k step, and the waves' partial tiles are
+// added in LDS, in wave order, at the end.
+//   * A wave loads its own step's weights, DEPTH segments ahead, four
+//     neighbouring lanes the four 16-byte pieces of a row, and turns them through
+//     a KB of LDS of its own into the matrix operand's order: lane (r, g) =
+//     (lane % 16, lane / 16) takes k block g (32 codes) of row r.  Loaded in that
+//     order at once (neighbours in different rows) the weights come at a quarter
+//     of the rate.
+//   * Everything else of a segment, the activations and both sides' scale
+//     bytes, goes through LDS (two buffers, one barrier per segment), loaded
+//     in whole 16-byte pieces and dwords and DEPTH segments ahead in registers.
+//     Loaded by each lane for itself, as the weights are, these small pieces
+//     cost as many vector-memory instructions as the weights several times
+//     over, and those bound the kernel.
 //   * MXFP8 and MXFP4 activations: v_mfma_scale_f32_16x16x128_f8f6f4 takes the
 //     codes and scale bytes as they are, the weights as its first operand.  It
 //     wants 4-bit k = 32g .. 32g+31 from lane group g, and of 8-bit values
@@ -19,9 +30,8 @@
 //   * BF16 activations: the codes become BF16 pairs, scaled in the conversion
 //     (exact: two significand bits and a power of two), and instruction j of
 //     four 16x16x32 ones takes k = 32g + 8j .. 32g + 8j + 7 of both sides.
-// A lane keeps DEPTH steps in flight in registers; requests past the last step
-// or row fall outside the buffer and come back as zeros, which add nothing.
-// The result is 4 consecutive n of one m per lane.
+// Requests past the last step or row fall outside the buffer and come back as
+// zeros, which add nothing.  A lane ends with 4 consecutive n of one m.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -32,129 +42,217 @@
 namespace wqd {
 namespace {
 
-constexpr uint32_t kWaves = 8;
-constexpr uint32_t kThreads = 64 * kWaves;
 constexpr uint32_t kPastEnd = 0x80000000u;
 
-template <MxFormat FMT, int MT>
-struct StepRegs {
-  u32x4_t w, wu;         // 32 weight codes of this lane's block (wu: up matrix)
-  uint32_t ws, wus;      // their scale bytes
-  ActRegs<FMT> a[MT];
-};
+template <MxFormat FMT>
+constexpr uint32_t kStepBytes = FMT == MxFormat::kBf16 ? 256 : (FMT == MxFormat::kFp8 ? 128 : 64);  // of an activation row
 
-template <MxFormat FMT, int MT, bool GATED, int DEPTH>
-__global__ __launch_bounds__(kThreads) void mx_skinny_kernel(MxOperands op) {
-  __shared__ f32x4_t part[GATED ? 2 : 1][kWaves][MT][64];
-  const uint32_t lane = threadIdx.x & 63u;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+template <MxFormat FMT, int NW, int MMAX, int NT, bool GATED, int DEPTH>
+__global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const uint8_t *__restrict__ W,
+                                                             const uint8_t *__restrict__ WS,
+                                                             const uint8_t *__restrict__ A, uint32_t K, uint32_t M,
+                                                             uint32_t N, uint32_t lda, const uint8_t *__restrict__ AS,
+                                                             const uint8_t *__restrict__ WU,
+                                                             const uint8_t *__restrict__ WUS, MxOut out) {
+  constexpr int MT = (MMAX + 15) / 16, G = GATED ? 2 : 1, WT = NT * G;  // 16-row tiles: activations, matrices, weights
+  constexpr bool kActScales = FMT != MxFormat::kBf16;
+  constexpr uint32_t kWaves = NW, kThreads = 64 * NW, kRowBytes = NW * kStepBytes<FMT>;  // of a segment's activation row
+  constexpr uint32_t kScaleBytes = 4 * NW;                                               // of a segment's scale row
+  // LDS rows are 16 bytes longer than the segment: the 16 lanes that read the
+  // same piece of 16 rows then use all 64 banks
+  constexpr uint32_t kPitch = kRowBytes + 16, kPieces = kRowBytes / 16;
+  constexpr uint32_t kARegion = MMAX * kPitch;
+  constexpr uint32_t kWsRows = 16 * WT, kScaleRows = kWsRows + (kActScales ? MMAX : 0);  // kScaleBytes each
+  constexpr uint32_t kBuffer = kARegion + kScaleRows * kScaleBytes;
+  constexpr int SA = (MMAX * kPieces + kThreads - 1) / kThreads, SS = (kScaleRows + 63) / 64;
+  constexpr uint32_t kParts = kWaves * WT * MT * 1024;
+  constexpr uint32_t kTurn = 2 * kBuffer;  // each wave's own KB per weight tile
+  constexpr uint32_t kLds = kTurn + NW * WT * 1024 > kParts ? kTurn + NW * WT * 1024 : kParts;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+
+  const uint32_t tid = threadIdx.x, lane = tid & 63u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t r = lane & 15u, g = lane >> 4;
-  const uint32_t chunks = (op.M + 16u * MT - 1u) / (16u * MT);
+  const uint32_t chunks = (M + MMAX - 1u) / MMAX;
   const uint32_t tile = blockIdx.x / chunks;
-  const uint32_t n0 = tile * 16u, m0 = (blockIdx.x - tile * chunks) * (16u * MT);
-  const uint32_t nb = op.K >> 5, steps = op.K >> 7;
-  const uint32_t nrows = op.N - n0 < 16u ? op.N - n0 : 16u;
-  const uint32_t mrows = op.M - m0 < 16u * MT ? op.M - m0 : 16u * MT;
+  const uint32_t n0 = tile * 16u * NT, m0 = (blockIdx.x - tile * chunks) * MMAX;
+  const uint32_t nb = K >> 5, steps = K >> 7, nseg = (steps + NW - 1u) / NW, wpitch = K >> 1;
+  const uint32_t nrows = N - n0 < 16u * NT ? N - n0 : 16u * NT;
+  const uint32_t mrows = M - m0 < (uint32_t)MMAX ? M - m0 : (uint32_t)MMAX;
+  const uint32_t apitch = act_bytes<FMT>(lda), arow = act_bytes<FMT>(K);
 
-  const __amdgpu_buffer_rsrc_t wr = rows_rsrc(op.W, n0, nrows, op.K >> 1, op.K >> 1);
-  const __amdgpu_buffer_rsrc_t wsr = rows_rsrc(op.WS, n0, nrows, nb, nb);
-  const __amdgpu_buffer_rsrc_t ur = rows_rsrc(GATED ? op.WU : op.W, n0, nrows, op.K >> 1, op.K >> 1);
-  const __amdgpu_buffer_rsrc_t usr = rows_rsrc(GATED ? op.WUS : op.WS, n0, nrows, nb, nb);
-  const uint32_t apitch = act_bytes<FMT>(op.lda), arow = act_bytes<FMT>(op.K);
-  const __amdgpu_buffer_rsrc_t ar = rows_rsrc(op.A, m0, mrows, apitch, arow);
-  const __amdgpu_buffer_rsrc_t asr = rows_rsrc(FMT == MxFormat::kBf16 ? op.A : op.AS, m0, mrows, nb, nb);
+  const __amdgpu_buffer_rsrc_t ar = rows_rsrc(A, m0, mrows, apitch, arow);
+  const __amdgpu_buffer_rsrc_t wr = rows_rsrc(W, n0, nrows, wpitch, wpitch);
+  const __amdgpu_buffer_rsrc_t ur = rows_rsrc(GATED ? WU : W, n0, nrows, wpitch, wpitch);
 
-  auto load = [&](uint32_t s) __attribute__((always_inline)) {
-    StepRegs<FMT, MT> x;
+  // scale rows of this wave's staging slots: weight rows (gated: 16 of the gate
+  // matrix, 16 of the up matrix, ...), then activation rows, 64 / NW per slot, so
+  // a slot's matrix is the same for the wave.  soff: this lane's first byte, or
+  // past the end.
+  __amdgpu_buffer_rsrc_t sr[SS];
+  uint32_t soff[SS];
+#pragma unroll
+  for (int u = 0; u < SS; ++u) {
+    constexpr uint32_t kRows = 64 / NW, kSlots = 16 / kRows;  // rows of a slot, slots of a tile
+    const uint32_t slot = wave + (uint32_t)u * kWaves, t = slot / kSlots;
+    const bool act = kActScales && t >= (uint32_t)WT;
+    const uint8_t *p = act ? AS : (GATED && (t & 1u) ? WUS : WS);
+    const uint32_t rows = act ? mrows : (t < (uint32_t)WT ? nrows : 0u);
+    const uint32_t row = (act ? slot * kRows - kWsRows : t / G * 16u + slot % kSlots * kRows) + lane / NW;
+    sr[u] = rows_rsrc(p, act ? m0 : n0, rows > 0u ? rows : 1u, nb, nb);
+    soff[u] = row < rows ? row * nb + lane % NW * 4u : kPastEnd;
+  }
+  const uint32_t sbyte = lane % NW * 4u;
+
+  // weights of segment i for this lane: tile t of each matrix
+  struct WSeg {
+    u32x4_t v[WT];
+  };
+  auto load_w = [&](uint32_t i) __attribute__((always_inline)) {
+    WSeg x;
+    const uint32_t s = i * NW + wave;
     const bool in = s < steps;
-    const uint32_t wo = in ? r * (op.K >> 1) + s * 64u + g * 16u : kPastEnd;
-    const uint32_t so = in ? r * nb + s * 4u + g : kPastEnd;
-    x.w = __builtin_amdgcn_raw_buffer_load_b128(wr, wo, 0, 0);
-    x.ws = __builtin_amdgcn_raw_buffer_load_b8(wsr, so, 0, 0);
-    if constexpr (GATED) {
-      x.wu = __builtin_amdgcn_raw_buffer_load_b128(ur, wo, 0, 0);
-      x.wus = __builtin_amdgcn_raw_buffer_load_b8(usr, so, 0, 0);
-    }
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const uint32_t m = 16u * t + r;
-      // rows past the last one have an offset of their own past the end: the
-      // pitch may be wider than the row
-      const bool ok = in && m < mrows;
-      const uint32_t ao = m * apitch;
-      if constexpr (FMT == MxFormat::kBf16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          x.a[t].v[j] = __builtin_amdgcn_raw_buffer_load_b128(ar, ok ? ao + s * 256u + g * 64u + 16u * j : kPastEnd, 0, 0);
-      } else {
-        if constexpr (FMT == MxFormat::kFp8) {
-          x.a[t].v[0] = __builtin_amdgcn_raw_buffer_load_b128(ar, ok ? ao + s * 128u + g * 16u : kPastEnd, 0, 0);
-          x.a[t].v[1] = __builtin_amdgcn_raw_buffer_load_b128(ar, ok ? ao + s * 128u + 64u + g * 16u : kPastEnd, 0, 0);
-        } else {
-          x.a[t].v[0] = __builtin_amdgcn_raw_buffer_load_b128(ar, ok ? ao + s * 64u + g * 16u : kPastEnd, 0, 0);
-        }
-        x.a[t].s = __builtin_amdgcn_raw_buffer_load_b8(asr, ok ? m * nb + s * 4u + g : kPastEnd, 0, 0);
-      }
+    for (int t = 0; t < WT; ++t) {
+      const uint32_t o = in ? ((uint32_t)(t / G) * 16u + (lane >> 2)) * wpitch + s * 64u + (lane & 3u) * 16u : kPastEnd;
+      x.v[t] = __builtin_amdgcn_raw_buffer_load_b128(GATED && (t & 1) ? ur : wr, o, 0, 0);
     }
     return x;
   };
-
-  f32x4_t acc[MT], accu[MT];
+  // staged pieces of segment i for this thread
+  struct SSeg {
+    u32x4_t a[SA];
+    uint32_t s[SS];
+  };
+  auto load_s = [&](uint32_t i) __attribute__((always_inline)) {
+    SSeg x;
 #pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = accu[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-
-  StepRegs<FMT, MT> ring[DEPTH];
-  uint32_t next = wave;
-  mx_unroll<0, DEPTH>([&](auto d) __attribute__((always_inline)) {
-    ring[decltype(d)::value] = load(next);
-    next += kWaves;
-  });
-  const uint32_t mine = steps > wave ? (steps - wave + kWaves - 1u) / kWaves : 0u;
-  for (uint32_t i = 0; i < mine; i += DEPTH)
-    mx_unroll<0, DEPTH>([&](auto d) __attribute__((always_inline)) {
-      StepRegs<FMT, MT> &x = ring[decltype(d)::value];
-      WeightRegs<FMT> w(x.w, x.ws), wu;
-      if constexpr (GATED) wu = WeightRegs<FMT>(x.wu, x.wus);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        acc[t] = mx_mfma<FMT>(w, x.a[t], acc[t]);
-        if constexpr (GATED) accu[t] = mx_mfma<FMT>(wu, x.a[t], accu[t]);
-      }
-      x = load(next);
-      next += kWaves;
-    });
-
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    part[0][wave][t][lane] = acc[t];
-    if constexpr (GATED) part[1][wave][t][lane] = accu[t];
-  }
-  __syncthreads();
-  for (uint32_t x = threadIdx.x; x < 64u * MT; x += kThreads) {
-    const uint32_t t = x >> 6, l = x & 63u;
-    f32x4_t c = part[0][0][t][l];
-#pragma unroll
-    for (uint32_t w = 1; w < kWaves; ++w) c += part[0][w][t][l];
-    if constexpr (GATED) {
-      f32x4_t u = part[1][0][t][l];
-#pragma unroll
-      for (uint32_t w = 1; w < kWaves; ++w) u += part[1][w][t][l];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = silu_times(c[i], u[i]);
+    for (int u = 0; u < SA; ++u) {
+      const uint32_t p = tid + (uint32_t)u * kThreads, m = p / kPieces;
+      const uint32_t b = i * kRowBytes + (p % kPieces) * 16u;  // byte of the row
+      x.a[u] = __builtin_amdgcn_raw_buffer_load_b128(ar, m < mrows && b < arow ? m * apitch + b : kPastEnd, 0, 0);
     }
-    const uint32_t m = m0 + 16u * t + (l & 15u), n = n0 + 4u * (l >> 4);
-    if (m < op.M) store4(op, m, n, c);
+#pragma unroll
+    for (int u = 0; u < SS; ++u) {
+      x.s[u] = __builtin_amdgcn_raw_buffer_load_b32(sr[u], i * kScaleBytes + sbyte < nb ? soff[u] + i * kScaleBytes : kPastEnd, 0, 0);
+    }
+    return x;
+  };
+  auto store_s = [&](const SSeg &x, uint32_t buf) __attribute__((always_inline)) {
+    uint8_t *p0 = lds + buf * kBuffer;
+#pragma unroll
+    for (int u = 0; u < SA; ++u) {
+      const uint32_t p = tid + (uint32_t)u * kThreads, m = p / kPieces;
+      if (m < (uint32_t)MMAX) *reinterpret_cast<u32x4_t *>(p0 + m * kPitch + (p % kPieces) * 16u) = x.a[u];
+    }
+#pragma unroll
+    for (int u = 0; u < SS; ++u) {
+      const uint32_t p = tid + (uint32_t)u * kThreads;
+      if (p < kScaleRows * NW) *reinterpret_cast<uint32_t *>(p0 + kARegion + p * 4u) = x.s[u];
+    }
+  };
+
+  f32x4_t acc[WT][MT];
+#pragma unroll
+  for (int t = 0; t < WT; ++t)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[t][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  auto compute = [&](const WSeg &x, uint32_t buf) __attribute__((always_inline)) {
+    const uint8_t *p0 = lds + buf * kBuffer, *ps = p0 + kARegion + wave * 4u + g;
+    // piece p of row r goes to slot p ^ (r / 4): the 16 lanes that read one piece meet all banks
+    uint8_t *turn = lds + kTurn + wave * (WT * 1024u);
+#pragma unroll
+    for (int t = 0; t < WT; ++t)
+      *reinterpret_cast<u32x4_t *>(turn + t * 1024 + (lane >> 2) * 64u + ((lane & 3u) ^ (lane >> 4)) * 16u) = x.v[t];
+    WeightRegs<FMT> w[WT];
+#pragma unroll
+    for (int t = 0; t < WT; ++t)
+      w[t] = WeightRegs<FMT>(*reinterpret_cast<const u32x4_t *>(turn + t * 1024 + r * 64u + (g ^ (r >> 2)) * 16u), ps[(t * 16u + r) * kScaleBytes]);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      // rows past the last staged one repeat row MMAX - 1: their outputs are not stored
+      const uint32_t m = MMAX % 16 == 0 ? j * 16u + r : (j * 16u + r < MMAX ? j * 16u + r : MMAX - 1u);
+      const uint8_t *pa = p0 + m * kPitch;
+      ActRegs<FMT> a;
+      if constexpr (FMT == MxFormat::kBf16) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) a.v[h] = *reinterpret_cast<const u32x4_t *>(pa + wave * 256u + g * 64u + h * 16);
+      } else {
+        a.v[0] = *reinterpret_cast<const u32x4_t *>(pa + wave * (FMT == MxFormat::kFp8 ? 128u : 64u) + g * 16u);
+        if constexpr (FMT == MxFormat::kFp8) a.v[1] = *reinterpret_cast<const u32x4_t *>(pa + wave * 128u + 64u + g * 16u);
+        a.s = ps[(kWsRows + m) * kScaleBytes];
+      }
+#pragma unroll
+      for (int t = 0; t < WT; ++t) acc[t][j] = mx_mfma<FMT>(w[t], a, acc[t][j]);
+    }
+  };
+
+  // segment i + 1 is written to LDS while segment i is computed, so the staged
+  // pieces' ring is one ahead of the weights'
+  SSeg first = load_s(0), sring[DEPTH];
+  WSeg wring[DEPTH];
+  mx_unroll<0, DEPTH>([&](auto d) __attribute__((always_inline)) {
+    wring[decltype(d)::value] = load_w(decltype(d)::value);
+    sring[decltype(d)::value] = load_s(decltype(d)::value + 1);
+  });
+  store_s(first, 0);
+  uint32_t i = 0;
+  auto segment = [&](auto d, auto more) __attribute__((always_inline)) {
+    constexpr int D = decltype(d)::value;
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's LDS accesses
+    __builtin_amdgcn_s_barrier();
+    compute(wring[D], i & 1u);
+    store_s(sring[D], (i + 1u) & 1u);
+    if constexpr (decltype(more)::value) {
+      wring[D] = load_w(i + DEPTH);
+      sring[D] = load_s(i + 1u + DEPTH);
+    }
+    ++i;
+  };
+  // whole rounds of the ring without a branch, so that the compiler's waits
+  // count the requests in flight exactly; the rest requests nothing
+  while (i + DEPTH <= nseg)
+    mx_unroll<0, DEPTH>([&](auto d) __attribute__((always_inline)) { segment(d, std::true_type{}); });
+  mx_unroll<0, DEPTH>([&](auto d) __attribute__((always_inline)) {
+    if (i < nseg) segment(d, std::false_type{});
+  });
+
+  __syncthreads();
+  f32x4_t *part = reinterpret_cast<f32x4_t *>(lds);
+#pragma unroll
+  for (int t = 0; t < WT; ++t)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) part[((wave * WT + t) * MT + j) * 64u + lane] = acc[t][j];
+  __syncthreads();
+  for (uint32_t x = tid; x < 64u * NT * MT; x += kThreads) {
+    const uint32_t l = x & 63u, j = (x >> 6) % MT, t = (x >> 6) / MT;
+    f32x4_t c = part[(t * G * MT + j) * 64u + l];
+#pragma unroll
+    for (uint32_t w = 1; w < kWaves; ++w) c += part[((w * WT + t * G) * MT + j) * 64u + l];
+    if constexpr (GATED) {
+      f32x4_t u = part[((t * G + 1) * MT + j) * 64u + l];
+#pragma unroll
+      for (uint32_t w = 1; w < kWaves; ++w) u += part[((w * WT + t * G + 1) * MT + j) * 64u + l];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = silu_times(c[e], u[e]);
+    }
+    const uint32_t m = m0 + 16u * j + (l & 15u), n = n0 + 16u * t + 4u * (l >> 4);
+    if (m < m0 + mrows) store4(out, N, m, n, c);
   }
 }
 
-template <MxFormat FMT, int MT, bool GATED, int DEPTH>
+template <MxFormat FMT, int NW, int MMAX, int NT, bool GATED, int DEPTH>
 hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
-  const uint32_t tiles = (op.N + 15u) / 16u;
-  const uint32_t rows = kMxMaxGrid / tiles * 16u * MT;  // N <= 2^24, so at least one chunk
+  const uint32_t tiles = (op.N + 16u * NT - 1u) / (16u * NT);
+  const uint32_t rows = kMxMaxGrid / tiles * MMAX;  // N <= 2^24, so at least one chunk
   for (uint32_t m = 0; m < op.M; m += rows) {
     const MxOperands part = mx_rows(op, FMT, m, rows);
-    const uint32_t chunks = (part.M + 16u * MT - 1u) / (16u * MT);
-    hipLaunchKernelGGL((mx_skinny_kernel<FMT, MT, GATED, DEPTH>), dim3(tiles * chunks), dim3(kThreads), 0, stream, part);
+    const uint32_t chunks = (part.M + MMAX - 1u) / MMAX;
+    hipLaunchKernelGGL((mx_skinny_kernel<FMT, NW, MMAX, NT, GATED, DEPTH>), dim3(tiles * chunks), dim3(64 * NW), 0, stream,
+                       static_cast<const uint8_t *>(part.W), static_cast<const uint8_t *>(part.WS),
+                       static_cast<const uint8_t *>(part.A), part.K, part.M, part.N, part.lda,
+                       static_cast<const uint8_t *>(part.AS), static_cast<const uint8_t *>(part.WU),
+                       static_cast<const uint8_t *>(part.WUS), part.out);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -163,9 +261,12 @@ hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
 
 template <MxFormat FMT, bool GATED>
 hipError_t launch_fmt(const MxOperands &op, hipStream_t stream) {
-  if (op.M <= 16u) return launch_cfg<FMT, 1, GATED, 4>(op, stream);
-  if (op.M <= 32u) return launch_cfg<FMT, 2, GATED, 2>(op, stream);
-  return launch_cfg<FMT, 4, GATED, FMT == MxFormat::kBf16 ? 1 : 2>(op, stream);
+  constexpr int kWide = GATED ? 1 : 2;
+  if (op.M <= 2u) return launch_cfg<FMT, 8, 2, 1, GATED, 2>(op, stream);
+  if (op.M <= 4u) return launch_cfg<FMT, 8, 4, 1, GATED, 2>(op, stream);
+  if (op.M <= 8u) return launch_cfg<FMT, 8, 8, 1, GATED, 2>(op, stream);
+  if (op.M <= 16u) return launch_cfg<FMT, 8, 16, kWide, GATED, 2>(op, stream);
+  return launch_cfg<FMT, 8, 32, kWide, GATED, 2>(op, stream);
 }
 
 }  // namespace

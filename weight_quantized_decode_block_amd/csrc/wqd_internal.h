@@ -65,6 +65,13 @@ uint32_t w8a16_gemv_rows_per_launch(uint32_t K);
 // Activation formats of the products with MXFP4 weights.
 enum class MxFormat : int { kBf16, kFp8, kFp4 };
 
+// The output of a product: BF16 rows of pitch ldc.
+struct MxOut {
+  uint16_t *C;
+  uint32_t ldc;
+  uint32_t wide;  // every 4 columns of C start on an 8-byte boundary
+};
+
 // Operands of one product (or gated pair of products) with MXFP4 weights.
 // Scales are E8M0 bytes [rows][K/32]; the codes of quantised activations have
 // pitch K.  Shapes validated by the caller.
@@ -72,9 +79,8 @@ struct MxOperands {
   const void *A, *AS;    // activations, their scales (unused for BF16)
   const void *W, *WS;    // weights [N][K/2]; the gate matrix of a gated product
   const void *WU, *WUS;  // the up matrix of a gated product
-  uint16_t *C;           // BF16, row pitch ldc
-  uint32_t M, N, K, lda, ldc;
-  uint32_t c_wide;       // every 4 columns of C start on an 8-byte boundary
+  uint32_t M, N, K, lda;
+  MxOut out;
 };
 
 // Enqueue a product (gated: silu of the first times the second) on the kernel

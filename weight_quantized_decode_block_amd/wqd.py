@@ -187,18 +187,18 @@ def _span(rows: int, pitch: int, width: int, size: int) -> int:
 
 def _arg(fn: str, name: str, x, nbytes: int) -> int | None:
     """Device address of an operand.  A tensor must live on the current device
-    (its stream is the one the call goes to), with rows packed as the call says
-    (the last dimension contiguous), and reach `nbytes` from its first element;
-    an integer is taken as it is."""
+    (its stream is the one the call goes to), with its last dimension contiguous,
+    and its memory must reach `nbytes` past its first element; an integer is
+    taken as it is."""
     if x is None or isinstance(x, int):
         return x
-    device = x.get_device()
-    if device < 0 or device != _current_device():
+    if x.get_device() != _current_device():
         raise ValueError(f"{fn}: {name} is not on the current GPU")
-    if x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
-        raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
-    if x.untyped_storage().nbytes() - x.storage_offset() * x.element_size() < nbytes:
-        raise ValueError(f"{fn}: {name} holds fewer than the {nbytes} bytes the call reaches")
+    if x.nbytes < nbytes or not x.is_contiguous():  # perhaps rows of a wider buffer
+        if x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
+            raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
+        if x.untyped_storage().nbytes() - x.storage_offset() * x.element_size() < nbytes:
+            raise ValueError(f"{fn}: {name} holds fewer than the {nbytes} bytes the call reaches")
     return x.data_ptr()
 
 
@@ -206,10 +206,11 @@ _current_device_raw = None
 
 
 def _current_device() -> int:
+    """Index of torch's current GPU, or -2 (no tensor's) where there is none."""
     global _current_device_raw
     if _current_device_raw is None:
         import torch
-        _current_device_raw = torch.cuda.current_device
+        _current_device_raw = torch._C._cuda_getDevice if torch.cuda.is_available() else lambda: -2
     return _current_device_raw()
 
 
