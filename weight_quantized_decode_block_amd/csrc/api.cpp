@@ -182,8 +182,7 @@ int run_mx_product(const char *fn, wqd::MxOperands op, wqd::MxFormat fmt, bool g
   if (int rc = check_device(fn)) return rc;
   op.out.wide = aligned(op.out.C, 8) && op.out.ldc % 4u == 0;
   (void)hipGetLastError();
-  const bool tile = op.M > 64u && wqd::mx_tile_supports(op);
-  return check_launch(fn, tile ? wqd::launch_mx_tile(op, fmt, gated, stream) : wqd::launch_mx_skinny(op, fmt, gated, stream));
+  return check_launch(fn, wqd::launch_mx_product(op, fmt, gated, stream));
 }
 
 wqd::MxOperands mx_operands(const void *A, const void *AS, const void *W, const void *WS, const void *WU,

@@ -15,26 +15,31 @@ struct ActRegs {
   uint32_t s;
 };
 
-// One lane's 32 weights of a step: BF16 (converted and scaled) or as stored.
-template <MxFormat FMT>
+// One lane's 32 weights of a step as they are stored.
+struct WeightCodes {
+  u32x4_t v;
+  uint32_t s;  // scale byte, in the byte of the register that the product is told
+};
+
+// The same as the matrix instructions take them: BF16 (converted and scaled) or as stored.
+template <MxFormat FMT, int B = 0>
 struct WeightRegs {
   u32x4_t v[FMT == MxFormat::kBf16 ? 4 : 1];
   uint32_t s;
-  WeightRegs() = default;
-  __device__ __forceinline__ WeightRegs(const u32x4_t &codes, uint32_t scale) {
+  __device__ __forceinline__ explicit WeightRegs(const WeightCodes &c) {
     if constexpr (FMT == MxFormat::kBf16) {
-      const float f = e8m0_value(scale);
+      const float f = e8m0_value(B == 0 ? c.s & 255u : c.s >> (8 * B) & 255u);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        v[j].x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j], f, 0));
-        v[j].y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j], f, 1));
-        v[j].z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j], f, 2));
-        v[j].w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j], f, 3));
+        v[j].x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c.v[j], f, 0));
+        v[j].y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c.v[j], f, 1));
+        v[j].z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c.v[j], f, 2));
+        v[j].w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c.v[j], f, 3));
       }
       s = 0;
     } else {
-      v[0] = codes;
-      s = scale;
+      v[0] = c.v;
+      s = c.s;
     }
   }
 };
@@ -43,7 +48,7 @@ struct WeightRegs {
 // n = 4 (l / 16) + i in element i and m = l % 16.  B: the byte of the scale
 // registers to use.
 template <MxFormat FMT, int B = 0>
-__device__ __forceinline__ f32x4_t mx_mfma(const WeightRegs<FMT> &w, const ActRegs<FMT> &a, f32x4_t acc) {
+__device__ __forceinline__ f32x4_t mx_mfma(const WeightRegs<FMT, B> &w, const ActRegs<FMT> &a, f32x4_t acc) {
   if constexpr (FMT == MxFormat::kBf16) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -76,6 +81,17 @@ inline MxOperands mx_rows(const MxOperands &op, MxFormat fmt, uint32_t m, uint32
   part.M = op.M - m < rows ? op.M - m : rows;
   return part;
 }
+
+// A unit of 16 rows x 64 bytes in LDS: piece p (16 bytes) of row r lies in slot
+// p ^ unit_turn(r) of the row.  A 16-byte LDS read serves lanes 0-3, 12-15,
+// 20-23 and 24-27 together (then 4-11, 16-19, 28-31; then the same of the upper
+// half): with 0, 2, 3, 1 for the four quarters of the rows, the lanes (r, g) that
+// read piece g of row r meet all 64 banks in each such set, and so do those that
+// read one piece of 16 rows.  With r / 4 itself every read took half as long again.
+__device__ __forceinline__ uint32_t unit_turn(uint32_t r) { return ((r >> 2 & 1u) << 1) ^ (r >> 3 & 1u) * 3u; }
+
+// Byte offset in a unit of piece p of row r
+__device__ __forceinline__ uint32_t unit_byte(uint32_t r, uint32_t p) { return r * 64u + (p ^ unit_turn(r)) * 16u; }
 
 // Bytes of n activation values
 template <MxFormat FMT>

@@ -159,15 +159,16 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const uint8_t *__res
     for (int j = 0; j < MT; ++j) acc[t][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   auto compute = [&](const WSeg &x, uint32_t buf) __attribute__((always_inline)) {
     const uint8_t *p0 = lds + buf * kBuffer, *ps = p0 + kARegion + wave * 4u + g;
-    // piece p of row r goes to slot p ^ (r / 4): the 16 lanes that read one piece meet all banks
     uint8_t *turn = lds + kTurn + wave * (WT * 1024u);
 #pragma unroll
     for (int t = 0; t < WT; ++t)
-      *reinterpret_cast<u32x4_t *>(turn + t * 1024 + (lane >> 2) * 64u + ((lane & 3u) ^ (lane >> 4)) * 16u) = x.v[t];
-    WeightRegs<FMT> w[WT];
+      *reinterpret_cast<u32x4_t *>(turn + t * 1024 + unit_byte(lane >> 2, lane & 3u)) = x.v[t];
+    WeightCodes w[WT];
 #pragma unroll
-    for (int t = 0; t < WT; ++t)
-      w[t] = WeightRegs<FMT>(*reinterpret_cast<const u32x4_t *>(turn + t * 1024 + r * 64u + (g ^ (r >> 2)) * 16u), ps[(t * 16u + r) * kScaleBytes]);
+    for (int t = 0; t < WT; ++t) {
+      w[t].v = *reinterpret_cast<const u32x4_t *>(turn + t * 1024 + unit_byte(r, g));
+      w[t].s = ps[(t * 16u + r) * kScaleBytes];
+    }
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       // rows past the last staged one repeat row MMAX - 1: their outputs are not stored
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const uint8_t *__res
         a.s = ps[(kWsRows + m) * kScaleBytes];
       }
 #pragma unroll
-      for (int t = 0; t < WT; ++t) acc[t][j] = mx_mfma<FMT>(w[t], a, acc[t][j]);
+      for (int t = 0; t < WT; ++t) acc[t][j] = mx_mfma<FMT>(WeightRegs<FMT>(w[t]), a, acc[t][j]);
     }
   };
 

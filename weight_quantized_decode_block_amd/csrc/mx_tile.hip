@@ -13,8 +13,7 @@
 //     neighbouring lanes bring the four 16-byte pieces of a row: with the lanes
 //     in a matrix operand's own order (neighbours in different rows) the same
 //     transfers run at a quarter of the rate (37 instead of 120 to 146 GB/s per
-//     compute unit from L2).  Piece p of row r lies in slot p ^ (r / 4) of the
-//     row, so the 16 lanes that read one piece of 16 rows meet all 64 banks.
+//     compute unit from L2).
 //     Rows past the matrix repeat its last row; their outputs are not stored.
 //   * Scales.  16 bytes per row cover four steps; they are staged the same way
 //     one group of four steps ahead.  A wave reads them once per group and
@@ -28,6 +27,8 @@
 //     that share an L2 at one time share rows of both operands.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "mx_common.h"
 #include "mx_product.h"
@@ -79,12 +80,14 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   constexpr int NBUF = PRE + 1;
   constexpr uint32_t kWUnits = BN / 16, kAUnits = BM / 16 * kActUnits<FMT>;
   constexpr uint32_t kStep = (kWUnits + kAUnits) * kUnit, kStage = KS * kStep;
-  static_assert(kWUnits % kGroupWaves == 0, "a wave's weight units are all of one matrix");
-  constexpr int WU = kWUnits / kGroupWaves, AU = (kAUnits + kGroupWaves - 1) / kGroupWaves, ND = WU + AU;
+  static_assert(!GATED || (kWUnits % 2 == 0 && kGroupWaves % 2 == 0 && NT % 2 == 0), "units of the two matrices alternate");
+  constexpr int WU = (kWUnits + kGroupWaves - 1) / kGroupWaves, AU = (kAUnits + kGroupWaves - 1) / kGroupWaves, ND = WU + AU;
   constexpr bool kActScales = FMT != MxFormat::kBf16;
-  constexpr uint32_t kScaleRows = BN + (kActScales ? (BM + 63) / 64 * 64 : 0);  // whole transfers of 64 rows
+  // scale rows in LDS: the weights' (gated: of either matrix), then the activations', whole transfers of 64 rows
+  constexpr uint32_t kMatRows = (BN / (GATED ? 2 : 1) + 63) / 64 * 64, kWsRows = kMatRows * (GATED ? 2 : 1);
+  constexpr uint32_t kScaleRows = kWsRows + (kActScales ? (BM + 63) / 64 * 64 : 0);
   constexpr uint32_t kScaleStage = kScaleRows * 16;
-  static_assert(BN % 64 == 0 && kScaleRows <= 64 * kWaves, "at most one scale transfer per wave");
+  static_assert(kScaleRows <= 64 * kWaves, "at most one scale transfer per wave");
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // NBUF stages, two scale stages
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
 
@@ -110,17 +113,17 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
 
   // transfers of this wave for its group's step: weight units wave, wave +
   // kGroupWaves, ... and activation units likewise (where they do not come out
-  // even, some are brought twice: every wave then has as many transfers in
-  // flight as the waits count).  Gated: even units are the gate matrix, odd ones
+  // even, some are brought twice, the same bytes to the same place: every wave
+  // then has as many transfers in flight as the waits count).  Gated: even units are the gate matrix, odd ones
   // the up matrix.
   const bool up = GATED && (wave & 1u);
   const rsrc_t wr = bytes_rsrc(up ? op.WU : op.W, (uint64_t)n0 * wpitch, (nlast + 1u) * wpitch);
   const rsrc_t ar = bytes_rsrc(op.A, (uint64_t)m0 * apitch, mlast * apitch + act_bytes<FMT>(op.K));
-  const uint32_t lrow = lane >> 2, lpiece = ((lane & 3u) ^ (lane >> 4)) * 16u;  // this lane's row and piece of a unit
+  const uint32_t lrow = lane >> 2, lpiece = ((lane & 3u) ^ unit_turn(lrow)) * 16u;  // this lane's row and piece of a unit
   uint32_t woff[WU], aoff[AU];
 #pragma unroll
   for (int i = 0; i < WU; ++i) {
-    const uint32_t u = wave + kGroupWaves * i;
+    const uint32_t u = (wave + kGroupWaves * i) % kWUnits;
     const uint32_t row = (GATED ? u >> 1 : u) * 16u + lrow;
     woff[i] = (row < nlast ? row : nlast) * wpitch + lpiece;
   }
@@ -132,11 +135,11 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   }
   // scale rows 64 w .. 64 w + 63 of wave w: weights (gated: gate, then up), then activations
   const uint32_t srow = all_wave * 64u + lane;
-  const bool s_act = all_wave * 64u >= (uint32_t)BN, s_up = GATED && !s_act && all_wave * 64u >= BNO;
+  const bool s_act = all_wave * 64u >= kWsRows, s_up = GATED && !s_act && all_wave * 64u >= kMatRows;
   const bool s_any = all_wave * 64u < kScaleRows;
   const rsrc_t sr = s_act ? bytes_rsrc(op.AS, (uint64_t)m0 * nb, (mlast + 1u) * nb)
                           : bytes_rsrc(s_up ? op.WUS : op.WS, (uint64_t)n0 * nb, (nlast + 1u) * nb);
-  const uint32_t s_in = s_act ? srow - BN : (s_up ? srow - BNO : srow);
+  const uint32_t s_in = s_act ? srow - kWsRows : (s_up ? srow - kMatRows : srow);
   const uint32_t s_last = s_act ? mlast : nlast;
   const uint32_t soff = (s_in < s_last ? s_in : s_last) * nb;
 
@@ -145,7 +148,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
     if (KS > 1) s = s < steps ? s : steps - 1u;  // a step too many is brought but not computed
     const uint32_t base = lds0 + buf * kStage + ks * kStep;
 #pragma unroll
-    for (int i = 0; i < WU; ++i) copy_to_lds(base + (wave + i * kGroupWaves) * kUnit, wr, woff[i] + s * 64u);
+    for (int i = 0; i < WU; ++i) copy_to_lds(base + (wave + i * kGroupWaves) % kWUnits * kUnit, wr, woff[i] + s * 64u);
 #pragma unroll
     for (int i = 0; i < AU; ++i)
       copy_to_lds(base + (kWUnits + (wave + kGroupWaves * i) % kAUnits) * kUnit, ar, aoff[i] + s * 64u * kActUnits<FMT>);
@@ -177,25 +180,22 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const uint32_t t = wn * NT + i;
-      const uint32_t row = (GATED ? (t & 1u) * BNO + (t >> 1) * 16u : t * 16u) + r;
+      const uint32_t row = (GATED ? (t & 1u) * kMatRows + (t >> 1) * 16u : t * 16u) + r;
       wsc[i] = turn(*reinterpret_cast<const u32x4_t *>(p + row * 16u), shift);
     }
     if constexpr (kActScales) {
 #pragma unroll
       for (int j = 0; j < MT; ++j)
-        asc[j] = turn(*reinterpret_cast<const u32x4_t *>(p + (BN + (wm * MT + j) * 16u + r) * 16u), shift);
+        asc[j] = turn(*reinterpret_cast<const u32x4_t *>(p + (kWsRows + (wm * MT + j) * 16u + r) * 16u), shift);
     }
   };
 
-  // operands of a step from LDS, and the products on them; T: the scales' byte
-  const uint32_t mine = r * 64u + (g ^ (r >> 2)) * 16u;  // piece g of row r of a unit
-  auto read_w = [&](uint32_t buf, auto T, WeightRegs<FMT> (&w)[NT]) __attribute__((always_inline)) {
-    constexpr int t = decltype(T)::value;
+  // operands of a step from LDS
+  const uint32_t mine = unit_byte(r, g);  // piece g of row r of a unit
+  auto read_w = [&](uint32_t buf, WeightCodes (&w)[NT]) __attribute__((always_inline)) {
     const uint8_t *p = lds + buf * kStage + ks * kStep + wn * NT * kUnit + mine;
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-      w[i] = WeightRegs<FMT>(*reinterpret_cast<const u32x4_t *>(p + i * kUnit),
-                             kActScales ? wsc[i] : (wsc[i] >> (8 * t)) & 255u);
+    for (int i = 0; i < NT; ++i) w[i] = {*reinterpret_cast<const u32x4_t *>(p + i * kUnit), wsc[i]};
   };
   auto read_a = [&](uint32_t buf, int j) __attribute__((always_inline)) {
     const uint8_t *p = lds + buf * kStage + ks * kStep + (kWUnits + wm * MT * kActUnits<FMT>) * kUnit;
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
     if constexpr (FMT == MxFormat::kBf16) {
 #pragma unroll
       for (uint32_t h = 0; h < 4; ++h)  // k 32g .. 32g + 31 are the four pieces of unit g
-        a.v[h] = *reinterpret_cast<const u32x4_t *>(p + (j * 4 + g) * kUnit + r * 64u + (h ^ (r >> 2)) * 16u);
+        a.v[h] = *reinterpret_cast<const u32x4_t *>(p + (j * 4 + g) * kUnit + unit_byte(r, h));
     } else {
 #pragma unroll
       for (uint32_t h = 0; h < kActUnits<FMT>; ++h)
@@ -237,9 +237,9 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
             read_scales(s0 / kGroup);
             __builtin_amdgcn_sched_barrier(0);  // their registers are free again before the operands' are taken
           }
-          WeightRegs<FMT> w[NT];
+          WeightCodes w[NT];
           ActRegs<FMT> a[MT];
-          read_w(buf, T, w);
+          read_w(buf, w);
 #pragma unroll
           for (int j = 0; j < MT; ++j) a[j] = read_a(buf, j);
           if constexpr (t == 0) {
@@ -254,9 +254,11 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
           __builtin_amdgcn_sched_barrier(0);
           __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-          for (int j = 0; j < MT; ++j)
+          for (int i = 0; i < NT; ++i) {
+            const WeightRegs<FMT, t> x(w[i]);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) acc[i][j] = mx_mfma<FMT, t>(w[i], a[j], acc[i][j]);
+            for (int j = 0; j < MT; ++j) acc[i][j] = mx_mfma<FMT, t>(x, a[j], acc[i][j]);
+          }
           __builtin_amdgcn_s_setprio(0);
           __builtin_amdgcn_sched_barrier(0);
           __builtin_amdgcn_s_barrier();
@@ -283,13 +285,13 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
           }
           if (s + PRE < stages) issue(s + PRE, buf == 0 ? NBUF - 1 : buf - 1);
           if (KS == 1 || s * KS + ks < steps) {
-            WeightRegs<FMT> w[NT];
-            read_w(buf, std::integral_constant<int, t * KS>{}, w);
+            WeightCodes w[NT];
+            read_w(buf, w);
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
               const ActRegs<FMT> a = read_a(buf, j);
 #pragma unroll
-              for (int i = 0; i < NT; ++i) acc[i][j] = mx_mfma<FMT, t * KS>(w[i], a, acc[i][j]);
+              for (int i = 0; i < NT; ++i) acc[i][j] = mx_mfma<FMT, t * KS>(WeightRegs<FMT, t * KS>(w[i]), a, acc[i][j]);
             }
           }
           buf = buf + 1u == (uint32_t)NBUF ? 0u : buf + 1u;
@@ -346,7 +348,8 @@ template <MxFormat FMT, int BM, int BN, int WM, int WN, int KS, int PRE, bool PP
 hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
   constexpr auto kern = mx_tile_kernel<FMT, BM, BN, WM, WN, KS, PRE, PP, GATED>;
   constexpr uint32_t kLds = (PRE + 1) * KS * (BN / 16 + BM / 16 * kActUnits<FMT>) * kUnit +
-                            2 * (BN + (FMT == MxFormat::kBf16 ? 0 : (BM + 63) / 64 * 64)) * 16;
+                            2 * ((BN / (GATED ? 2 : 1) + 63) / 64 * 64 * (GATED ? 2 : 1) +
+                                 (FMT == MxFormat::kBf16 ? 0 : (BM + 63) / 64 * 64)) * 16;
   static_assert(kLds <= 160 * 1024, "one workgroup's LDS");
   static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
@@ -364,28 +367,134 @@ hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
   return hipSuccess;
 }
 
+// What a configuration takes per 128-k step, in ns: the first round of tiles
+// over the compute units, and every further one; `share` workgroups fit one
+// compute unit, so a further round comes in that many parts.  Measured at
+// K = 5120 with 256, 512 and 1024 tiles (MI355X, weights from memory).
+struct Cost {
+  uint32_t bm, bn;  // outputs of a tile
+  uint32_t first, more, share;
+};
+
+// The kernel for few rows works in tiles of 32 x 32 (gated: 16) and splits K
+// eight ways, so it is ahead while its tiles do not fill the chip: 400 x 512
+// outputs, K = 5120, MXFP8 7.7 us against 10.8 with 64 x 64 tiles, 1000 x 512
+// 14.5 against 11.1.  Larger tiles cost less per output (MXFP8: 64 x 64 51 ns
+// per 1000 outputs and step, 128 x 128 29, 256 x 256 24) and lose by rounds
+// that they do not fill: 4096 x 5120, MXFP4, is 320 tiles of 256 x 256 (two
+// rounds, 94 us) and 512 of 256 x 160 (two rounds, 78 us); 1000 x 5120,
+// K = 17408, MXFP8 one round of 128 x 160 (98 us) or of 80 tiles of 256 x 256
+// (160 us).  So the configuration of the least estimated time is taken.
 template <MxFormat FMT, bool GATED>
-hipError_t launch_fmt(const MxOperands &op, hipStream_t stream) {
-  if constexpr (FMT == MxFormat::kBf16)
-    return launch_cfg<FMT, 128, 256, 2, 4, 1, 2, true, GATED>(op, stream);
-  else if constexpr (FMT == MxFormat::kFp8)
+struct Costs;
+template <>
+struct Costs<MxFormat::kBf16, false> {
+  static constexpr Cost v[] = {{32, 32, 258, 240, 1},   {64, 64, 461, 420, 1},    {96, 256, 1364, 1310, 1},
+                               {128, 192, 1435, 1350, 1}, {128, 256, 1777, 1620, 1}};
+};
+template <>
+struct Costs<MxFormat::kBf16, true> {
+  static constexpr Cost v[] = {{32, 16, 258, 240, 1}, {64, 64, 638, 610, 1}, {96, 128, 1364, 1310, 1}, {128, 128, 1777, 1620, 1}};
+};
+template <>
+struct Costs<MxFormat::kFp8, false> {
+  static constexpr Cost v[] = {{32, 32, 175, 160, 1},   {64, 64, 260, 210, 2},     {128, 128, 649, 470, 2},
+                               {128, 160, 779, 690, 1}, {256, 160, 1191, 1100, 1}, {256, 224, 1509, 1430, 1},
+                               {256, 256, 1685, 1590, 1}};
+};
+template <>
+struct Costs<MxFormat::kFp8, true> {
+  static constexpr Cost v[] = {{32, 16, 175, 160, 1},  {64, 64, 430, 400, 1},    {128, 64, 649, 470, 2},
+                               {256, 96, 1398, 1260, 1}, {256, 128, 1685, 1590, 1}};
+};
+template <>
+struct Costs<MxFormat::kFp4, false> {
+  static constexpr Cost v[] = {{32, 32, 140, 115, 1},   {64, 64, 206, 172, 2},    {128, 128, 569, 435, 2},
+                               {128, 160, 663, 545, 1}, {256, 160, 1022, 948, 1}, {256, 224, 1240, 1180, 1},
+                               {256, 256, 1328, 1290, 1}};
+};
+template <>
+struct Costs<MxFormat::kFp4, true> {
+  static constexpr Cost v[] = {{32, 16, 140, 115, 1},  {64, 64, 331, 285, 2},    {128, 64, 569, 435, 2},
+                               {256, 96, 1110, 1057, 1}, {256, 128, 1328, 1290, 1}};
+};
+
+uint64_t cost_of(const Cost &c, const MxOperands &op, uint32_t cus) {
+  const uint64_t tiles = (uint64_t)((op.M + c.bm - 1u) / c.bm) * ((op.N + c.bn - 1u) / c.bn);
+  const uint64_t parts = (tiles * c.share + cus - 1u) / cus;  // of a round
+  return c.first + (parts > c.share ? (parts - c.share) * c.more / c.share : 0u);
+}
+
+// The index of the least cost; 0, the kernel for few rows, up to 32 rows (its
+// own row tiles) and for K below the four steps that scales are staged in.
+template <MxFormat FMT, bool GATED>
+uint32_t pick(const MxOperands &op, uint32_t cus) {
+  using C = Costs<FMT, GATED>;
+  if (op.M <= 32u || op.K < 512u) return 0u;
+  uint32_t best = 0;
+  for (uint32_t i = 1; i < sizeof(C::v) / sizeof(Cost); ++i)
+    if (cost_of(C::v[i], op, cus) < cost_of(C::v[best], op, cus)) best = i;
+  return best;
+}
+
+template <MxFormat FMT, bool GATED>
+hipError_t launch_fmt(const MxOperands &op, uint32_t cus, hipStream_t stream) {
+  const uint32_t i = pick<FMT, GATED>(op, cus);
+  if (i == 0u) return launch_mx_skinny(op, FMT, GATED, stream);
+  if constexpr (FMT == MxFormat::kBf16 && GATED) {
+    if (i == 1u) return launch_cfg<FMT, 64, 128, 1, 4, 2, 1, false, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, true, GATED>(op, stream);
+    return launch_cfg<FMT, 128, 256, 1, 8, 1, 2, true, GATED>(op, stream);
+  } else if constexpr (FMT == MxFormat::kBf16) {
+    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, false, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, true, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 128, 192, 2, 4, 1, 2, true, GATED>(op, stream);
+    return launch_cfg<FMT, 128, 256, 1, 8, 1, 2, true, GATED>(op, stream);
+  } else if constexpr (GATED) {
+    if (i == 1u) return launch_cfg<FMT, 64, 128, 2, 2, 2, 2, false, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, true, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 256, 192, 4, 2, 1, 2, true, GATED>(op, stream);
     return launch_cfg<FMT, 256, 256, 4, 2, 1, 2, true, GATED>(op, stream);
-  else
-    return launch_cfg<FMT, 256, 256, 4, 2, 1, 3, true, GATED>(op, stream);
+  } else {
+    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, false, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, true, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 128, 160, 4, 2, 1, 2, true, GATED>(op, stream);
+    if (i == 4u) return launch_cfg<FMT, 256, 160, 4, 2, 1, 2, true, GATED>(op, stream);
+    if (i == 5u) return launch_cfg<FMT, 256, 224, 4, 2, 1, 2, true, GATED>(op, stream);
+    return launch_cfg<FMT, 256, 256, 4, 2, 1, 2, true, GATED>(op, stream);
+  }
+}
+
+// Compute units of the current device, asked for once per device.
+hipError_t compute_units(uint32_t &cus) {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  if (dev < 64) n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess) return e;
+    n = n > 0 ? n : 1;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  cus = (uint32_t)n;
+  return hipSuccess;
 }
 
 }  // namespace
 
-bool mx_tile_supports(const MxOperands &op) { return op.K >= 512u; }
-
-hipError_t launch_mx_tile(const MxOperands &op, MxFormat fmt, bool gated, hipStream_t stream) {
+hipError_t launch_mx_product(const MxOperands &op, MxFormat fmt, bool gated, hipStream_t stream) {
+  uint32_t cus = 1;
+  const hipError_t e = compute_units(cus);
+  if (e != hipSuccess) return e;
   switch (fmt) {
     case MxFormat::kBf16:
-      return gated ? launch_fmt<MxFormat::kBf16, true>(op, stream) : launch_fmt<MxFormat::kBf16, false>(op, stream);
+      return gated ? launch_fmt<MxFormat::kBf16, true>(op, cus, stream) : launch_fmt<MxFormat::kBf16, false>(op, cus, stream);
     case MxFormat::kFp8:
-      return gated ? launch_fmt<MxFormat::kFp8, true>(op, stream) : launch_fmt<MxFormat::kFp8, false>(op, stream);
+      return gated ? launch_fmt<MxFormat::kFp8, true>(op, cus, stream) : launch_fmt<MxFormat::kFp8, false>(op, cus, stream);
     default:
-      return gated ? launch_fmt<MxFormat::kFp4, true>(op, stream) : launch_fmt<MxFormat::kFp4, false>(op, stream);
+      return gated ? launch_fmt<MxFormat::kFp4, true>(op, cus, stream) : launch_fmt<MxFormat::kFp4, false>(op, cus, stream);
   }
 }
 

@@ -83,13 +83,11 @@ struct MxOperands {
   MxOut out;
 };
 
-// Enqueue a product (gated: silu of the first times the second) on the kernel
-// for few rows, which takes any M.
+// Enqueue a product (gated: silu of the first times the second); the kernel is
+// chosen by sizes and format (mx_tile.hip).  launch_mx_skinny is the one for
+// few rows, which takes any size.
+hipError_t launch_mx_product(const MxOperands &op, MxFormat fmt, bool gated, hipStream_t stream);
 hipError_t launch_mx_skinny(const MxOperands &op, MxFormat fmt, bool gated, hipStream_t stream);
-
-// The same on the kernel for many rows, for K of at least 512.
-bool mx_tile_supports(const MxOperands &op);
-hipError_t launch_mx_tile(const MxOperands &op, MxFormat fmt, bool gated, hipStream_t stream);
 
 // Enqueue quantisation of M rows to MXFP4 or MXFP8, its inverse, and the
 // residual addition with a root-mean-square norm (R and H, and Y, may be
