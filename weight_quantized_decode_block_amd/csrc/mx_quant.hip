@@ -232,7 +232,9 @@ hipError_t dequantize_as(const void *Q, const void *S, void *Y, uint32_t M, uint
 // registers between the sum of squares and the scaling, so the row is read
 // once.  h is rounded to BF16 before the sum: the norm is that of the residual
 // stream as the next layer reads it.  The sum and the quotient are held in 64
-// bits: the squares of BF16 values leave fp32's range at either end.
+// bits: the squares of BF16 values leave fp32's range at either end, and in 32
+// bits the kernel is no faster (4096 x 5120 31.3 against 30.5 us), as memory
+// bounds it (147 MB, 4.8 TB/s).
 constexpr uint32_t kNormMaxThreads = 1024;
 
 __device__ __forceinline__ double wave_sum(double x) {
@@ -340,8 +342,11 @@ hipError_t launch_mx_dequantize(const void *Q, const void *S, bool fp4, void *Y,
 
 hipError_t launch_add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *Y, void *Q, void *S,
                                   uint32_t M, uint32_t K, uint32_t ldx, uint32_t ldr, float eps, hipStream_t stream) {
+  // Few rows want one group per thread (one row of 5120 3.2 us, with two 3.4;
+  // 256 rows 4.0, 4.3); from 1024 rows on two keep more loads in flight (1024
+  // rows 9.7 -> 9.2 us, 8192 rows 58 -> 54, without a residual 4096 22 -> 17).
   const uint32_t gpr = K >> 3;
-  if (gpr <= kNormMaxThreads) return norm_as<1>(X, R, G, H, Y, Q, S, M, K, ldx, ldr, eps, stream);
+  if (gpr <= kNormMaxThreads && M < 1024u) return norm_as<1>(X, R, G, H, Y, Q, S, M, K, ldx, ldr, eps, stream);
   if (gpr <= 2 * kNormMaxThreads) return norm_as<2>(X, R, G, H, Y, Q, S, M, K, ldx, ldr, eps, stream);
   return norm_as<4>(X, R, G, H, Y, Q, S, M, K, ldx, ldr, eps, stream);
 }

@@ -405,7 +405,7 @@ struct Costs<MxFormat::kFp8, false> {
 template <>
 struct Costs<MxFormat::kFp8, true> {
   static constexpr Cost v[] = {{32, 16, 175, 160, 1},  {64, 64, 430, 400, 1},    {128, 64, 649, 470, 2},
-                               {256, 96, 1398, 1260, 1}, {256, 128, 1685, 1590, 1}};
+                               {192, 128, 1373, 1250, 1}, {256, 128, 1685, 1590, 1}};
 };
 template <>
 struct Costs<MxFormat::kFp4, false> {
@@ -416,7 +416,7 @@ struct Costs<MxFormat::kFp4, false> {
 template <>
 struct Costs<MxFormat::kFp4, true> {
   static constexpr Cost v[] = {{32, 16, 140, 115, 1},  {64, 64, 331, 285, 2},    {128, 64, 569, 435, 2},
-                               {256, 96, 1110, 1057, 1}, {256, 128, 1328, 1290, 1}};
+                               {192, 128, 1143, 1080, 1}, {256, 128, 1328, 1290, 1}};
 };
 
 uint64_t cost_of(const Cost &c, const MxOperands &op, uint32_t cus) {
@@ -453,7 +453,7 @@ hipError_t launch_fmt(const MxOperands &op, uint32_t cus, hipStream_t stream) {
   } else if constexpr (GATED) {
     if (i == 1u) return launch_cfg<FMT, 64, 128, 2, 2, 2, 2, false, GATED>(op, stream);
     if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, true, GATED>(op, stream);
-    if (i == 3u) return launch_cfg<FMT, 256, 192, 4, 2, 1, 2, true, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 192, 256, 4, 2, 1, 2, true, GATED>(op, stream);
     return launch_cfg<FMT, 256, 256, 4, 2, 1, 2, true, GATED>(op, stream);
   } else {
     if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, false, GATED>(op, stream);

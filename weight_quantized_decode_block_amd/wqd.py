@@ -185,14 +185,14 @@ def _span(rows: int, pitch: int, width: int, size: int) -> int:
     return ((rows - 1) * pitch + width) * size if rows > 0 else 0
 
 
-def _arg(fn: str, name: str, x, nbytes: int) -> int | None:
-    """Device address of an operand.  A tensor must live on the current device
-    (its stream is the one the call goes to), with its last dimension contiguous,
-    and its memory must reach `nbytes` past its first element; an integer is
-    taken as it is."""
+def _arg(fn: str, name: str, x, nbytes: int, device: int) -> int | None:
+    """Device address of an operand.  A tensor must live on `device`, the current
+    one (the call goes to its stream), with its last dimension contiguous, and
+    its memory must reach `nbytes` past its first element; an integer is taken as
+    it is."""
     if x is None or isinstance(x, int):
         return x
-    if x.get_device() != _current_device():
+    if x.get_device() != device:
         raise ValueError(f"{fn}: {name} is not on the current GPU")
     if x.nbytes < nbytes or not x.is_contiguous():  # perhaps rows of a wider buffer
         if x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
@@ -202,16 +202,23 @@ def _arg(fn: str, name: str, x, nbytes: int) -> int | None:
     return x.data_ptr()
 
 
-_current_device_raw = None
+_no_gpu = -2  # no tensor's device
+_raw_device = _raw_stream = None
 
 
-def _current_device() -> int:
-    """Index of torch's current GPU, or -2 (no tensor's) where there is none."""
-    global _current_device_raw
-    if _current_device_raw is None:
+def _here(stream) -> tuple[int, int | None]:
+    """Index of torch's current GPU and the stream of a call: `stream`, or the
+    current one of that GPU."""
+    global _raw_device, _raw_stream
+    if _raw_device is None:
         import torch
-        _current_device_raw = torch._C._cuda_getDevice if torch.cuda.is_available() else lambda: -2
-    return _current_device_raw()
+        gpu = torch.cuda.is_available()
+        if gpu:
+            torch.cuda.init()
+        _raw_device = torch._C._cuda_getDevice if gpu else lambda: _no_gpu
+        _raw_stream = torch._C._cuda_getCurrentRawStream if gpu else lambda device: None
+    device = _raw_device()
+    return device, (_raw_stream(device) if stream is None else _stream(stream))
 
 
 def _type_of(fn: str, x, given: int | None) -> int:
@@ -246,9 +253,10 @@ def mx_quantize(X, Q, S, fmt, M: int, K: int, x_row_stride: int | None = None, x
     fn, ld = "mx_quantize", K if x_row_stride is None else x_row_stride
     _sizes(fn, M | K | ld)
     f, t = _mx_format(fn, fmt), _type_of(fn, X, x_type)
-    _check(fn, lib().mx_quantize(_arg(fn, "X", X, _span(M, ld, K, 4 if t == TYPE_FP32 else 2)), t,
-                                 _arg(fn, "Q", Q, _code_bytes(f, M * K)), _arg(fn, "S", S, M * K // 32), f, M, K, ld,
-                                 _stream(stream)))
+    d, st = _here(stream)
+    _check(fn, (_lib or lib()).mx_quantize(_arg(fn, "X", X, _span(M, ld, K, 4 if t == TYPE_FP32 else 2), d), t,
+                                           _arg(fn, "Q", Q, _code_bytes(f, M * K), d),
+                                           _arg(fn, "S", S, M * K // 32, d), f, M, K, ld, st))
 
 
 def mx_dequantize(Q, S, Y, fmt, M: int, K: int, y_row_stride: int | None = None, y_type: int | None = None,
@@ -257,9 +265,11 @@ def mx_dequantize(Q, S, Y, fmt, M: int, K: int, y_row_stride: int | None = None,
     fn, ld = "mx_dequantize", K if y_row_stride is None else y_row_stride
     _sizes(fn, M | K | ld)
     f, t = _mx_format(fn, fmt), _type_of(fn, Y, y_type)
-    _check(fn, lib().mx_dequantize(_arg(fn, "Q", Q, _code_bytes(f, M * K)), _arg(fn, "S", S, M * K // 32), f,
-                                   _arg(fn, "Y", Y, _span(M, ld, K, 4 if t == TYPE_FP32 else 2)), t, M, K, ld,
-                                   _stream(stream)))
+    d, st = _here(stream)
+    _check(fn, (_lib or lib()).mx_dequantize(_arg(fn, "Q", Q, _code_bytes(f, M * K), d),
+                                             _arg(fn, "S", S, M * K // 32, d), f,
+                                             _arg(fn, "Y", Y, _span(M, ld, K, 4 if t == TYPE_FP32 else 2), d), t,
+                                             M, K, ld, st))
 
 
 def add_rmsnorm_mx8(X, R, G, H, Y, Q, S, M: int, K: int, eps: float, x_row_stride: int | None = None,
@@ -270,54 +280,73 @@ def add_rmsnorm_mx8(X, R, G, H, Y, Q, S, M: int, K: int, eps: float, x_row_strid
     lx, lr = K if x_row_stride is None else x_row_stride, K if r_row_stride is None else r_row_stride
     _sizes(fn, M | K | lx | lr)
     rows = _span(M, lr, K, 2)
-    _check(fn, lib().add_rmsnorm_mx8(_arg(fn, "X", X, _span(M, lx, K, 2)), _arg(fn, "R", R, rows),
-                                     _arg(fn, "G", G, 2 * K), _arg(fn, "H", H, rows), _arg(fn, "Y", Y, 2 * M * K),
-                                     _arg(fn, "Q", Q, M * K), _arg(fn, "S", S, M * K // 32), M, K, lx, lr, eps,
-                                     _stream(stream)))
+    d, st = _here(stream)
+    _check(fn, (_lib or lib()).add_rmsnorm_mx8(_arg(fn, "X", X, _span(M, lx, K, 2), d), _arg(fn, "R", R, rows, d),
+                                               _arg(fn, "G", G, 2 * K, d), _arg(fn, "H", H, rows, d),
+                                               _arg(fn, "Y", Y, 2 * M * K, d), _arg(fn, "Q", Q, M * K, d),
+                                               _arg(fn, "S", S, M * K // 32, d), M, K, lx, lr, eps, st))
 
 
-def _a16(fn: str, M: int, N: int, K: int, A, weights, C, a_row_stride, c_row_stride, stream) -> None:
-    lda, ldc = K if a_row_stride is None else a_row_stride, N if c_row_stride is None else c_row_stride
+def _gemm(call, fn: str, fmt: int | None, A, AS, W, WS, C, M, N, K, lda, ldc, stream) -> None:
+    """A product with MXFP4 weights; fmt is that of the activations, None for BF16 rows of pitch lda."""
+    ldc = N if ldc is None else ldc
+    lda = K if lda is None else lda
     _sizes(fn, M | N | K | lda | ldc)
-    w = [_arg(fn, "weights", x, N * K // (32 if i & 1 else 2)) for i, x in enumerate(weights)]
-    _check(fn, getattr(lib(), fn)(_arg(fn, "A", A, _span(M, lda, K, 2)), *w, _arg(fn, "C", C, _span(M, ldc, N, 2)),
-                                  M, N, K, lda, ldc, _stream(stream)))
+    d, st = _here(stream)
+    w, ws = _arg(fn, "W", W, N * K // 2, d), _arg(fn, "WS", WS, N * K // 32, d)
+    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d)
+    if fmt is None:
+        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d), w, ws, c, M, N, K, lda, ldc, st)
+    else:
+        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d), _arg(fn, "AS", AS, M * K // 32, d), w, ws, c, M, N, K,
+                  ldc, st)
+    _check(fn, rc)
 
 
-def _quantised(fn: str, fmt: int, M: int, N: int, K: int, A, AS, weights, C, c_row_stride, stream) -> None:
-    ldc = N if c_row_stride is None else c_row_stride
-    _sizes(fn, M | N | K | ldc)
-    w = [_arg(fn, "weights", x, N * K // (32 if i & 1 else 2)) for i, x in enumerate(weights)]
-    _check(fn, getattr(lib(), fn)(_arg(fn, "A", A, _code_bytes(fmt, M * K)), _arg(fn, "AS", AS, M * K // 32), *w,
-                                  _arg(fn, "C", C, _span(M, ldc, N, 2)), M, N, K, ldc, _stream(stream)))
+def _gated(call, fn: str, fmt: int | None, A, AS, WG, WGS, WU, WUS, C, M, N, K, lda, ldc, stream) -> None:
+    """The same for the pair of products of a gated block."""
+    ldc = N if ldc is None else ldc
+    lda = K if lda is None else lda
+    _sizes(fn, M | N | K | lda | ldc)
+    d, st = _here(stream)
+    w = (_arg(fn, "WG", WG, N * K // 2, d), _arg(fn, "WGS", WGS, N * K // 32, d),
+         _arg(fn, "WU", WU, N * K // 2, d), _arg(fn, "WUS", WUS, N * K // 32, d))
+    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d)
+    if fmt is None:
+        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d), *w, c, M, N, K, lda, ldc, st)
+    else:
+        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d), _arg(fn, "AS", AS, M * K // 32, d), *w, c, M, N, K,
+                  ldc, st)
+    _check(fn, rc)
 
 
 def w4a16_gemm(A, W, WS, C, M: int, N: int, K: int, a_row_stride: int | None = None,
                c_row_stride: int | None = None, stream=None) -> None:
-    _a16("w4a16_gemm", M, N, K, A, (W, WS), C, a_row_stride, c_row_stride, stream)
+    _gemm((_lib or lib()).w4a16_gemm, "w4a16_gemm", None, A, None, W, WS, C, M, N, K, a_row_stride, c_row_stride, stream)
 
 
 def w4a8_gemm(A, AS, W, WS, C, M: int, N: int, K: int, c_row_stride: int | None = None, stream=None) -> None:
-    _quantised("w4a8_gemm", MXFP8, M, N, K, A, AS, (W, WS), C, c_row_stride, stream)
+    _gemm((_lib or lib()).w4a8_gemm, "w4a8_gemm", MXFP8, A, AS, W, WS, C, M, N, K, None, c_row_stride, stream)
 
 
 def w4a4_gemm(A, AS, W, WS, C, M: int, N: int, K: int, c_row_stride: int | None = None, stream=None) -> None:
-    _quantised("w4a4_gemm", MXFP4, M, N, K, A, AS, (W, WS), C, c_row_stride, stream)
+    _gemm((_lib or lib()).w4a4_gemm, "w4a4_gemm", MXFP4, A, AS, W, WS, C, M, N, K, None, c_row_stride, stream)
 
 
 def w4a16_gated(A, WG, WGS, WU, WUS, C, M: int, N: int, K: int, a_row_stride: int | None = None,
                 c_row_stride: int | None = None, stream=None) -> None:
-    _a16("w4a16_gated", M, N, K, A, (WG, WGS, WU, WUS), C, a_row_stride, c_row_stride, stream)
+    _gated((_lib or lib()).w4a16_gated, "w4a16_gated", None, A, None, WG, WGS, WU, WUS, C, M, N, K, a_row_stride,
+           c_row_stride, stream)
 
 
 def w4a8_gated(A, AS, WG, WGS, WU, WUS, C, M: int, N: int, K: int, c_row_stride: int | None = None,
                stream=None) -> None:
-    _quantised("w4a8_gated", MXFP8, M, N, K, A, AS, (WG, WGS, WU, WUS), C, c_row_stride, stream)
+    _gated((_lib or lib()).w4a8_gated, "w4a8_gated", MXFP8, A, AS, WG, WGS, WU, WUS, C, M, N, K, None, c_row_stride, stream)
 
 
 def w4a4_gated(A, AS, WG, WGS, WU, WUS, C, M: int, N: int, K: int, c_row_stride: int | None = None,
                stream=None) -> None:
-    _quantised("w4a4_gated", MXFP4, M, N, K, A, AS, (WG, WGS, WU, WUS), C, c_row_stride, stream)
+    _gated((_lib or lib()).w4a4_gated, "w4a4_gated", MXFP4, A, AS, WG, WGS, WU, WUS, C, M, N, K, None, c_row_stride, stream)
 
 
 # ------------------------------------------------------------ host helpers
