@@ -93,6 +93,10 @@ __device__ __forceinline__ uint32_t unit_turn(uint32_t r) { return ((r >> 2 & 1u
 // Byte offset in a unit of piece p of row r
 __device__ __forceinline__ uint32_t unit_byte(uint32_t r, uint32_t p) { return r * 64u + (p ^ unit_turn(r)) * 16u; }
 
+// The same for a tile of 16 rows x 128 bytes (two steps of 4-bit codes): piece p
+// of row r in slot p ^ pair_turn(r) of the eight.
+__device__ __forceinline__ uint32_t pair_turn(uint32_t r) { return (r >> 1 & 7u) ^ (r & 8u ? 0u : 2u); }
+
 // Bytes of n activation values
 template <MxFormat FMT>
 __device__ __forceinline__ uint32_t act_bytes(uint32_t n) {

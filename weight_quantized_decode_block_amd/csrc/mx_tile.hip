@@ -70,24 +70,47 @@ __device__ __forceinline__ void step_barrier() {
 }
 
 // KS: groups of waves that take the steps in turn and add their sums at the
-// end.  PP: the two halves of the waves, one of each per SIMD, run half a step
-// apart, one reading LDS while the other has the matrix unit.
-template <MxFormat FMT, int BM, int BN, int WM, int WN, int KS, int PRE, bool PP, bool GATED>
+// end.  MODE:
+constexpr int kPlain = 0;   // read a step's operands, multiply
+constexpr int kHalves = 1;  // the two halves of the waves, one of each per SIMD, run half a step apart:
+                            // one reads LDS while the other has the matrix unit
+constexpr int kPair = 2;    // MXFP4 activations: a stage is two steps, so that every row piece brought is a whole
+                            // 128-byte line, and one barrier serves both
+
+// LDS of a workgroup: PRE + 1 stages of all groups' (kPair: two) steps, and
+// two stages of scales, whose rows are the weights' (gated: of either matrix),
+// then the activations', in whole transfers of 64.
+template <int BN, bool GATED>
+constexpr uint32_t kMatScaleRows = (BN / (GATED ? 2 : 1) + 63) / 64 * 64;  // of one weight matrix
+template <MxFormat FMT, int BM, int BN, bool GATED>
+constexpr uint32_t kAllScaleRows = kMatScaleRows<BN, GATED> * (GATED ? 2 : 1) +
+                                   (FMT == MxFormat::kBf16 ? 0 : (BM + 63) / 64 * 64);
+template <MxFormat FMT, int BM, int BN, int KS, int MODE>
+constexpr uint32_t kStageBytes = (MODE == kPair ? 2 : KS) * (BN / 16 + BM / 16 * kActUnits<FMT>) * kUnit;
+
+template <MxFormat FMT, int BM, int BN, int KS, int PRE, int MODE, bool GATED>
+constexpr uint32_t lds_bytes() {
+  return (PRE + 1) * kStageBytes<FMT, BM, BN, KS, MODE> + 2 * kAllScaleRows<FMT, BM, BN, GATED> * 16;
+}
+
+template <MxFormat FMT, int BM, int BN, int WM, int WN, int KS, int PRE, int MODE, bool GATED>
 __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands op) {
-  static_assert(!PP || (KS == 1 && WM * WN == 8), "two waves per SIMD");
+  static_assert(MODE != kHalves || (KS == 1 && WM * WN == 8), "two waves per SIMD");
   constexpr uint32_t kGroupWaves = WM * WN, kWaves = kGroupWaves * KS;
   constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
   constexpr int NBUF = PRE + 1;
-  constexpr uint32_t kWUnits = BN / 16, kAUnits = BM / 16 * kActUnits<FMT>;
+  constexpr bool kTwo = MODE == kPair;  // two steps per stage, units of 8 rows x 128 bytes
+  static_assert(!kTwo || (FMT == MxFormat::kFp4 && KS == 1 && kGroupWaves % 4 == 0), "4-bit codes on both sides");
+  constexpr uint32_t kWUnits = BN / (kTwo ? 8 : 16), kAUnits = BM / (kTwo ? 8 : 16) * kActUnits<FMT>;
   constexpr uint32_t kStep = (kWUnits + kAUnits) * kUnit, kStage = KS * kStep;
+  static_assert((kStage == kStageBytes<FMT, BM, BN, KS, MODE>));
   static_assert(!GATED || (kWUnits % 2 == 0 && kGroupWaves % 2 == 0 && NT % 2 == 0), "units of the two matrices alternate");
   constexpr int WU = (kWUnits + kGroupWaves - 1) / kGroupWaves, AU = (kAUnits + kGroupWaves - 1) / kGroupWaves, ND = WU + AU;
   constexpr bool kActScales = FMT != MxFormat::kBf16;
-  // scale rows in LDS: the weights' (gated: of either matrix), then the activations', whole transfers of 64 rows
-  constexpr uint32_t kMatRows = (BN / (GATED ? 2 : 1) + 63) / 64 * 64, kWsRows = kMatRows * (GATED ? 2 : 1);
-  constexpr uint32_t kScaleRows = kWsRows + (kActScales ? (BM + 63) / 64 * 64 : 0);
+  constexpr uint32_t kMatRows = kMatScaleRows<BN, GATED>, kWsRows = kMatRows * (GATED ? 2 : 1);
+  constexpr uint32_t kScaleRows = kAllScaleRows<FMT, BM, BN, GATED>;
   constexpr uint32_t kScaleStage = kScaleRows * 16;
-  static_assert(kScaleRows <= 64 * kWaves, "at most one scale transfer per wave");
+  constexpr int SN = (kScaleRows / 64 + kWaves - 1) / kWaves;  // scale transfers per wave
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // NBUF stages, two scale stages
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
 
@@ -109,41 +132,61 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   const uint32_t nlast = (op.N - n0 < BNO ? op.N - n0 : BNO) - 1u;
 
   const uint32_t steps = op.K >> 7, nb = op.K >> 5, wpitch = op.K >> 1, apitch = act_bytes<FMT>(op.lda);
-  const uint32_t stages = (steps + KS - 1u) / KS;
+  constexpr uint32_t kSteps = kTwo ? 2 : KS;  // of a stage
+  const uint32_t stages = (steps + kSteps - 1u) / kSteps;
 
   // transfers of this wave for its group's step: weight units wave, wave +
   // kGroupWaves, ... and activation units likewise (where they do not come out
   // even, some are brought twice, the same bytes to the same place: every wave
   // then has as many transfers in flight as the waits count).  Gated: even units are the gate matrix, odd ones
   // the up matrix.
-  const bool up = GATED && (wave & 1u);
+  // Units of two steps: two are a tile of 16 rows, so the matrices alternate by
+  // pairs of units.
+  const bool up = GATED && (kTwo ? wave >> 1 & 1u : wave & 1u);
   const rsrc_t wr = bytes_rsrc(up ? op.WU : op.W, (uint64_t)n0 * wpitch, (nlast + 1u) * wpitch);
   const rsrc_t ar = bytes_rsrc(op.A, (uint64_t)m0 * apitch, mlast * apitch + act_bytes<FMT>(op.K));
-  const uint32_t lrow = lane >> 2, lpiece = ((lane & 3u) ^ unit_turn(lrow)) * 16u;  // this lane's row and piece of a unit
+  // this lane's row of a unit (of its 16-row tile) and piece of the row
+  const uint32_t lrow = kTwo ? (wave & 1u) * 8u + (lane >> 3) : lane >> 2;
+  const uint32_t lpiece = kTwo ? ((lane & 7u) ^ pair_turn(lrow)) * 16u : ((lane & 3u) ^ unit_turn(lrow)) * 16u;
+  constexpr uint32_t kPerTile = kTwo ? 2 : 1;  // weight units of a 16-row tile
   uint32_t woff[WU], aoff[AU];
 #pragma unroll
   for (int i = 0; i < WU; ++i) {
     const uint32_t u = (wave + kGroupWaves * i) % kWUnits;
-    const uint32_t row = (GATED ? u >> 1 : u) * 16u + lrow;
-    woff[i] = (row < nlast ? row : nlast) * wpitch + lpiece;
+    const uint32_t row = u / kPerTile / (GATED ? 2u : 1u) * 16u + lrow;
+    woff[i] = (row < nlast ? row : nlast) * wpitch + (kTwo ? 0u : lpiece);
   }
 #pragma unroll
   for (int i = 0; i < AU; ++i) {
     const uint32_t u = (wave + kGroupWaves * i) % kAUnits;
-    const uint32_t row = u / kActUnits<FMT> * 16u + lrow;
-    aoff[i] = (row < mlast ? row : mlast) * apitch + (u % kActUnits<FMT>) * 64u + lpiece;
+    const uint32_t row = (kTwo ? u / 2u : u / kActUnits<FMT>) * 16u + lrow;
+    aoff[i] = (row < mlast ? row : mlast) * apitch + (kTwo ? 0u : (u % kActUnits<FMT>) * 64u + lpiece);
   }
-  // scale rows 64 w .. 64 w + 63 of wave w: weights (gated: gate, then up), then activations
-  const uint32_t srow = all_wave * 64u + lane;
-  const bool s_act = all_wave * 64u >= kWsRows, s_up = GATED && !s_act && all_wave * 64u >= kMatRows;
-  const bool s_any = all_wave * 64u < kScaleRows;
-  const rsrc_t sr = s_act ? bytes_rsrc(op.AS, (uint64_t)m0 * nb, (mlast + 1u) * nb)
-                          : bytes_rsrc(s_up ? op.WUS : op.WS, (uint64_t)n0 * nb, (nlast + 1u) * nb);
-  const uint32_t s_in = s_act ? srow - kWsRows : (s_up ? srow - kMatRows : srow);
-  const uint32_t s_last = s_act ? mlast : nlast;
-  const uint32_t soff = (s_in < s_last ? s_in : s_last) * nb;
+  // scale rows 64 p .. 64 p + 63 in transfer p, waves in turn: weights (gated: gate, then up), then activations
+  rsrc_t sr[SN];
+  uint32_t soff[SN];
+#pragma unroll
+  for (int i = 0; i < SN; ++i) {
+    const uint32_t row = (all_wave + (uint32_t)i * kWaves) * 64u;
+    const bool act = row >= kWsRows, s_up = GATED && !act && row >= kMatRows;
+    sr[i] = act ? bytes_rsrc(op.AS, (uint64_t)m0 * nb, (mlast + 1u) * nb)
+                : bytes_rsrc(s_up ? op.WUS : op.WS, (uint64_t)n0 * nb, (nlast + 1u) * nb);
+    const uint32_t in = row - (act ? kWsRows : (s_up ? kMatRows : 0u)) + lane, last = act ? mlast : nlast;
+    soff[i] = (in < last ? in : last) * nb;
+  }
 
   auto issue = [&](uint32_t stage, uint32_t buf) __attribute__((always_inline)) {
+    if constexpr (kTwo) {
+      // where the last stage is one step, its pieces are brought twice
+      const uint32_t k = stage * 128u + (stage * 2u + 1u < steps ? lpiece : lpiece & 48u);
+#pragma unroll
+      for (int i = 0; i < WU; ++i)
+        copy_to_lds(lds0 + buf * kStage + (wave + i * kGroupWaves) % kWUnits * kUnit, wr, woff[i] + k);
+#pragma unroll
+      for (int i = 0; i < AU; ++i)
+        copy_to_lds(lds0 + buf * kStage + (kWUnits + (wave + kGroupWaves * i) % kAUnits) * kUnit, ar, aoff[i] + k);
+      return;
+    }
     uint32_t s = stage * KS + ks;
     if (KS > 1) s = s < steps ? s : steps - 1u;  // a step too many is brought but not computed
     const uint32_t base = lds0 + buf * kStage + ks * kStep;
@@ -156,7 +199,11 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   // the 16 scale bytes from step 4q on, or the row's last 16 where fewer are left (nb >= 16)
   auto issue_scales = [&](uint32_t q) __attribute__((always_inline)) {
     const uint32_t at = 16u * q + 16u <= nb ? 16u * q : nb - 16u;
-    if (s_any) copy_to_lds(lds0 + NBUF * kStage + (q & 1u) * kScaleStage + all_wave * kUnit, sr, soff + at);
+#pragma unroll
+    for (int i = 0; i < SN; ++i) {
+      const uint32_t p = all_wave + (uint32_t)i * kWaves;
+      if (p < kScaleRows / 64u) copy_to_lds(lds0 + NBUF * kStage + (q & 1u) * kScaleStage + p * kUnit, sr[i], soff[i] + at);
+    }
   };
 
   const uint32_t wm = wave / WN, wn = wave % WN;  // this wave's part of the tile
@@ -220,7 +267,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   });
   uint32_t buf = 0;
   constexpr int kGroup = 4 / KS;  // stages per group of four steps
-  if constexpr (PP) {
+  if constexpr (MODE == kHalves) {
     // Stage s has arrived for everybody before the barrier that ends the read
     // half of stage s - 1; the second half of the waves starts one barrier late.
     if (PRE <= stages)
@@ -267,6 +314,44 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
       });
     }
     if (wave < 4u) __builtin_amdgcn_s_barrier();
+  } else if constexpr (MODE == kPair) {
+    for (uint32_t s0 = 0; s0 < stages; s0 += 2u) {
+      mx_unroll<0, 2>([&](auto T) __attribute__((always_inline)) {
+        constexpr int t = decltype(T)::value;
+        const uint32_t s = s0 + t;
+        if (s < stages) {
+          if (s + PRE <= stages)
+            step_barrier<(PRE - 1) * ND>();
+          else
+            step_barrier<0>();
+          if constexpr (t == 0) {
+            read_scales(s0 / 2u);
+            if (s0 + 2u < stages) issue_scales(s0 / 2u + 1u);
+          }
+          if (s + PRE < stages) issue(s + PRE, buf == 0 ? NBUF - 1 : buf - 1);
+          mx_unroll<0, 2>([&](auto H) __attribute__((always_inline)) {
+            constexpr int h = decltype(H)::value;
+            if (h == 0 || s * 2u + 1u < steps) {
+              const uint32_t mine2 = r * 128u + ((h * 4u + g) ^ pair_turn(r)) * 16u;
+              const uint8_t *pw = lds + buf * kStage + wn * NT * 2u * kUnit + mine2;
+              const uint8_t *pa = lds + buf * kStage + (kWUnits + wm * MT * 2u) * kUnit + mine2;
+              WeightCodes w[NT];
+              ActRegs<FMT> a[MT];
+#pragma unroll
+              for (int j = 0; j < MT; ++j) a[j] = {{*reinterpret_cast<const u32x4_t *>(pa + j * 2 * kUnit)}, asc[kActScales ? j : 0]};
+#pragma unroll
+              for (int i = 0; i < NT; ++i) w[i] = {*reinterpret_cast<const u32x4_t *>(pw + i * 2 * kUnit), wsc[i]};
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+                  acc[i][j] = mx_mfma<FMT, t * 2 + h>(WeightRegs<FMT, t * 2 + h>(w[i]), a[j], acc[i][j]);
+            }
+          });
+          buf = buf + 1u == (uint32_t)NBUF ? 0u : buf + 1u;
+        }
+      });
+    }
   } else {
     for (uint32_t s0 = 0; s0 < stages; s0 += kGroup) {
       mx_unroll<0, kGroup>([&](auto T) __attribute__((always_inline)) {
@@ -344,12 +429,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   }
 }
 
-template <MxFormat FMT, int BM, int BN, int WM, int WN, int KS, int PRE, bool PP, bool GATED>
+template <MxFormat FMT, int BM, int BN, int WM, int WN, int KS, int PRE, int MODE, bool GATED>
 hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
-  constexpr auto kern = mx_tile_kernel<FMT, BM, BN, WM, WN, KS, PRE, PP, GATED>;
-  constexpr uint32_t kLds = (PRE + 1) * KS * (BN / 16 + BM / 16 * kActUnits<FMT>) * kUnit +
-                            2 * ((BN / (GATED ? 2 : 1) + 63) / 64 * 64 * (GATED ? 2 : 1) +
-                                 (FMT == MxFormat::kBf16 ? 0 : (BM + 63) / 64 * 64)) * 16;
+  constexpr auto kern = mx_tile_kernel<FMT, BM, BN, WM, WN, KS, PRE, MODE, GATED>;
+  constexpr uint32_t kLds = lds_bytes<FMT, BM, BN, KS, PRE, MODE, GATED>();
   static_assert(kLds <= 160 * 1024, "one workgroup's LDS");
   static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
@@ -409,14 +492,13 @@ struct Costs<MxFormat::kFp8, true> {
 };
 template <>
 struct Costs<MxFormat::kFp4, false> {
-  static constexpr Cost v[] = {{32, 32, 140, 115, 1},   {64, 64, 206, 172, 2},    {128, 128, 569, 435, 2},
-                               {128, 160, 663, 545, 1}, {256, 160, 1022, 948, 1}, {256, 224, 1240, 1180, 1},
-                               {256, 256, 1328, 1290, 1}};
+  static constexpr Cost v[] = {{32, 32, 140, 115, 1}, {64, 64, 206, 172, 2}, {128, 128, 509, 377, 2},
+                               {256, 192, 1064, 983, 1}, {256, 256, 1289, 1230, 1}};
 };
 template <>
 struct Costs<MxFormat::kFp4, true> {
-  static constexpr Cost v[] = {{32, 16, 140, 115, 1},  {64, 64, 331, 285, 2},    {128, 64, 569, 435, 2},
-                               {192, 128, 1143, 1080, 1}, {256, 128, 1328, 1290, 1}};
+  static constexpr Cost v[] = {{32, 16, 140, 115, 1}, {64, 64, 331, 285, 2}, {128, 64, 509, 377, 2},
+                               {192, 128, 1076, 987, 1}, {256, 128, 1289, 1230, 1}};
 };
 
 uint64_t cost_of(const Cost &c, const MxOperands &op, uint32_t cus) {
@@ -442,26 +524,36 @@ hipError_t launch_fmt(const MxOperands &op, uint32_t cus, hipStream_t stream) {
   const uint32_t i = pick<FMT, GATED>(op, cus);
   if (i == 0u) return launch_mx_skinny(op, FMT, GATED, stream);
   if constexpr (FMT == MxFormat::kBf16 && GATED) {
-    if (i == 1u) return launch_cfg<FMT, 64, 128, 1, 4, 2, 1, false, GATED>(op, stream);
-    if (i == 2u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, true, GATED>(op, stream);
-    return launch_cfg<FMT, 128, 256, 1, 8, 1, 2, true, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 128, 1, 4, 2, 1, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
+    return launch_cfg<FMT, 128, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
   } else if constexpr (FMT == MxFormat::kBf16) {
-    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, false, GATED>(op, stream);
-    if (i == 2u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, true, GATED>(op, stream);
-    if (i == 3u) return launch_cfg<FMT, 128, 192, 2, 4, 1, 2, true, GATED>(op, stream);
-    return launch_cfg<FMT, 128, 256, 1, 8, 1, 2, true, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 128, 192, 2, 4, 1, 2, kHalves, GATED>(op, stream);
+    return launch_cfg<FMT, 128, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
+  } else if constexpr (FMT == MxFormat::kFp4 && GATED) {
+    if (i == 1u) return launch_cfg<FMT, 64, 128, 2, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 1, kPair, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 192, 256, 4, 2, 1, 1, kPair, GATED>(op, stream);
+    return launch_cfg<FMT, 256, 256, 4, 2, 1, 1, kPair, GATED>(op, stream);
+  } else if constexpr (FMT == MxFormat::kFp4) {
+    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 1, kPair, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 256, 192, 4, 2, 1, 1, kPair, GATED>(op, stream);
+    return launch_cfg<FMT, 256, 256, 4, 2, 1, 1, kPair, GATED>(op, stream);
   } else if constexpr (GATED) {
-    if (i == 1u) return launch_cfg<FMT, 64, 128, 2, 2, 2, 2, false, GATED>(op, stream);
-    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, true, GATED>(op, stream);
-    if (i == 3u) return launch_cfg<FMT, 192, 256, 4, 2, 1, 2, true, GATED>(op, stream);
-    return launch_cfg<FMT, 256, 256, 4, 2, 1, 2, true, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 128, 2, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 192, 256, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    return launch_cfg<FMT, 256, 256, 4, 2, 1, 2, kHalves, GATED>(op, stream);
   } else {
-    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, false, GATED>(op, stream);
-    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, true, GATED>(op, stream);
-    if (i == 3u) return launch_cfg<FMT, 128, 160, 4, 2, 1, 2, true, GATED>(op, stream);
-    if (i == 4u) return launch_cfg<FMT, 256, 160, 4, 2, 1, 2, true, GATED>(op, stream);
-    if (i == 5u) return launch_cfg<FMT, 256, 224, 4, 2, 1, 2, true, GATED>(op, stream);
-    return launch_cfg<FMT, 256, 256, 4, 2, 1, 2, true, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 128, 160, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 4u) return launch_cfg<FMT, 256, 160, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 5u) return launch_cfg<FMT, 256, 224, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    return launch_cfg<FMT, 256, 256, 4, 2, 1, 2, kHalves, GATED>(op, stream);
   }
 }
 
