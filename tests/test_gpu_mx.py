@@ -257,6 +257,24 @@ def test_product_exact_sums(fmt, M, N, K):
     assert np.array_equal(gen.bf16_values(c).astype(np.float64), ref.bf16(want))
 
 
+# The tile sizes are chosen by M, N and the format (csrc/mx_tile.hip, Costs): with 256 compute units these
+# outputs meet every one of them, for products and gated pairs of each format, with ragged last tiles; the
+# K have 4, 5, 6, 7 and 9 steps of 128, so the last group of four is full and partial, pairs whole and half.
+MANY = [(33, 4164, 640), (65, 12493, 512), (65, 16714, 896), (67, 8321, 1152), (98, 16549, 768), (130, 16408, 640),
+        (132, 13672, 512), (257, 13829, 896), (293, 16391, 640), (385, 12515, 1152), (397, 16447, 640),
+        (482, 10850, 768), (528, 16458, 512), (645, 16512, 896), (781, 14341, 640)]
+
+
+@pytest.mark.parametrize("fmt", ACTS)
+@pytest.mark.parametrize("M,N,K", MANY)
+def test_many_outputs_exact_sums(fmt, M, N, K):
+    a, s = ref.exact_activations(M + N, M, K, fmt)
+    w, ws = ref.weights(K + N, N, K)
+    c = product_gpu(fmt, a, s, (w, ws), N, K, lda_pad=8, ldc_pad=N % 3, shift=M % 2)
+    want, _ = sums(ref.act_values(a, s, fmt), ref.values(w, ws, "mxfp4"), exact=True)
+    assert np.array_equal(gen.bf16_values(c).astype(np.float64), ref.bf16(want))
+
+
 def check_product(c, want, mag, K):
     e = K * 2.0 ** -24 * mag
     d = np.abs(gen.bf16_values(c).astype(np.float64) - want)
@@ -280,6 +298,16 @@ def test_product_random(fmt, M, N, K, lda_pad, ldc_pad, shift):
 @pytest.mark.parametrize("M,N,K,ldc_pad,shift", [(1, 1000, 1024, 0, 0), (5, 17, 384, 3, 1), (16, 128, 5120, 0, 0), (33, 130, 640, 2, 2),
                                                  (64, 64, 1024, 0, 0), (129, 257, 1280, 1, 0), (300, 384, 2048, 0, 0), (520, 129, 896, 7, 3)])
 def test_gated(fmt, M, N, K, ldc_pad, shift):
+    check_gated(fmt, M, N, K, ldc_pad, shift)
+
+
+@pytest.mark.parametrize("fmt", ACTS)
+@pytest.mark.parametrize("M,N,K", MANY)
+def test_gated_many_outputs(fmt, M, N, K):
+    check_gated(fmt, M, N, K, N % 4, 0)
+
+
+def check_gated(fmt, M, N, K, ldc_pad, shift):
     a, s = ref.activations(M + 1, M, K, fmt)
     g, gs = ref.weights(2 * N, N, K, spread=5)
     u, us = ref.weights(2 * N + 1, N, K, spread=5)
@@ -447,6 +475,10 @@ def test_binding_checks_tensors():
         wqd.mx_quantize(x, q, s, "mxfp8", 4, 64)
     with pytest.raises(ValueError, match="fewer"):
         wqd.mx_quantize(x, q, s, "mxfp4", 4, 64, x_row_stride=72)
+    with pytest.raises(ValueError, match="2-byte"):
+        wqd.w4a16_gemm(x.float(), q, s, x, 4, 4, 64)
+    with pytest.raises(ValueError, match="1-byte"):
+        wqd.mx_dequantize(q, s.half(), x, "mxfp4", 4, 64)
     with pytest.raises(ValueError, match="contiguous"):
         wqd.mx_quantize(x.t(), q, s, "mxfp4", 4, 64)
     with pytest.raises(ValueError, match="current GPU"):

@@ -1,30 +1,46 @@
 // Products with MXFP4 weights for many rows, for gfx950 (MI355X): the
 // operations of mx_skinny.hip, bound by the matrix instructions.
 //
-// A workgroup of 8 waves owns BM x BN outputs (in the gated form BN / 2
-// outputs of both matrices) and walks K in steps of 128.  Each wave owns a
-// (BM / WM) x (BN / WN) part as 16 x 16 tiles: the weights are the matrix
-// instruction's rows, the activations its columns, so a lane ends with four
-// consecutive n of one m.
+// A workgroup owns BM x BN outputs (in the gated form BN / 2 outputs of both
+// matrices) and walks K in steps of 128.  Each wave owns a (BM / WM) x (BN / WN)
+// part as 16 x 16 tiles: the weights are the matrix instruction's rows, the
+// activations its columns, so a lane ends with four consecutive n of one m.
 //
-//   * Staging.  A step's codes go straight from memory to LDS (16 bytes per
-//     lane, no registers), PRE steps ahead of their use, into NBUF = PRE + 1
-//     buffers.  The unit is 16 rows x 64 bytes in one instruction.  Four
-//     neighbouring lanes bring the four 16-byte pieces of a row: with the lanes
-//     in a matrix operand's own order (neighbours in different rows) the same
-//     transfers run at a quarter of the rate (37 instead of 120 to 146 GB/s per
-//     compute unit from L2).
-//     Rows past the matrix repeat its last row; their outputs are not stored.
+//   * Staging.  Codes go straight from memory to LDS (16 bytes per lane, no
+//     registers), PRE stages ahead of their use, into PRE + 1 buffers.  A
+//     transfer is 16 rows x 64 bytes, four neighbouring lanes the four pieces of
+//     a row: with the lanes in a matrix operand's own order (neighbours in
+//     different rows) the same transfers run at a quarter of the rate (37
+//     instead of 120 to 146 GB/s per compute unit from L2).  4-bit codes of one
+//     step are half a 128-byte line per row; with 4-bit codes on both sides
+//     large tiles stage two steps at once as 8 rows x 128 bytes (transfers alone
+//     95 instead of 54 GB/s per compute unit, 128 x 128 tiles 435 -> 377 ns a
+//     step).  Rows past the matrix repeat its last row; their outputs are not
+//     stored.
 //   * Scales.  16 bytes per row cover four steps; they are staged the same way
 //     one group of four steps ahead.  A wave reads them once per group and
 //     turns them so that byte t of a lane's register is its k block in step t,
 //     which the matrix instruction's byte select takes directly.
-//   * One barrier per step: before it a wave waits for its own transfers of the
-//     step (later ones stay in flight) and for its LDS reads; after it the
-//     buffer of the step before is free.
+//   * A wave waits for its own transfers of a stage (later ones stay in flight)
+//     and for its LDS reads before the barrier that opens the stage; after it
+//     the buffer of the stage before is free.
+//   * Large tiles run the two halves of the waves half a step apart (kHalves):
+//     4096 x 17408, K = 5120, MXFP8 380 -> 312 us; 1000 x 5120, K = 17408, BF16
+//     207 -> 188.  Small tiles, bound by the latency of a step, give alternate
+//     steps to two groups of waves (KS = 2): 64 x 5120, K = 5120, MXFP8 14.8 ->
+//     9.7 us.
+//   * BF16 activations: the weights are converted between the matrix
+//     instructions that use them, and 8 waves side by side in n convert each
+//     weight once (the conversions, 7.5 cycles each, otherwise cost as much as
+//     half the matrix instructions).
 //   * Workgroups are dealt to the 8 XCDs in contiguous runs of tiles, and tiles
 //     run down four tile rows before the next tile column, so the workgroups
 //     that share an L2 at one time share rows of both operands.
+//
+// What bounds it: with all compute units on random operands the chip lowers its
+// clock (matrix instructions alone reach 4.3 PFLOP/s on FP4 x FP8, 8 on FP4 x
+// FP4, 2.1 on BF16); 4096 x 17408, K = 5120, MXFP8 runs at 2.45 PFLOP/s, 4096 x
+// 5120, K = 5120, MXFP4 at 2.8, 1000 x 5120, K = 17408, BF16 at 1.19.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -429,13 +445,25 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   }
 }
 
+// Lets a kernel use all of a compute unit's LDS on the current device, once per device.
+hipError_t allow_lds(const void *kern, std::atomic<uint64_t> &ready) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit && (ready.load(std::memory_order_relaxed) & bit)) return hipSuccess;
+  e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  if (e == hipSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 template <MxFormat FMT, int BM, int BN, int WM, int WN, int KS, int PRE, int MODE, bool GATED>
 hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
   constexpr auto kern = mx_tile_kernel<FMT, BM, BN, WM, WN, KS, PRE, MODE, GATED>;
   constexpr uint32_t kLds = lds_bytes<FMT, BM, BN, KS, PRE, MODE, GATED>();
   static_assert(kLds <= 160 * 1024, "one workgroup's LDS");
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  static std::atomic<uint64_t> ready;  // devices on which the kernel may use that much LDS
+  const hipError_t attr = allow_lds(reinterpret_cast<const void *>(kern), ready);
   if (attr != hipSuccess) return attr;
   const uint32_t bno = GATED ? BN / 2 : BN;
   const uint32_t tn = (op.N + bno - 1u) / bno;

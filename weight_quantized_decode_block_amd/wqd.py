@@ -185,15 +185,17 @@ def _span(rows: int, pitch: int, width: int, size: int) -> int:
     return ((rows - 1) * pitch + width) * size if rows > 0 else 0
 
 
-def _arg(fn: str, name: str, x, nbytes: int, device: int) -> int | None:
+def _arg(fn: str, name: str, x, nbytes: int, device: int, size: int = 1) -> int | None:
     """Device address of an operand.  A tensor must live on `device`, the current
-    one (the call goes to its stream), with its last dimension contiguous, and
-    its memory must reach `nbytes` past its first element; an integer is taken as
-    it is."""
+    one (the call goes to its stream), have `size`-byte elements and its last
+    dimension contiguous, and its memory must reach `nbytes` past its first
+    element; an integer is taken as it is."""
     if x is None or isinstance(x, int):
         return x
     if x.get_device() != device:
         raise ValueError(f"{fn}: {name} is not on the current GPU")
+    if x.element_size() != size:
+        raise ValueError(f"{fn}: {name} must have {size}-byte elements")
     if x.nbytes < nbytes or not x.is_contiguous():  # perhaps rows of a wider buffer
         if x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
             raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
@@ -253,8 +255,9 @@ def mx_quantize(X, Q, S, fmt, M: int, K: int, x_row_stride: int | None = None, x
     fn, ld = "mx_quantize", K if x_row_stride is None else x_row_stride
     _sizes(fn, M | K | ld)
     f, t = _mx_format(fn, fmt), _type_of(fn, X, x_type)
+    w = 4 if t == TYPE_FP32 else 2
     d, st = _here(stream)
-    _check(fn, (_lib or lib()).mx_quantize(_arg(fn, "X", X, _span(M, ld, K, 4 if t == TYPE_FP32 else 2), d), t,
+    _check(fn, (_lib or lib()).mx_quantize(_arg(fn, "X", X, _span(M, ld, K, w), d, w), t,
                                            _arg(fn, "Q", Q, _code_bytes(f, M * K), d),
                                            _arg(fn, "S", S, M * K // 32, d), f, M, K, ld, st))
 
@@ -265,10 +268,11 @@ def mx_dequantize(Q, S, Y, fmt, M: int, K: int, y_row_stride: int | None = None,
     fn, ld = "mx_dequantize", K if y_row_stride is None else y_row_stride
     _sizes(fn, M | K | ld)
     f, t = _mx_format(fn, fmt), _type_of(fn, Y, y_type)
+    w = 4 if t == TYPE_FP32 else 2
     d, st = _here(stream)
     _check(fn, (_lib or lib()).mx_dequantize(_arg(fn, "Q", Q, _code_bytes(f, M * K), d),
                                              _arg(fn, "S", S, M * K // 32, d), f,
-                                             _arg(fn, "Y", Y, _span(M, ld, K, 4 if t == TYPE_FP32 else 2), d), t,
+                                             _arg(fn, "Y", Y, _span(M, ld, K, w), d, w), t,
                                              M, K, ld, st))
 
 
@@ -281,9 +285,9 @@ def add_rmsnorm_mx8(X, R, G, H, Y, Q, S, M: int, K: int, eps: float, x_row_strid
     _sizes(fn, M | K | lx | lr)
     rows = _span(M, lr, K, 2)
     d, st = _here(stream)
-    _check(fn, (_lib or lib()).add_rmsnorm_mx8(_arg(fn, "X", X, _span(M, lx, K, 2), d), _arg(fn, "R", R, rows, d),
-                                               _arg(fn, "G", G, 2 * K, d), _arg(fn, "H", H, rows, d),
-                                               _arg(fn, "Y", Y, 2 * M * K, d), _arg(fn, "Q", Q, M * K, d),
+    _check(fn, (_lib or lib()).add_rmsnorm_mx8(_arg(fn, "X", X, _span(M, lx, K, 2), d, 2), _arg(fn, "R", R, rows, d, 2),
+                                               _arg(fn, "G", G, 2 * K, d, 2), _arg(fn, "H", H, rows, d, 2),
+                                               _arg(fn, "Y", Y, 2 * M * K, d, 2), _arg(fn, "Q", Q, M * K, d),
                                                _arg(fn, "S", S, M * K // 32, d), M, K, lx, lr, eps, st))
 
 
@@ -294,9 +298,9 @@ def _gemm(call, fn: str, fmt: int | None, A, AS, W, WS, C, M, N, K, lda, ldc, st
     _sizes(fn, M | N | K | lda | ldc)
     d, st = _here(stream)
     w, ws = _arg(fn, "W", W, N * K // 2, d), _arg(fn, "WS", WS, N * K // 32, d)
-    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d)
+    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, 2)
     if fmt is None:
-        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d), w, ws, c, M, N, K, lda, ldc, st)
+        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, 2), w, ws, c, M, N, K, lda, ldc, st)
     else:
         rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d), _arg(fn, "AS", AS, M * K // 32, d), w, ws, c, M, N, K,
                   ldc, st)
@@ -311,9 +315,9 @@ def _gated(call, fn: str, fmt: int | None, A, AS, WG, WGS, WU, WUS, C, M, N, K, 
     d, st = _here(stream)
     w = (_arg(fn, "WG", WG, N * K // 2, d), _arg(fn, "WGS", WGS, N * K // 32, d),
          _arg(fn, "WU", WU, N * K // 2, d), _arg(fn, "WUS", WUS, N * K // 32, d))
-    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d)
+    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, 2)
     if fmt is None:
-        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d), *w, c, M, N, K, lda, ldc, st)
+        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, 2), *w, c, M, N, K, lda, ldc, st)
     else:
         rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d), _arg(fn, "AS", AS, M * K // 32, d), *w, c, M, N, K,
                   ldc, st)
