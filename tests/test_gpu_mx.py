@@ -270,9 +270,10 @@ MANY = [(33, 4164, 640), (65, 12493, 512), (65, 16714, 896), (67, 8321, 1152), (
 def test_many_outputs_exact_sums(fmt, M, N, K):
     a, s = ref.exact_activations(M + N, M, K, fmt)
     w, ws = ref.weights(K + N, N, K)
-    c = product_gpu(fmt, a, s, (w, ws), N, K, lda_pad=8, ldc_pad=N % 3, shift=M % 2)
-    want, _ = sums(ref.act_values(a, s, fmt), ref.values(w, ws, "mxfp4"), exact=True)
-    assert np.array_equal(gen.bf16_values(c).astype(np.float64), ref.bf16(want))
+    want = ref.bf16(sums(ref.act_values(a, s, fmt), ref.values(w, ws, "mxfp4"), exact=True)[0])
+    for pad, shift in ((N % 3, M % 2), (-N % 8, 0)):  # outputs at any alignment, and whole 16-byte pieces
+        c = product_gpu(fmt, a, s, (w, ws), N, K, lda_pad=8, ldc_pad=pad, shift=shift)
+        assert np.array_equal(gen.bf16_values(c).astype(np.float64), want)
 
 
 def check_product(c, want, mag, K):
@@ -304,7 +305,8 @@ def test_gated(fmt, M, N, K, ldc_pad, shift):
 @pytest.mark.parametrize("fmt", ACTS)
 @pytest.mark.parametrize("M,N,K", MANY)
 def test_gated_many_outputs(fmt, M, N, K):
-    check_gated(fmt, M, N, K, N % 4, 0)
+    for ldc_pad in (N % 3, -N % 8):
+        check_gated(fmt, M, N, K, ldc_pad, 0)
 
 
 def check_gated(fmt, M, N, K, ldc_pad, shift):

@@ -180,7 +180,7 @@ int run_mx_product(const char *fn, wqd::MxOperands op, wqd::MxFormat fmt, bool g
   if (!aligned(op.out.C, 2)) return fail(WQD_EALIGN, "%s: C must be 2-byte aligned", fn);
   if (op.M == 0) return WQD_OK;  // no rows: nothing to launch
   if (int rc = check_device(fn)) return rc;
-  op.out.wide = aligned(op.out.C, 8) && op.out.ldc % 4u == 0;
+  op.out.wide = aligned(op.out.C, 16) && op.out.ldc % 8u == 0 ? 2u : (aligned(op.out.C, 8) && op.out.ldc % 4u == 0 ? 1u : 0u);
   (void)hipGetLastError();
   return check_launch(fn, wqd::launch_mx_product(op, fmt, gated, stream));
 }

@@ -422,27 +422,51 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   }
 
   // the lane again, so that nothing of it stays in registers through the loop
-  const uint32_t l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)), ln = (l >> 4) * 4u;
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const uint32_t m = m0 + (wm * MT + j) * 16u + (l & 15u);
+  const uint32_t l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)), lm = l & 15u, ln = (l >> 4) * 4u;
+  constexpr int NO = GATED ? NT / 2 : NT;  // 16-column output tiles of this wave
+  const uint32_t mw = m0 + wm * MT * 16u, nw = n0 + wn * NO * 16u;
+  auto output = [&](int i, int j) __attribute__((always_inline)) {
     if constexpr (GATED) {
+      f32x4_t c;
 #pragma unroll
-      for (int i = 0; i < NT; i += 2) {
-        f32x4_t c;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = silu_times(acc[i][j][e], acc[i + 1][j][e]);
-        const uint32_t n = n0 + (wn * NT + i) * 8u + ln;
-        if (m < op.M) store4(op.out, op.N, m, n, c);
-      }
+      for (int e = 0; e < 4; ++e) c[e] = silu_times(acc[2 * i][j][e], acc[2 * i + 1][j][e]);
+      return c;
     } else {
+      return acc[i][j];
+    }
+  };
+  // A lane holds 4 columns of a row: written as they are, an instruction covers
+  // 32 bytes of 16 rows.  Large tiles inside the matrix go through LDS, each
+  // wave's part on its own, and leave in whole row pieces of 16 bytes per lane.
+  if constexpr (KS == 1) {
+    constexpr uint32_t kRow = NO * 32 + 16, kPieces = NO * 2, kPart = MT * 16 * kRow;  // bytes, 16-byte pieces of a row
+    static_assert(kPart % 16 == 0 && kWaves * kPart <= lds_bytes<FMT, BM, BN, KS, PRE, MODE, GATED>(), "outputs fit in LDS");
+    if (op.out.wide >= 2u && n0 + BNO <= op.N) {
+      step_barrier<0>();  // everybody has read the last stage
+      uint8_t *part = lds + wave * kPart;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const uint32_t n = n0 + (wn * NT + i) * 16u + ln;
-        if (m < op.M) store4(op.out, op.N, m, n, acc[i][j]);
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+          const f32x4_t c = output(i, j);
+          *reinterpret_cast<u32x2_t *>(part + (j * 16u + lm) * kRow + i * 32u + ln * 2u) =
+              u32x2_t{bf16x2_rne(c[0], c[1]), bf16x2_rne(c[2], c[3])};
+        }
+#pragma unroll
+      for (uint32_t p = 0; p < (MT * 16u * kPieces + 63u) / 64u; ++p) {
+        const uint32_t x = p * 64u + l, row = x / kPieces, piece = x % kPieces;
+        if ((MT * 16u * kPieces % 64u == 0u || x < MT * 16u * kPieces) && mw + row < op.M)
+          *reinterpret_cast<u32x4_t *>(op.out.C + (uint64_t)(mw + row) * op.out.ldc + nw + piece * 8u) =
+              *reinterpret_cast<const u32x4_t *>(part + row * kRow + piece * 16u);
       }
+      return;
     }
   }
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+      if (mw + j * 16u + lm < op.M) store4(op.out, op.N, mw + j * 16u + lm, nw + i * 16u + ln, output(i, j));
 }
 
 // Lets a kernel use all of a compute unit's LDS on the current device, once per device.

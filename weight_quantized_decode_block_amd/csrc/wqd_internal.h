@@ -69,7 +69,7 @@ enum class MxFormat : int { kBf16, kFp8, kFp4 };
 struct MxOut {
   uint16_t *C;
   uint32_t ldc;
-  uint32_t wide;  // every 4 columns of C start on an 8-byte boundary
+  uint32_t wide;  // 1: every 4 columns of C start on an 8-byte boundary, 2: and every 8 on a 16-byte one
 };
 
 // Operands of one product (or gated pair of products) with MXFP4 weights.
