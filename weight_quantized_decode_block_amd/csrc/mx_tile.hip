@@ -12,10 +12,10 @@
 //     a row: with the lanes in a matrix operand's own order (neighbours in
 //     different rows) the same transfers run at a quarter of the rate (37
 //     instead of 120 to 146 GB/s per compute unit from L2).  4-bit codes of one
-//     step are half a 128-byte line per row; with 4-bit codes on both sides
-//     large tiles stage two steps at once as 8 rows x 128 bytes (transfers alone
-//     95 instead of 54 GB/s per compute unit, 128 x 128 tiles 435 -> 377 ns a
-//     step).  Rows past the matrix repeat its last row; their outputs are not
+//     step are half a 128-byte line per row; where a stage is two steps they are
+//     brought together, 8 rows x 128 bytes a transfer (transfers alone 95
+//     instead of 54 GB/s per compute unit, 128 x 128 tiles of 4-bit codes on
+//     both sides 435 -> 377 ns a step).  Rows past the matrix repeat its last row; their outputs are not
 //     stored.
 //   * Scales.  16 bytes per row cover four steps; they are staged the same way
 //     one group of four steps ahead.  A wave reads them once per group and
@@ -90,8 +90,7 @@ __device__ __forceinline__ void step_barrier() {
 constexpr int kPlain = 0;   // read a step's operands, multiply
 constexpr int kHalves = 1;  // the two halves of the waves, one of each per SIMD, run half a step apart:
                             // one reads LDS while the other has the matrix unit
-constexpr int kPair = 2;    // MXFP4 activations: a stage is two steps, so that every row piece brought is a whole
-                            // 128-byte line, and one barrier serves both
+constexpr int kPair = 2;    // MXFP4 activations: a stage is two steps, which one barrier serves
 
 // LDS of a workgroup: PRE + 1 stages of all groups' (kPair: two) steps, and
 // two stages of scales, whose rows are the weights' (gated: of either matrix),
@@ -115,13 +114,19 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   constexpr uint32_t kGroupWaves = WM * WN, kWaves = kGroupWaves * KS;
   constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
   constexpr int NBUF = PRE + 1;
-  constexpr bool kTwo = MODE == kPair;  // two steps per stage, units of 8 rows x 128 bytes
-  static_assert(!kTwo || (FMT == MxFormat::kFp4 && KS == 1 && kGroupWaves % 4 == 0), "4-bit codes on both sides");
-  constexpr uint32_t kWUnits = BN / (kTwo ? 8 : 16), kAUnits = BM / (kTwo ? 8 : 16) * kActUnits<FMT>;
-  constexpr uint32_t kStep = (kWUnits + kAUnits) * kUnit, kStage = KS * kStep;
+  constexpr bool kTwo = MODE == kPair;  // a stage is two steps of every wave
+  static_assert(!kTwo || (FMT == MxFormat::kFp4 && KS == 1), "4-bit codes on both sides");
+  static_assert(KS <= 2);
+  // 4-bit codes of a stage's two steps come in units of 8 rows x 128 bytes,
+  // which all waves share; others in units of 16 rows x 64 bytes per step.
+  constexpr bool kLineW = kTwo || KS == 2, kLineA = kLineW && FMT == MxFormat::kFp4;
+  constexpr uint32_t kWWaves = kLineW ? kWaves : kGroupWaves, kAWaves = kLineA ? kWaves : kGroupWaves;
+  constexpr uint32_t kWUnits = BN / (kLineW ? 8 : 16), kAUnits = kLineA ? BM / 8 : BM / 16 * kActUnits<FMT>;
+  constexpr uint32_t kStage = (kWUnits + (kLineA ? 1 : KS) * kAUnits) * kUnit;
   static_assert((kStage == kStageBytes<FMT, BM, BN, KS, MODE>));
-  static_assert(!GATED || (kWUnits % 2 == 0 && kGroupWaves % 2 == 0 && NT % 2 == 0), "units of the two matrices alternate");
-  constexpr int WU = (kWUnits + kGroupWaves - 1) / kGroupWaves, AU = (kAUnits + kGroupWaves - 1) / kGroupWaves, ND = WU + AU;
+  static_assert(!GATED || (kWUnits % 4 == 0 && kWWaves % 4 == 0 && NT % 2 == 0), "units of the two matrices alternate");
+  static_assert(!kLineW || (kWaves % 2 == 0 && kWUnits % 2 == 0 && kAUnits % 2 == 0), "a wave's units are one half of the row tiles");
+  constexpr int WU = (kWUnits + kWWaves - 1) / kWWaves, AU = (kAUnits + kAWaves - 1) / kAWaves, ND = WU + AU;
   constexpr bool kActScales = FMT != MxFormat::kBf16;
   constexpr uint32_t kMatRows = kMatScaleRows<BN, GATED>, kWsRows = kMatRows * (GATED ? 2 : 1);
   constexpr uint32_t kScaleRows = kAllScaleRows<FMT, BM, BN, GATED>;
@@ -151,32 +156,32 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   constexpr uint32_t kSteps = kTwo ? 2 : KS;  // of a stage
   const uint32_t stages = (steps + kSteps - 1u) / kSteps;
 
-  // transfers of this wave for its group's step: weight units wave, wave +
-  // kGroupWaves, ... and activation units likewise (where they do not come out
-  // even, some are brought twice, the same bytes to the same place: every wave
-  // then has as many transfers in flight as the waits count).  Gated: even units are the gate matrix, odd ones
-  // the up matrix.
-  // Units of two steps: two are a tile of 16 rows, so the matrices alternate by
-  // pairs of units.
-  const bool up = GATED && (kTwo ? wave >> 1 & 1u : wave & 1u);
+  // Transfers of this wave: weight units ww, ww + kWWaves, ... and activation
+  // units likewise (where they do not come out even, some are brought twice, the
+  // same bytes to the same place: every wave then has as many transfers in
+  // flight as the waits count).  Gated: 16-row tiles are of the gate and the up
+  // matrix in turn, and a wave's units all of one.
+  const uint32_t ww = kLineW ? all_wave : wave, aw = kLineA ? all_wave : wave;
+  const bool up = GATED && (kLineW ? ww >> 1 & 1u : ww & 1u);
   const rsrc_t wr = bytes_rsrc(up ? op.WU : op.W, (uint64_t)n0 * wpitch, (nlast + 1u) * wpitch);
   const rsrc_t ar = bytes_rsrc(op.A, (uint64_t)m0 * apitch, mlast * apitch + act_bytes<FMT>(op.K));
-  // this lane's row of a unit (of its 16-row tile) and piece of the row
-  const uint32_t lrow = kTwo ? (wave & 1u) * 8u + (lane >> 3) : lane >> 2;
-  const uint32_t lpiece = kTwo ? ((lane & 7u) ^ pair_turn(lrow)) * 16u : ((lane & 3u) ^ unit_turn(lrow)) * 16u;
-  constexpr uint32_t kPerTile = kTwo ? 2 : 1;  // weight units of a 16-row tile
+  // this lane's row of a 16-row tile and piece of the row
+  const uint32_t line_w = (ww & 1u) * 8u + (lane >> 3), line_a = (aw & 1u) * 8u + (lane >> 3);
+  const uint32_t wrow = kLineW ? line_w : lane >> 2, arow = kLineA ? line_a : lane >> 2;
+  const uint32_t wpiece = (kLineW ? (lane & 7u) ^ pair_turn(wrow) : (lane & 3u) ^ unit_turn(wrow)) * 16u;
+  const uint32_t apiece = (kLineA ? (lane & 7u) ^ pair_turn(arow) : (lane & 3u) ^ unit_turn(arow)) * 16u;
   uint32_t woff[WU], aoff[AU];
 #pragma unroll
   for (int i = 0; i < WU; ++i) {
-    const uint32_t u = (wave + kGroupWaves * i) % kWUnits;
-    const uint32_t row = u / kPerTile / (GATED ? 2u : 1u) * 16u + lrow;
-    woff[i] = (row < nlast ? row : nlast) * wpitch + (kTwo ? 0u : lpiece);
+    const uint32_t u = (ww + kWWaves * i) % kWUnits;
+    const uint32_t row = u / (kLineW ? 2u : 1u) / (GATED ? 2u : 1u) * 16u + wrow;
+    woff[i] = (row < nlast ? row : nlast) * wpitch + (kLineW ? 0u : wpiece);
   }
 #pragma unroll
   for (int i = 0; i < AU; ++i) {
-    const uint32_t u = (wave + kGroupWaves * i) % kAUnits;
-    const uint32_t row = (kTwo ? u / 2u : u / kActUnits<FMT>) * 16u + lrow;
-    aoff[i] = (row < mlast ? row : mlast) * apitch + (kTwo ? 0u : (u % kActUnits<FMT>) * 64u + lpiece);
+    const uint32_t u = (aw + kAWaves * i) % kAUnits;
+    const uint32_t row = u / (kLineA ? 2u : kActUnits<FMT>) * 16u + arow;
+    aoff[i] = (row < mlast ? row : mlast) * apitch + (kLineA ? 0u : (u % kActUnits<FMT>) * 64u + apiece);
   }
   // scale rows 64 p .. 64 p + 63 in transfer p, waves in turn: weights (gated: gate, then up), then activations
   rsrc_t sr[SN];
@@ -191,26 +196,20 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
     soff[i] = (in < last ? in : last) * nb;
   }
 
+  constexpr uint32_t kABase = kWUnits * kUnit;  // of a stage, its weights before it
+  const uint32_t a_group = kABase + (kLineA ? 0u : ks * kAUnits * kUnit);
   auto issue = [&](uint32_t stage, uint32_t buf) __attribute__((always_inline)) {
-    if constexpr (kTwo) {
-      // where the last stage is one step, its pieces are brought twice
-      const uint32_t k = stage * 128u + (stage * 2u + 1u < steps ? lpiece : lpiece & 48u);
+    const uint32_t base = lds0 + buf * kStage;
+    // where the last stage lacks its second step, what is brought of the first
+    // one serves for it; it is not multiplied
+    const uint32_t s = stage * KS + ks < steps ? stage * KS + ks : steps - 1u;
+    const bool whole = stage * 2u + 1u < steps;
+    const uint32_t kw = kLineW ? stage * 128u + (whole ? wpiece : wpiece & 48u) : s * 64u;
+    const uint32_t ka = kLineA ? stage * 128u + (whole ? apiece : apiece & 48u) : s * 64u * kActUnits<FMT>;
 #pragma unroll
-      for (int i = 0; i < WU; ++i)
-        copy_to_lds(lds0 + buf * kStage + (wave + i * kGroupWaves) % kWUnits * kUnit, wr, woff[i] + k);
+    for (int i = 0; i < WU; ++i) copy_to_lds(base + (ww + i * kWWaves) % kWUnits * kUnit, wr, woff[i] + kw);
 #pragma unroll
-      for (int i = 0; i < AU; ++i)
-        copy_to_lds(lds0 + buf * kStage + (kWUnits + (wave + kGroupWaves * i) % kAUnits) * kUnit, ar, aoff[i] + k);
-      return;
-    }
-    uint32_t s = stage * KS + ks;
-    if (KS > 1) s = s < steps ? s : steps - 1u;  // a step too many is brought but not computed
-    const uint32_t base = lds0 + buf * kStage + ks * kStep;
-#pragma unroll
-    for (int i = 0; i < WU; ++i) copy_to_lds(base + (wave + i * kGroupWaves) % kWUnits * kUnit, wr, woff[i] + s * 64u);
-#pragma unroll
-    for (int i = 0; i < AU; ++i)
-      copy_to_lds(base + (kWUnits + (wave + kGroupWaves * i) % kAUnits) * kUnit, ar, aoff[i] + s * 64u * kActUnits<FMT>);
+    for (int i = 0; i < AU; ++i) copy_to_lds(base + a_group + (aw + i * kAWaves) % kAUnits * kUnit, ar, aoff[i] + ka);
   };
   // the 16 scale bytes from step 4q on, or the row's last 16 where fewer are left (nb >= 16)
   auto issue_scales = [&](uint32_t q) __attribute__((always_inline)) {
@@ -253,24 +252,29 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
     }
   };
 
-  // operands of a step from LDS
+  // operands of a step from LDS; h: which of a stage's two steps
   const uint32_t mine = unit_byte(r, g);  // piece g of row r of a unit
-  auto read_w = [&](uint32_t buf, WeightCodes (&w)[NT]) __attribute__((always_inline)) {
-    const uint8_t *p = lds + buf * kStage + ks * kStep + wn * NT * kUnit + mine;
+  auto line_byte = [&](uint32_t h) __attribute__((always_inline)) { return r * 128u + ((h * 4u + g) ^ pair_turn(r)) * 16u; };
+  auto read_w = [&](uint32_t buf, uint32_t h, WeightCodes (&w)[NT]) __attribute__((always_inline)) {
+    constexpr uint32_t kTile = (kLineW ? 2 : 1) * kUnit;  // 16 rows
+    const uint8_t *p = lds + buf * kStage + wn * NT * kTile + (kLineW ? line_byte(h) : mine);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) w[i] = {*reinterpret_cast<const u32x4_t *>(p + i * kUnit), wsc[i]};
+    for (int i = 0; i < NT; ++i) w[i] = {*reinterpret_cast<const u32x4_t *>(p + i * kTile), wsc[i]};
   };
-  auto read_a = [&](uint32_t buf, int j) __attribute__((always_inline)) {
-    const uint8_t *p = lds + buf * kStage + ks * kStep + (kWUnits + wm * MT * kActUnits<FMT>) * kUnit;
+  auto read_a = [&](uint32_t buf, uint32_t h, int j) __attribute__((always_inline)) {
+    constexpr uint32_t kTile = (kLineA ? 2 : kActUnits<FMT>) * kUnit;
+    const uint8_t *p = lds + buf * kStage + a_group + (wm * MT + j) * kTile;
     ActRegs<FMT> a;
     if constexpr (FMT == MxFormat::kBf16) {
 #pragma unroll
-      for (uint32_t h = 0; h < 4; ++h)  // k 32g .. 32g + 31 are the four pieces of unit g
-        a.v[h] = *reinterpret_cast<const u32x4_t *>(p + (j * 4 + g) * kUnit + unit_byte(r, h));
+      for (uint32_t x = 0; x < 4; ++x)  // k 32g .. 32g + 31 are the four pieces of unit g
+        a.v[x] = *reinterpret_cast<const u32x4_t *>(p + g * kUnit + unit_byte(r, x));
+    } else if constexpr (kLineA) {
+      a.v[0] = *reinterpret_cast<const u32x4_t *>(p + line_byte(h));
+      a.s = asc[j];
     } else {
 #pragma unroll
-      for (uint32_t h = 0; h < kActUnits<FMT>; ++h)
-        a.v[h] = *reinterpret_cast<const u32x4_t *>(p + (j * kActUnits<FMT> + h) * kUnit + mine);
+      for (uint32_t x = 0; x < kActUnits<FMT>; ++x) a.v[x] = *reinterpret_cast<const u32x4_t *>(p + x * kUnit + mine);
       a.s = asc[j];
     }
     return a;
@@ -302,9 +306,9 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
           }
           WeightCodes w[NT];
           ActRegs<FMT> a[MT];
-          read_w(buf, w);
+          read_w(buf, 0u, w);
 #pragma unroll
-          for (int j = 0; j < MT; ++j) a[j] = read_a(buf, j);
+          for (int j = 0; j < MT; ++j) a[j] = read_a(buf, 0u, j);
           if constexpr (t == 0) {
             if (s0 + kGroup < stages) issue_scales(s0 / kGroup + 1u);
           }
@@ -348,15 +352,11 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
           mx_unroll<0, 2>([&](auto H) __attribute__((always_inline)) {
             constexpr int h = decltype(H)::value;
             if (h == 0 || s * 2u + 1u < steps) {
-              const uint32_t mine2 = r * 128u + ((h * 4u + g) ^ pair_turn(r)) * 16u;
-              const uint8_t *pw = lds + buf * kStage + wn * NT * 2u * kUnit + mine2;
-              const uint8_t *pa = lds + buf * kStage + (kWUnits + wm * MT * 2u) * kUnit + mine2;
               WeightCodes w[NT];
               ActRegs<FMT> a[MT];
 #pragma unroll
-              for (int j = 0; j < MT; ++j) a[j] = {{*reinterpret_cast<const u32x4_t *>(pa + j * 2 * kUnit)}, asc[kActScales ? j : 0]};
-#pragma unroll
-              for (int i = 0; i < NT; ++i) w[i] = {*reinterpret_cast<const u32x4_t *>(pw + i * 2 * kUnit), wsc[i]};
+              for (int j = 0; j < MT; ++j) a[j] = read_a(buf, h, j);
+              read_w(buf, h, w);
 #pragma unroll
               for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -387,10 +387,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
           if (s + PRE < stages) issue(s + PRE, buf == 0 ? NBUF - 1 : buf - 1);
           if (KS == 1 || s * KS + ks < steps) {
             WeightCodes w[NT];
-            read_w(buf, w);
+            read_w(buf, ks, w);
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
-              const ActRegs<FMT> a = read_a(buf, j);
+              const ActRegs<FMT> a = read_a(buf, ks, j);
 #pragma unroll
               for (int i = 0; i < NT; ++i) acc[i][j] = mx_mfma<FMT, t * KS>(WeightRegs<FMT, t * KS>(w[i]), a, acc[i][j]);
             }
