@@ -226,7 +226,7 @@ int w8a16_gemv_batch16_strided(const void *A, const void *W, const float *S, voi
 #define WQD_MX_MAX_ROWS     (1u << 24)  /* largest M and N of the products */
 #define WQD_MX_NORM_MAX_K   (1u << 15)  /* largest K of add_rmsnorm_mx8 */
 #define WQD_MX_NORM_MAX_M   (1u << 21)  /* largest M of add_rmsnorm_mx8 */
-#define WQD_MX_MAX_VALUES   (1ull << 36) /* largest M * K of mx_quantize and mx_dequantize */
+#define WQD_MX_MAX_VALUES   (1ull << 35) /* largest M * K of mx_quantize and mx_dequantize */
 
 /*
  * mx_quantize - rows of BF16, FP16 or FP32 values to MXFP4 or MXFP8.  Per
