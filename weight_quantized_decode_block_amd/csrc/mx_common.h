@@ -30,13 +30,6 @@ __device__ __forceinline__ void mx_unroll(F &&f) {
   }
 }
 
-__device__ __forceinline__ uint32_t bf16_rne(float f) {
-  uint32_t u = __float_as_uint(f);
-  if ((u & 0x7f800000u) == 0x7f800000u && (u & 0x007fffffu) != 0) return (u >> 16) | 0x40u;
-  u += 0x7fffu + ((u >> 16) & 1u);
-  return u >> 16;
-}
-
 // Two fp32 as BF16, round to nearest even, `a` in the low half
 __device__ __forceinline__ uint32_t bf16x2_rne(float a, float b) {
   typedef float f32x2_t __attribute__((ext_vector_type(2)));

@@ -43,11 +43,25 @@ namespace wqd {
 namespace {
 
 constexpr uint32_t kPastEnd = 0x80000000u;
+// Waves of a workgroup, and segments in flight.  8 x 5120, K = 17408, MXFP8
+// (16 us): 4 or 16 waves, and 1, 3 or 4 segments, are all slower.
+constexpr int NW = 8, DEPTH = 2;
 
+// Bytes of an activation row in a step.
 template <MxFormat FMT>
-constexpr uint32_t kStepBytes = FMT == MxFormat::kBf16 ? 256 : (FMT == MxFormat::kFp8 ? 128 : 64);  // of an activation row
+constexpr uint32_t kStepBytes = FMT == MxFormat::kBf16 ? 256 : (FMT == MxFormat::kFp8 ? 128 : 64);
 
-template <MxFormat FMT, int NW, int MMAX, int NT, bool GATED, int DEPTH>
+// Place of 16-byte piece p of activation row m.  BF16: the row's k block of 32
+// is four pieces, so pieces 4 apart are read together; rows 4-11 turn them among
+// places 0-7 and the others among 8-15.
+template <MxFormat FMT>
+__device__ __forceinline__ uint32_t act_piece(uint32_t m, uint32_t p) {
+  if constexpr (FMT != MxFormat::kBf16) return p;
+  const uint32_t r = m & 15u;
+  return p ^ (r < 4u ? r + 8u : (r < 12u ? r - 4u : r));
+}
+
+template <MxFormat FMT, int MMAX, int NT, bool GATED>
 __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const uint8_t *__restrict__ W,
                                                              const uint8_t *__restrict__ WS,
                                                              const uint8_t *__restrict__ A, uint32_t K, uint32_t M,
@@ -56,14 +70,18 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const uint8_t *__res
                                                              const uint8_t *__restrict__ WUS, MxOut out) {
   constexpr int MT = (MMAX + 15) / 16, G = GATED ? 2 : 1, WT = NT * G;  // 16-row tiles: activations, matrices, weights
   constexpr bool kActScales = FMT != MxFormat::kBf16;
-  constexpr uint32_t kWaves = NW, kThreads = 64 * NW, kRowBytes = NW * kStepBytes<FMT>;  // of a segment's activation row
-  constexpr uint32_t kScaleBytes = 4 * NW;                                               // of a segment's scale row
-  // LDS rows are 16 bytes longer than the segment: the 16 lanes that read the
-  // same piece of 16 rows then use all 64 banks
-  constexpr uint32_t kPitch = kRowBytes + 16, kPieces = kRowBytes / 16;
+  constexpr uint32_t kWaves = NW, kThreads = 64 * NW;
+  constexpr uint32_t kRowBytes = NW * kStepBytes<FMT>;                     // of a segment's activation row
+  constexpr uint32_t kScaleBytes = 4 * NW, kScalePitch = kScaleBytes + 4;  // of a segment's scale row
+  // A 16-byte LDS read serves lanes 0-3, 12-15, 20-27 (then 4-11, 16-19, 28-31)
+  // together: rows 0-3 and 12-15 of one piece and 4-11 of the next k block's.
+  // Quantised rows 32 bytes longer than the segment, and BF16 rows with their
+  // pieces' places turned by the row (act_piece), then meet all 64 banks: 16 x
+  // 17408, K = 5120, MXFP8 16.6 -> 16.3 us against rows 16 bytes longer.
+  constexpr uint32_t kPitch = kRowBytes + (FMT == MxFormat::kBf16 ? 0 : 32), kPieces = kRowBytes / 16;
   constexpr uint32_t kARegion = MMAX * kPitch;
-  constexpr uint32_t kWsRows = 16 * WT, kScaleRows = kWsRows + (kActScales ? MMAX : 0);  // kScaleBytes each
-  constexpr uint32_t kBuffer = kARegion + kScaleRows * kScaleBytes;
+  constexpr uint32_t kWsRows = 16 * WT, kScaleRows = kWsRows + (kActScales ? MMAX : 0);  // kScalePitch each
+  constexpr uint32_t kBuffer = (kARegion + kScaleRows * kScalePitch + 15) / 16 * 16;
   constexpr int SA = (MMAX * kPieces + kThreads - 1) / kThreads, SS = (kScaleRows + 63) / 64;
   constexpr uint32_t kParts = kWaves * WT * MT * 1024;
   constexpr uint32_t kTurn = 2 * kBuffer;  // each wave's own KB per weight tile
@@ -134,7 +152,8 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const uint8_t *__res
     }
 #pragma unroll
     for (int u = 0; u < SS; ++u) {
-      x.s[u] = __builtin_amdgcn_raw_buffer_load_b32(sr[u], i * kScaleBytes + sbyte < nb ? soff[u] + i * kScaleBytes : kPastEnd, 0, 0);
+      const uint32_t b = i * kScaleBytes;
+      x.s[u] = __builtin_amdgcn_raw_buffer_load_b32(sr[u], b + sbyte < nb ? soff[u] + b : kPastEnd, 0, 0);
     }
     return x;
   };
@@ -143,12 +162,14 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const uint8_t *__res
 #pragma unroll
     for (int u = 0; u < SA; ++u) {
       const uint32_t p = tid + (uint32_t)u * kThreads, m = p / kPieces;
-      if (m < (uint32_t)MMAX) *reinterpret_cast<u32x4_t *>(p0 + m * kPitch + (p % kPieces) * 16u) = x.a[u];
+      if (m < (uint32_t)MMAX)
+        *reinterpret_cast<u32x4_t *>(p0 + m * kPitch + act_piece<FMT>(m, p % kPieces) * 16u) = x.a[u];
     }
 #pragma unroll
     for (int u = 0; u < SS; ++u) {
       const uint32_t p = tid + (uint32_t)u * kThreads;
-      if (p < kScaleRows * NW) *reinterpret_cast<uint32_t *>(p0 + kARegion + p * 4u) = x.s[u];
+      if (p < kScaleRows * NW)
+        *reinterpret_cast<uint32_t *>(p0 + kARegion + p / NW * kScalePitch + p % NW * 4u) = x.s[u];
     }
   };
 
@@ -167,7 +188,7 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const uint8_t *__res
 #pragma unroll
     for (int t = 0; t < WT; ++t) {
       w[t].v = *reinterpret_cast<const u32x4_t *>(turn + t * 1024 + unit_byte(r, g));
-      w[t].s = ps[(t * 16u + r) * kScaleBytes];
+      w[t].s = ps[(t * 16u + r) * kScalePitch];
     }
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
@@ -177,11 +198,13 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const uint8_t *__res
       ActRegs<FMT> a;
       if constexpr (FMT == MxFormat::kBf16) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) a.v[h] = *reinterpret_cast<const u32x4_t *>(pa + wave * 256u + g * 64u + h * 16);
+        for (uint32_t h = 0; h < 4; ++h)
+          a.v[h] = *reinterpret_cast<const u32x4_t *>(pa + act_piece<FMT>(m, wave * 16u + g * 4u + h) * 16u);
       } else {
-        a.v[0] = *reinterpret_cast<const u32x4_t *>(pa + wave * (FMT == MxFormat::kFp8 ? 128u : 64u) + g * 16u);
-        if constexpr (FMT == MxFormat::kFp8) a.v[1] = *reinterpret_cast<const u32x4_t *>(pa + wave * 128u + 64u + g * 16u);
-        a.s = ps[(kWsRows + m) * kScaleBytes];
+        a.v[0] = *reinterpret_cast<const u32x4_t *>(pa + wave * kStepBytes<FMT> + g * 16u);
+        if constexpr (FMT == MxFormat::kFp8)
+          a.v[1] = *reinterpret_cast<const u32x4_t *>(pa + wave * 128u + 64u + g * 16u);
+        a.s = ps[(kWsRows + m) * kScalePitch];
       }
 #pragma unroll
       for (int t = 0; t < WT; ++t) acc[t][j] = mx_mfma<FMT>(WeightRegs<FMT>(w[t]), a, acc[t][j]);
@@ -242,14 +265,14 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const uint8_t *__res
   }
 }
 
-template <MxFormat FMT, int NW, int MMAX, int NT, bool GATED, int DEPTH>
+template <MxFormat FMT, int MMAX, int NT, bool GATED>
 hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
   const uint32_t tiles = (op.N + 16u * NT - 1u) / (16u * NT);
   const uint32_t rows = kMxMaxGrid / tiles * MMAX;  // N <= 2^24, so at least one chunk
   for (uint32_t m = 0; m < op.M; m += rows) {
     const MxOperands part = mx_rows(op, FMT, m, rows);
     const uint32_t chunks = (part.M + MMAX - 1u) / MMAX;
-    hipLaunchKernelGGL((mx_skinny_kernel<FMT, NW, MMAX, NT, GATED, DEPTH>), dim3(tiles * chunks), dim3(64 * NW), 0, stream,
+    hipLaunchKernelGGL((mx_skinny_kernel<FMT, MMAX, NT, GATED>), dim3(tiles * chunks), dim3(64 * NW), 0, stream,
                        static_cast<const uint8_t *>(part.W), static_cast<const uint8_t *>(part.WS),
                        static_cast<const uint8_t *>(part.A), part.K, part.M, part.N, part.lda,
                        static_cast<const uint8_t *>(part.AS), static_cast<const uint8_t *>(part.WU),
@@ -260,14 +283,21 @@ hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
   return hipSuccess;
 }
 
+// Activation rows of a workgroup: the least of 2, 4, 8, 16 and 32 that hold M
+// (32 at a time above).  Rows that are not there are staged and multiplied all
+// the same: 1 x 5120, K = 5120, BF16 5.6 us with 2 rows, 8.4 with 16.
+// Weight rows: 16, and from 9 activation rows on 32, over which the activations'
+// pass through LDS is shared (16 rows: 5120 outputs, K = 17408, BF16 30.1 -> 23.3
+// us; 17408 outputs, K = 5120, MXFP8 17.5 -> 16.5).  The gated form already has
+// two matrices' 16 rows; twice that is slower (30.4 against 28.0 us).
 template <MxFormat FMT, bool GATED>
 hipError_t launch_fmt(const MxOperands &op, hipStream_t stream) {
   constexpr int kWide = GATED ? 1 : 2;
-  if (op.M <= 2u) return launch_cfg<FMT, 8, 2, 1, GATED, 2>(op, stream);
-  if (op.M <= 4u) return launch_cfg<FMT, 8, 4, 1, GATED, 2>(op, stream);
-  if (op.M <= 8u) return launch_cfg<FMT, 8, 8, 1, GATED, 2>(op, stream);
-  if (op.M <= 16u) return launch_cfg<FMT, 8, 16, kWide, GATED, 2>(op, stream);
-  return launch_cfg<FMT, 8, 32, kWide, GATED, 2>(op, stream);
+  if (op.M <= 2u) return launch_cfg<FMT, 2, 1, GATED>(op, stream);
+  if (op.M <= 4u) return launch_cfg<FMT, 4, 1, GATED>(op, stream);
+  if (op.M <= 8u) return launch_cfg<FMT, 8, 1, GATED>(op, stream);
+  if (op.M <= 16u) return launch_cfg<FMT, 16, kWide, GATED>(op, stream);
+  return launch_cfg<FMT, 32, kWide, GATED>(op, stream);
 }
 
 }  // namespace

@@ -15,8 +15,8 @@
 //     step are half a 128-byte line per row; where a stage is two steps they are
 //     brought together, 8 rows x 128 bytes a transfer (transfers alone 95
 //     instead of 54 GB/s per compute unit, 128 x 128 tiles of 4-bit codes on
-//     both sides 435 -> 377 ns a step).  Rows past the matrix repeat its last row; their outputs are not
-//     stored.
+//     both sides 435 -> 377 ns a step).  Rows past the matrix repeat its last
+//     row; their outputs are not stored.
 //   * Scales.  16 bytes per row cover four steps; they are staged the same way
 //     one group of four steps ahead.  A wave reads them once per group and
 //     turns them so that byte t of a lane's register is its k block in step t,
@@ -39,8 +39,8 @@
 //
 // What bounds it: with all compute units on random operands the chip lowers its
 // clock (matrix instructions alone reach 4.3 PFLOP/s on FP4 x FP8, 8 on FP4 x
-// FP4, 2.1 on BF16); 4096 x 17408, K = 5120, MXFP8 runs at 2.45 PFLOP/s, 4096 x
-// 5120, K = 5120, MXFP4 at 2.8, 1000 x 5120, K = 17408, BF16 at 1.19.
+// FP4, 2.1 on BF16); 4096 x 17408, K = 5120, MXFP8 runs at 2.56 PFLOP/s, 4096 x
+// 5120, K = 5120, MXFP4 at 3.0, 1000 x 5120, K = 17408, BF16 at 1.18.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -124,8 +124,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   constexpr uint32_t kWUnits = BN / (kLineW ? 8 : 16), kAUnits = kLineA ? BM / 8 : BM / 16 * kActUnits<FMT>;
   constexpr uint32_t kStage = (kWUnits + (kLineA ? 1 : KS) * kAUnits) * kUnit;
   static_assert((kStage == kStageBytes<FMT, BM, BN, KS, MODE>));
-  static_assert(!GATED || (kWUnits % 4 == 0 && kWWaves % 4 == 0 && NT % 2 == 0), "units of the two matrices alternate");
-  static_assert(!kLineW || (kWaves % 2 == 0 && kWUnits % 2 == 0 && kAUnits % 2 == 0), "a wave's units are one half of the row tiles");
+  static_assert(!GATED || (kWUnits % 4 == 0 && kWWaves % 4 == 0 && NT % 2 == 0),
+                "units of the two matrices alternate");
+  static_assert(!kLineW || (kWaves % 2 == 0 && kWUnits % 2 == 0 && kAUnits % 2 == 0),
+                "a wave's units are one half of the row tiles");
   constexpr int WU = (kWUnits + kWWaves - 1) / kWWaves, AU = (kAUnits + kAWaves - 1) / kAWaves, ND = WU + AU;
   constexpr bool kActScales = FMT != MxFormat::kBf16;
   constexpr uint32_t kMatRows = kMatScaleRows<BN, GATED>, kWsRows = kMatRows * (GATED ? 2 : 1);
@@ -513,13 +515,14 @@ struct Cost {
 
 // The kernel for few rows works in tiles of 32 x 32 (gated: 16) and splits K
 // eight ways, so it is ahead while its tiles do not fill the chip: 400 x 512
-// outputs, K = 5120, MXFP8 7.7 us against 10.8 with 64 x 64 tiles, 1000 x 512
+// outputs, K = 5120, MXFP8 7.7 us against 10.8 with 64 x 64 tiles, 800 x 512
 // 14.5 against 11.1.  Larger tiles cost less per output (MXFP8: 64 x 64 51 ns
 // per 1000 outputs and step, 128 x 128 29, 256 x 256 24) and lose by rounds
-// that they do not fill: 4096 x 5120, MXFP4, is 320 tiles of 256 x 256 (two
-// rounds, 94 us) and 512 of 256 x 160 (two rounds, 78 us); 1000 x 5120,
-// K = 17408, MXFP8 one round of 128 x 160 (98 us) or of 80 tiles of 256 x 256
-// (160 us).  So the configuration of the least estimated time is taken.
+// that they do not fill: 4096 x 5120, K = 5120, MXFP4, is 320 tiles of
+// 256 x 256 (two rounds, 94 us) and 1280 of 128 x 128, two to a compute unit
+// (five half rounds, 72 us); 1000 x 5120, K = 17408, MXFP8 one round of
+// 128 x 160 (98 us) or of 80 tiles of 256 x 256 (160 us).  So the configuration
+// of the least estimated time is taken.
 template <MxFormat FMT, bool GATED>
 struct Costs;
 template <>
