@@ -261,7 +261,7 @@ int mx_dequantize(const void *Q, const void *S, uint32_t format, void *Y, uint32
  * add_rmsnorm_mx8 - residual addition, root-mean-square norm and MXFP8 rows:
  *   h = bf16(x + r);  y = h / sqrt(mean_k(h^2) + eps) * g  (fp32);
  *   (Q, S) = y in MXFP8, as mx_quantize rounds it;  Y = bf16(y).
- * The mean is that of the BF16 h; its sum is held in fp32.
+ * The mean is that of the BF16 h; y's arithmetic is fp64, rounded to fp32.
  *
  *   X  device, BF16, row m at X + m * x_row_stride, 16-byte aligned
  *   R  device, BF16 residual rows, pitch r_row_stride, 16-byte aligned; or NULL:
@@ -272,7 +272,8 @@ int mx_dequantize(const void *Q, const void *S, uint32_t format, void *Y, uint32
  *   Y  device, BF16 [M][K], 16-byte aligned; or NULL where only MXFP8 is wanted
  *   Q, S  device, MXFP8 codes (16-byte aligned) and scales of M rows
  *   M  rows (0: nothing is launched), at most WQD_MX_NORM_MAX_M;  K  a
- *      positive multiple of 32, at most WQD_MX_NORM_MAX_K;  strides >= K and multiples of 8;  eps finite, >= 0
+ *      positive multiple of 32, at most WQD_MX_NORM_MAX_K;  strides >= K and
+ *      multiples of 8;  eps finite, >= 0
  */
 int add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *Y, void *Q, void *S,
                     uint32_t M, uint32_t K, uint32_t x_row_stride, uint32_t r_row_stride, float eps,

@@ -215,7 +215,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t *__r
 }
 
 // Groups per thread: two loads in flight per lane where there is work for it on
-// every compute unit (17408 x 5120 to 4 bits 42 us; four 49), one where the call
+// every compute unit (17408 x 5120 to 4 bits 40 us; four 49), one where the call
 // is small and latency counts.
 constexpr uint64_t kManyGroups = 256ull * 4 * 4 * kThreads;
 
@@ -226,10 +226,12 @@ hipError_t quantize_as(const void *X, void *Q, void *S, uint32_t M, uint32_t K, 
   const uint32_t grid = (uint32_t)((groups + kThreads * g - 1) / (kThreads * g));
   if (g == 2)
     hipLaunchKernelGGL((quantize_kernel<T, FP4, 2>), dim3(grid), dim3(kThreads), 0, stream,
-                       static_cast<const uint8_t *>(X), static_cast<uint8_t *>(Q), static_cast<uint8_t *>(S), groups, K, ldx);
+                       static_cast<const uint8_t *>(X), static_cast<uint8_t *>(Q), static_cast<uint8_t *>(S), groups, K,
+                       ldx);
   else
     hipLaunchKernelGGL((quantize_kernel<T, FP4, 1>), dim3(grid), dim3(kThreads), 0, stream,
-                       static_cast<const uint8_t *>(X), static_cast<uint8_t *>(Q), static_cast<uint8_t *>(S), groups, K, ldx);
+                       static_cast<const uint8_t *>(X), static_cast<uint8_t *>(Q), static_cast<uint8_t *>(S), groups, K,
+                       ldx);
   return hipGetLastError();
 }
 
@@ -240,10 +242,12 @@ hipError_t dequantize_as(const void *Q, const void *S, void *Y, uint32_t M, uint
   const uint32_t grid = (uint32_t)((groups + kThreads * g - 1) / (kThreads * g));
   if (g == 2)
     hipLaunchKernelGGL((dequantize_kernel<T, FP4, 2>), dim3(grid), dim3(kThreads), 0, stream,
-                       static_cast<const uint8_t *>(Q), static_cast<const uint8_t *>(S), static_cast<uint8_t *>(Y), groups, K, ldy);
+                       static_cast<const uint8_t *>(Q), static_cast<const uint8_t *>(S), static_cast<uint8_t *>(Y), groups,
+                       K, ldy);
   else
     hipLaunchKernelGGL((dequantize_kernel<T, FP4, 1>), dim3(grid), dim3(kThreads), 0, stream,
-                       static_cast<const uint8_t *>(Q), static_cast<const uint8_t *>(S), static_cast<uint8_t *>(Y), groups, K, ldy);
+                       static_cast<const uint8_t *>(Q), static_cast<const uint8_t *>(S), static_cast<uint8_t *>(Y), groups,
+                       K, ldy);
   return hipGetLastError();
 }
 
@@ -251,10 +255,10 @@ hipError_t dequantize_as(const void *Q, const void *S, void *Y, uint32_t M, uint
 // One workgroup per row; a thread keeps its NCH groups of 8 values in
 // registers between the sum of squares and the scaling, so the row is read
 // once.  h is rounded to BF16 before the sum: the norm is that of the residual
-// stream as the next layer reads it.  The sum and the quotient are held in 64
-// bits: the squares of BF16 values leave fp32's range at either end, and in 32
-// bits the kernel is no faster (4096 x 5120 31.3 against 30.5 us), as memory
-// bounds it (147 MB, 4.8 TB/s).
+// stream as the next layer reads it.  The sum and the products are held in 64
+// bits and y is rounded to fp32 once: the squares of BF16 values leave fp32's
+// range at either end, and in 32 bits the kernel is no faster (4096 x 5120 31.3
+// against 30.5 us), as memory bounds it (147 MB, 4.8 TB/s).
 constexpr uint32_t kNormMaxThreads = 1024;
 
 __device__ __forceinline__ double wave_sum(double x) {
@@ -322,7 +326,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void add_rmsnorm_kernel(const uint
     bf16x8_to_f32(h[u], v);
     bf16x8_to_f32(g[u], w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)((double)v[i] * inv) * w[i];
+    for (int i = 0; i < 8; ++i) v[i] = (float)((double)v[i] * inv * (double)w[i]);
     const uint64_t grp = (uint64_t)row * gpr + c;
     if (Y && c < gpr) store8<Bf16>(Y + grp * 16u, v);
     quantize_store<false>(v, Q, S, grp, c < gpr);
@@ -345,19 +349,25 @@ hipError_t norm_as(const void *X, const void *R, const void *G, void *H, void *Y
 hipError_t launch_mx_quantize(const void *X, uint32_t type, void *Q, void *S, bool fp4, uint32_t M, uint32_t K,
                               uint32_t ldx, hipStream_t stream) {
   if (type == WQD_TYPE_BF16)
-    return fp4 ? quantize_as<Bf16, true>(X, Q, S, M, K, ldx, stream) : quantize_as<Bf16, false>(X, Q, S, M, K, ldx, stream);
+    return fp4 ? quantize_as<Bf16, true>(X, Q, S, M, K, ldx, stream)
+               : quantize_as<Bf16, false>(X, Q, S, M, K, ldx, stream);
   if (type == WQD_TYPE_FP16)
-    return fp4 ? quantize_as<Fp16, true>(X, Q, S, M, K, ldx, stream) : quantize_as<Fp16, false>(X, Q, S, M, K, ldx, stream);
-  return fp4 ? quantize_as<Fp32, true>(X, Q, S, M, K, ldx, stream) : quantize_as<Fp32, false>(X, Q, S, M, K, ldx, stream);
+    return fp4 ? quantize_as<Fp16, true>(X, Q, S, M, K, ldx, stream)
+               : quantize_as<Fp16, false>(X, Q, S, M, K, ldx, stream);
+  return fp4 ? quantize_as<Fp32, true>(X, Q, S, M, K, ldx, stream)
+             : quantize_as<Fp32, false>(X, Q, S, M, K, ldx, stream);
 }
 
 hipError_t launch_mx_dequantize(const void *Q, const void *S, bool fp4, void *Y, uint32_t type, uint32_t M, uint32_t K,
                                 uint32_t ldy, hipStream_t stream) {
   if (type == WQD_TYPE_BF16)
-    return fp4 ? dequantize_as<Bf16, true>(Q, S, Y, M, K, ldy, stream) : dequantize_as<Bf16, false>(Q, S, Y, M, K, ldy, stream);
+    return fp4 ? dequantize_as<Bf16, true>(Q, S, Y, M, K, ldy, stream)
+               : dequantize_as<Bf16, false>(Q, S, Y, M, K, ldy, stream);
   if (type == WQD_TYPE_FP16)
-    return fp4 ? dequantize_as<Fp16, true>(Q, S, Y, M, K, ldy, stream) : dequantize_as<Fp16, false>(Q, S, Y, M, K, ldy, stream);
-  return fp4 ? dequantize_as<Fp32, true>(Q, S, Y, M, K, ldy, stream) : dequantize_as<Fp32, false>(Q, S, Y, M, K, ldy, stream);
+    return fp4 ? dequantize_as<Fp16, true>(Q, S, Y, M, K, ldy, stream)
+               : dequantize_as<Fp16, false>(Q, S, Y, M, K, ldy, stream);
+  return fp4 ? dequantize_as<Fp32, true>(Q, S, Y, M, K, ldy, stream)
+             : dequantize_as<Fp32, false>(Q, S, Y, M, K, ldy, stream);
 }
 
 hipError_t launch_add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *Y, void *Q, void *S,
