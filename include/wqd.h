@@ -214,6 +214,7 @@ int w8a16_gemv_batch16_strided(const void *A, const void *W, const float *S, voi
  *              byte i
  *   WQD_MXFP8  codes uint8 [rows][K]: E4M3FN
  *   scales     uint8 [rows][K/32], for both
+ * Where a call has no rows (M = 0) the operands that hold them may be NULL.
  */
 #define WQD_MXFP4      4
 #define WQD_MXFP8      8

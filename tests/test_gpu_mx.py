@@ -492,3 +492,32 @@ def test_binding_checks_tensors():
         wqd.mx_quantize(x, q, s, "mxfp4", 4, 48)
     assert e.value.code == wqd.WQD_EINVAL
     wqd.mx_quantize(x, q, s, "mxfp4", 4, 64)
+
+
+def test_binding_checks_views():
+    """A view's rows have to lie as far apart as the call reads them."""
+    wide = torch.randn(6, 96, device="cuda").bfloat16()
+    x = wide[:, :64]
+    q, s = torch.zeros(6, 32, dtype=torch.uint8, device="cuda"), torch.zeros(6, 2, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="rows are not 64"):
+        wqd.mx_quantize(x, q, s, "mxfp4", 6, 64)
+    with pytest.raises(ValueError, match="rows are not 32"):
+        wqd.mx_quantize(x, torch.zeros(6, 48, dtype=torch.uint8, device="cuda")[:, :32], s, "mxfp4", 6, 64, x_row_stride=96)
+    with pytest.raises(ValueError, match="rows are not 96"):
+        wqd.mx_quantize(x[:1].expand(6, 64), q, s, "mxfp4", 6, 64, x_row_stride=96)
+    wqd.mx_quantize(x, q, s, "mxfp4", 6, 64, x_row_stride=96)
+    want = ref.quantize(x.double().cpu().numpy(), "mxfp4")
+    assert same(q.cpu().numpy(), want[0]) and same(s.cpu().numpy(), want[1])
+    wqd.mx_quantize(wide.view(2, 3, 96)[:, :, :64], q, s, "mxfp4", 6, 64, x_row_stride=96)
+    assert same(q.cpu().numpy(), want[0])
+
+
+def test_empty_tensors():
+    x, q, s = (torch.zeros(0, n, dtype=t, device="cuda") for n, t in ((128, torch.bfloat16), (128, torch.uint8), (4, torch.uint8)))
+    w, ws = torch.zeros(16, 64, dtype=torch.uint8, device="cuda"), torch.zeros(16, 4, dtype=torch.uint8, device="cuda")
+    c, g = torch.zeros(0, 16, dtype=torch.bfloat16, device="cuda"), torch.zeros(128, dtype=torch.bfloat16, device="cuda")
+    wqd.mx_quantize(x, q, s, "mxfp8", 0, 128)
+    wqd.mx_dequantize(q, s, x, "mxfp8", 0, 128)
+    wqd.add_rmsnorm_mx8(x, x, g, x, x, q, s, 0, 128, 1e-6)
+    wqd.w4a16_gemm(x, w, ws, c, 0, 16, 128)
+    wqd.w4a8_gated(q, s, w, ws, w, ws, c, 0, 16, 128)

@@ -109,6 +109,24 @@ def test_no_rows_is_a_noop(L):
     assert L.add_rmsnorm_mx8(P, P, P, P, P, P, P, 0, 64, 64, 64, 1e-6, None) == wqd.WQD_OK
 
 
+def test_no_rows_need_no_rows_memory(L):
+    """An empty tensor's address is NULL."""
+    for fn in PRODUCTS:
+        assert product(L, fn, PROD | dict(M=0, A=None, AS=None, C=None)) == wqd.WQD_OK
+        assert product(L, fn, PROD | dict(M=0, W=None)) == wqd.WQD_ENULL
+    assert L.mx_quantize(None, 0, None, None, 4, 0, 64, 64, None) == wqd.WQD_OK
+    assert L.mx_dequantize(None, None, 8, None, 2, 0, 64, 64, None) == wqd.WQD_OK
+    assert L.add_rmsnorm_mx8(None, None, P, None, None, None, None, 0, 64, 64, 72, 1e-6, None) == wqd.WQD_OK
+
+
+def test_rows_of_a_view():
+    t = torch.zeros(4, 6, 40)
+    assert wqd._rows_apart(t[:, :, :32], 40) and not wqd._rows_apart(t[:, :, :32], 32)
+    assert not wqd._rows_apart(t[:, :3, :32], 40)  # a gap between the leading dimension's rows
+    assert wqd._rows_apart(t[:, 0, :32], 240) and wqd._rows_apart(t[:1, :3, :32], 40)
+    assert wqd._rows_apart(t[0, :1, :32], 7) and wqd._rows_apart(t[0, 0], 7)  # one row
+
+
 def test_valid_calls_reach_the_device_check(L):
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")

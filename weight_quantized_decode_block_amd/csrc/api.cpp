@@ -137,7 +137,7 @@ int validate_pitches(const char *fn, uint32_t M, uint32_t N, uint32_t K, uint32_
 // pitch, the format, and sizes that one launch covers.
 int validate_mx_rows(const char *fn, const void *V, const char *v_name, uint32_t type, const void *Q, const void *S,
                      uint32_t format, uint32_t M, uint32_t K, uint32_t row_stride) {
-  if (!V || !Q || !S) return fail(WQD_ENULL, "%s: %s, Q and S must be non-NULL", fn, v_name);
+  if (M && (!V || !Q || !S)) return fail(WQD_ENULL, "%s: %s, Q and S must be non-NULL", fn, v_name);
   if (type != WQD_TYPE_BF16 && type != WQD_TYPE_FP16 && type != WQD_TYPE_FP32)
     return fail(WQD_EINVAL, "%s: type %u of %s is not BF16, FP16 or FP32", fn, type, v_name);
   if (format != WQD_MXFP4 && format != WQD_MXFP8)
@@ -159,7 +159,7 @@ int validate_mx_rows(const char *fn, const void *V, const char *v_name, uint32_t
 // kernel.  A BF16 call has no activation scales; a quantised one has pitch K.
 int run_mx_product(const char *fn, wqd::MxOperands op, wqd::MxFormat fmt, bool gated, hipStream_t stream) {
   const bool bf16 = fmt == wqd::MxFormat::kBf16;
-  if (!op.A || !op.W || !op.WS || !op.out.C || (!bf16 && !op.AS) || (gated && (!op.WU || !op.WUS)))
+  if (!op.W || !op.WS || (gated && (!op.WU || !op.WUS)) || (op.M && (!op.A || !op.out.C || (!bf16 && !op.AS))))
     return fail(WQD_ENULL, "%s: operands must be non-NULL", fn);
   if (op.N == 0) return fail(WQD_EINVAL, "%s: N must be >= 1", fn);
   if (op.K == 0 || op.K % 128u != 0) return fail(WQD_EINVAL, "%s: K=%u is not a positive multiple of 128", fn, op.K);
@@ -347,7 +347,7 @@ int mx_dequantize(const void *Q, const void *S, uint32_t format, void *Y, uint32
 int add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *Y, void *Q, void *S, uint32_t M,
                     uint32_t K, uint32_t x_row_stride, uint32_t r_row_stride, float eps, hipStream_t stream) {
   static const char fn[] = "add_rmsnorm_mx8";
-  if (!X || !G || !Q || !S) return fail(WQD_ENULL, "%s: X, G, Q and S must be non-NULL", fn);
+  if (!G || (M && (!X || !Q || !S))) return fail(WQD_ENULL, "%s: X, G, Q and S must be non-NULL", fn);
   if (!R != !H) return fail(WQD_ENULL, "%s: R and H must both be given or both be NULL", fn);
   if (K == 0 || K % WQD_MX_BLOCK != 0) return fail(WQD_EINVAL, "%s: K=%u is not a positive multiple of 32", fn, K);
   if (K > WQD_MX_NORM_MAX_K) return fail(WQD_EUNSUPPORTED, "%s: K=%u above %u", fn, K, (unsigned)WQD_MX_NORM_MAX_K);
@@ -355,7 +355,7 @@ int add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *
   if (x_row_stride < K || x_row_stride % 8u != 0 || (R && (r_row_stride < K || r_row_stride % 8u != 0)))
     return fail(WQD_EINVAL, "%s: row strides %u, %u must be at least K=%u and multiples of 8 (16-byte rows)", fn,
                 x_row_stride, r_row_stride, K);
-  if (H == X && x_row_stride != r_row_stride)
+  if (M && H == X && x_row_stride != r_row_stride)
     return fail(WQD_EINVAL, "%s: H may be X only where their row strides are equal (%u, %u)", fn, x_row_stride,
                 r_row_stride);
   if (!std::isfinite(eps) || eps < 0.0f) return fail(WQD_EINVAL, "%s: eps must be finite and not negative", fn);

@@ -185,11 +185,21 @@ def _span(rows: int, pitch: int, width: int, size: int) -> int:
     return ((rows - 1) * pitch + width) * size if rows > 0 else 0
 
 
-def _arg(fn: str, name: str, x, nbytes: int, device: int, size: int = 1) -> int | None:
+def _rows_apart(x, pitch: int) -> bool:
+    """Whether the rows of x, all its leading dimensions counted through, are `pitch` elements apart."""
+    for n, step in zip(reversed(x.shape[:-1]), reversed(x.stride()[:-1])):
+        if n > 1 and step != pitch:
+            return False
+        pitch *= n
+    return True
+
+
+def _arg(fn: str, name: str, x, nbytes: int, device: int, size: int = 1, pitch: int = 0) -> int | None:
     """Device address of an operand.  A tensor must live on `device`, the current
     one (the call goes to its stream), have `size`-byte elements and its last
     dimension contiguous, and its memory must reach `nbytes` past its first
-    element; an integer is taken as it is."""
+    element; a view with gaps has its rows `pitch` elements apart.  An integer
+    is taken as it is."""
     if x is None or isinstance(x, int):
         return x
     if x.get_device() != device:
@@ -199,6 +209,8 @@ def _arg(fn: str, name: str, x, nbytes: int, device: int, size: int = 1) -> int 
     if x.nbytes < nbytes or not x.is_contiguous():  # perhaps rows of a wider buffer
         if x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
             raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
+        if not x.is_contiguous() and not _rows_apart(x, pitch):
+            raise ValueError(f"{fn}: {name}'s rows are not {pitch} elements apart")
         if x.untyped_storage().nbytes() - x.storage_offset() * x.element_size() < nbytes:
             raise ValueError(f"{fn}: {name} holds fewer than the {nbytes} bytes the call reaches")
     return x.data_ptr()
@@ -257,9 +269,9 @@ def mx_quantize(X, Q, S, fmt, M: int, K: int, x_row_stride: int | None = None, x
     f, t = _mx_format(fn, fmt), _type_of(fn, X, x_type)
     w = 4 if t == TYPE_FP32 else 2
     d, st = _here(stream)
-    _check(fn, (_lib or lib()).mx_quantize(_arg(fn, "X", X, _span(M, ld, K, w), d, w), t,
-                                           _arg(fn, "Q", Q, _code_bytes(f, M * K), d),
-                                           _arg(fn, "S", S, M * K // 32, d), f, M, K, ld, st))
+    _check(fn, (_lib or lib()).mx_quantize(_arg(fn, "X", X, _span(M, ld, K, w), d, w, ld), t,
+                                           _arg(fn, "Q", Q, _code_bytes(f, M * K), d, 1, _code_bytes(f, K)),
+                                           _arg(fn, "S", S, M * K // 32, d, 1, K // 32), f, M, K, ld, st))
 
 
 def mx_dequantize(Q, S, Y, fmt, M: int, K: int, y_row_stride: int | None = None, y_type: int | None = None,
@@ -270,9 +282,9 @@ def mx_dequantize(Q, S, Y, fmt, M: int, K: int, y_row_stride: int | None = None,
     f, t = _mx_format(fn, fmt), _type_of(fn, Y, y_type)
     w = 4 if t == TYPE_FP32 else 2
     d, st = _here(stream)
-    _check(fn, (_lib or lib()).mx_dequantize(_arg(fn, "Q", Q, _code_bytes(f, M * K), d),
-                                             _arg(fn, "S", S, M * K // 32, d), f,
-                                             _arg(fn, "Y", Y, _span(M, ld, K, w), d, w), t,
+    _check(fn, (_lib or lib()).mx_dequantize(_arg(fn, "Q", Q, _code_bytes(f, M * K), d, 1, _code_bytes(f, K)),
+                                             _arg(fn, "S", S, M * K // 32, d, 1, K // 32), f,
+                                             _arg(fn, "Y", Y, _span(M, ld, K, w), d, w, ld), t,
                                              M, K, ld, st))
 
 
@@ -285,10 +297,11 @@ def add_rmsnorm_mx8(X, R, G, H, Y, Q, S, M: int, K: int, eps: float, x_row_strid
     _sizes(fn, M | K | lx | lr)
     rows = _span(M, lr, K, 2)
     d, st = _here(stream)
-    _check(fn, (_lib or lib()).add_rmsnorm_mx8(_arg(fn, "X", X, _span(M, lx, K, 2), d, 2), _arg(fn, "R", R, rows, d, 2),
-                                               _arg(fn, "G", G, 2 * K, d, 2), _arg(fn, "H", H, rows, d, 2),
-                                               _arg(fn, "Y", Y, 2 * M * K, d, 2), _arg(fn, "Q", Q, M * K, d),
-                                               _arg(fn, "S", S, M * K // 32, d), M, K, lx, lr, eps, st))
+    _check(fn, (_lib or lib()).add_rmsnorm_mx8(_arg(fn, "X", X, _span(M, lx, K, 2), d, 2, lx),
+                                               _arg(fn, "R", R, rows, d, 2, lr),
+                                               _arg(fn, "G", G, 2 * K, d, 2), _arg(fn, "H", H, rows, d, 2, lr),
+                                               _arg(fn, "Y", Y, 2 * M * K, d, 2, K), _arg(fn, "Q", Q, M * K, d, 1, K),
+                                               _arg(fn, "S", S, M * K // 32, d, 1, K // 32), M, K, lx, lr, eps, st))
 
 
 def _gemm(call, fn: str, fmt: int | None, A, AS, W, WS, C, M, N, K, lda, ldc, stream) -> None:
@@ -297,12 +310,13 @@ def _gemm(call, fn: str, fmt: int | None, A, AS, W, WS, C, M, N, K, lda, ldc, st
     lda = K if lda is None else lda
     _sizes(fn, M | N | K | lda | ldc)
     d, st = _here(stream)
-    w, ws = _arg(fn, "W", W, N * K // 2, d), _arg(fn, "WS", WS, N * K // 32, d)
-    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, 2)
+    w, ws = _arg(fn, "W", W, N * K // 2, d, 1, K // 2), _arg(fn, "WS", WS, N * K // 32, d, 1, K // 32)
+    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, 2, ldc)
     if fmt is None:
-        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, 2), w, ws, c, M, N, K, lda, ldc, st)
+        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, 2, lda), w, ws, c, M, N, K, lda, ldc, st)
     else:
-        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d), _arg(fn, "AS", AS, M * K // 32, d), w, ws, c, M, N, K,
+        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d, 1, _code_bytes(fmt, K)),
+                  _arg(fn, "AS", AS, M * K // 32, d, 1, K // 32), w, ws, c, M, N, K,
                   ldc, st)
     _check(fn, rc)
 
@@ -313,13 +327,14 @@ def _gated(call, fn: str, fmt: int | None, A, AS, WG, WGS, WU, WUS, C, M, N, K, 
     lda = K if lda is None else lda
     _sizes(fn, M | N | K | lda | ldc)
     d, st = _here(stream)
-    w = (_arg(fn, "WG", WG, N * K // 2, d), _arg(fn, "WGS", WGS, N * K // 32, d),
-         _arg(fn, "WU", WU, N * K // 2, d), _arg(fn, "WUS", WUS, N * K // 32, d))
-    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, 2)
+    w = (_arg(fn, "WG", WG, N * K // 2, d, 1, K // 2), _arg(fn, "WGS", WGS, N * K // 32, d, 1, K // 32),
+         _arg(fn, "WU", WU, N * K // 2, d, 1, K // 2), _arg(fn, "WUS", WUS, N * K // 32, d, 1, K // 32))
+    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, 2, ldc)
     if fmt is None:
-        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, 2), *w, c, M, N, K, lda, ldc, st)
+        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, 2, lda), *w, c, M, N, K, lda, ldc, st)
     else:
-        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d), _arg(fn, "AS", AS, M * K // 32, d), *w, c, M, N, K,
+        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d, 1, _code_bytes(fmt, K)),
+                  _arg(fn, "AS", AS, M * K // 32, d, 1, K // 32), *w, c, M, N, K,
                   ldc, st)
     _check(fn, rc)
 
