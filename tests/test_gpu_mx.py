@@ -521,3 +521,19 @@ def test_empty_tensors():
     wqd.add_rmsnorm_mx8(x, x, g, x, x, q, s, 0, 128, 1e-6)
     wqd.w4a16_gemm(x, w, ws, c, 0, 16, 128)
     wqd.w4a8_gated(q, s, w, ws, w, ws, c, 0, 16, 128)
+
+
+# tiles of 64 x 32 outputs, four groups of waves: whole and part stages of four steps
+NARROW = [(40, 7001, 1152), (47, 5130, 512), (61, 7170, 640), (100, 2100, 896), (128, 4096, 768)]
+
+
+@pytest.mark.parametrize("fmt", ACTS)
+@pytest.mark.parametrize("M,N,K", NARROW)
+def test_narrow_tiles_exact_sums(fmt, M, N, K):
+    test_many_outputs_exact_sums(fmt, M, N, K)
+
+
+@pytest.mark.parametrize("fmt", ACTS)
+@pytest.mark.parametrize("M,N,K", NARROW)
+def test_gated_narrow_tiles(fmt, M, N, K):
+    test_gated_many_outputs(fmt, M, N, K)

@@ -26,9 +26,10 @@
 //     the buffer of the stage before is free.
 //   * Large tiles run the two halves of the waves half a step apart (kHalves):
 //     4096 x 17408, K = 5120, MXFP8 380 -> 312 us; 1000 x 5120, K = 17408, BF16
-//     207 -> 188.  Small tiles, bound by the latency of a step, give alternate
-//     steps to two groups of waves (KS = 2): 64 x 5120, K = 5120, MXFP8 14.8 ->
-//     9.7 us.
+//     207 -> 188.  Small tiles, bound by the latency of a step, give the steps
+//     in turn to two groups of waves (KS = 2): 64 x 5120, K = 5120, MXFP8 14.8 ->
+//     9.7 us, and the narrowest ones, 64 x 32, to four (MXFP8 and MXFP4; of
+//     64 x 64 four are no faster than two).
 //   * BF16 activations: the weights are converted between the matrix
 //     instructions that use them, and 8 waves side by side in n convert each
 //     weight once (the conversions, 7.5 cycles each, otherwise cost as much as
@@ -116,13 +117,14 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   constexpr int NBUF = PRE + 1;
   constexpr bool kTwo = MODE == kPair;  // a stage is two steps of every wave
   static_assert(!kTwo || (FMT == MxFormat::kFp4 && KS == 1), "4-bit codes on both sides");
-  static_assert(KS <= 2);
+  static_assert(KS == 1 || KS == 2 || KS == 4, "a group of four scale bytes is whole stages");
   // 4-bit codes of a stage's two steps come in units of 8 rows x 128 bytes,
   // which all waves share; others in units of 16 rows x 64 bytes per step.
-  constexpr bool kLineW = kTwo || KS == 2, kLineA = kLineW && FMT == MxFormat::kFp4;
-  constexpr uint32_t kWWaves = kLineW ? kWaves : kGroupWaves, kAWaves = kLineA ? kWaves : kGroupWaves;
+  constexpr bool kLineW = kTwo || KS >= 2, kLineA = kLineW && FMT == MxFormat::kFp4;
+  constexpr uint32_t kPairs = KS == 4 ? 2 : 1, kPairWaves = kWaves / kPairs;  // pairs of steps in a stage of lines
+  constexpr uint32_t kWWaves = kLineW ? kPairWaves : kGroupWaves, kAWaves = kLineA ? kPairWaves : kGroupWaves;
   constexpr uint32_t kWUnits = BN / (kLineW ? 8 : 16), kAUnits = kLineA ? BM / 8 : BM / 16 * kActUnits<FMT>;
-  constexpr uint32_t kStage = (kWUnits + (kLineA ? 1 : KS) * kAUnits) * kUnit;
+  constexpr uint32_t kStage = (kPairs * kWUnits + (kLineA ? kPairs : KS) * kAUnits) * kUnit;
   static_assert((kStage == kStageBytes<FMT, BM, BN, KS, MODE>));
   static_assert(!GATED || (kWUnits % 4 == 0 && kWWaves % 4 == 0 && NT % 2 == 0),
                 "units of the two matrices alternate");
@@ -163,7 +165,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   // same bytes to the same place: every wave then has as many transfers in
   // flight as the waits count).  Gated: 16-row tiles are of the gate and the up
   // matrix in turn, and a wave's units all of one.
-  const uint32_t ww = kLineW ? all_wave : wave, aw = kLineA ? all_wave : wave;
+  const uint32_t pair = kPairs == 1 ? 0u : all_wave / kPairWaves, line_wave = all_wave - pair * kPairWaves;
+  const uint32_t ww = kLineW ? line_wave : wave, aw = kLineA ? line_wave : wave;
   const bool up = GATED && (kLineW ? ww >> 1 & 1u : ww & 1u);
   const rsrc_t wr = bytes_rsrc(up ? op.WU : op.W, (uint64_t)n0 * wpitch, (nlast + 1u) * wpitch);
   const rsrc_t ar = bytes_rsrc(op.A, (uint64_t)m0 * apitch, mlast * apitch + act_bytes<FMT>(op.K));
@@ -198,20 +201,25 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
     soff[i] = (in < last ? in : last) * nb;
   }
 
-  constexpr uint32_t kABase = kWUnits * kUnit;  // of a stage, its weights before it
-  const uint32_t a_group = kABase + (kLineA ? 0u : ks * kAUnits * kUnit);
+  // of a stage: its weights (a pair's after the other's), then its activations (of pairs or steps)
+  constexpr uint32_t kABase = kPairs * kWUnits * kUnit;
+  const uint32_t w_group = kPairs == 1 ? 0u : (ks >> 1) * kWUnits * kUnit;  // that this wave multiplies
+  const uint32_t a_group = kABase + (kLineA ? (kPairs == 1 ? 0u : (ks >> 1)) : ks) * kAUnits * kUnit;
+  const uint32_t w_put = pair * kWUnits * kUnit;  // that this wave brings
+  const uint32_t a_put = kLineA ? kABase + pair * kAUnits * kUnit : a_group;
   auto issue = [&](uint32_t stage, uint32_t buf) __attribute__((always_inline)) {
     const uint32_t base = lds0 + buf * kStage;
     // where the last stage lacks its second step, what is brought of the first
     // one serves for it; it is not multiplied
     const uint32_t s = stage * KS + ks < steps ? stage * KS + ks : steps - 1u;
-    const bool whole = stage * 2u + 1u < steps;
-    const uint32_t kw = kLineW ? stage * 128u + (whole ? wpiece : wpiece & 48u) : s * 64u;
-    const uint32_t ka = kLineA ? stage * 128u + (whole ? apiece : apiece & 48u) : s * 64u * kActUnits<FMT>;
+    const uint32_t last = (steps - 1u) >> 1, sp = kPairs == 1 ? stage : (stage * 2u + pair < last ? stage * 2u + pair : last);
+    const bool whole = sp * 2u + 1u < steps;
+    const uint32_t kw = kLineW ? sp * 128u + (whole ? wpiece : wpiece & 48u) : s * 64u;
+    const uint32_t ka = kLineA ? sp * 128u + (whole ? apiece : apiece & 48u) : s * 64u * kActUnits<FMT>;
 #pragma unroll
-    for (int i = 0; i < WU; ++i) copy_to_lds(base + (ww + i * kWWaves) % kWUnits * kUnit, wr, woff[i] + kw);
+    for (int i = 0; i < WU; ++i) copy_to_lds(base + w_put + (ww + i * kWWaves) % kWUnits * kUnit, wr, woff[i] + kw);
 #pragma unroll
-    for (int i = 0; i < AU; ++i) copy_to_lds(base + a_group + (aw + i * kAWaves) % kAUnits * kUnit, ar, aoff[i] + ka);
+    for (int i = 0; i < AU; ++i) copy_to_lds(base + a_put + (aw + i * kAWaves) % kAUnits * kUnit, ar, aoff[i] + ka);
   };
   // the 16 scale bytes from step 4q on, or the row's last 16 where fewer are left (nb >= 16)
   auto issue_scales = [&](uint32_t q) __attribute__((always_inline)) {
@@ -259,7 +267,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   auto line_byte = [&](uint32_t h) __attribute__((always_inline)) { return r * 128u + ((h * 4u + g) ^ pair_turn(r)) * 16u; };
   auto read_w = [&](uint32_t buf, uint32_t h, WeightCodes (&w)[NT]) __attribute__((always_inline)) {
     constexpr uint32_t kTile = (kLineW ? 2 : 1) * kUnit;  // 16 rows
-    const uint8_t *p = lds + buf * kStage + wn * NT * kTile + (kLineW ? line_byte(h) : mine);
+    const uint8_t *p = lds + buf * kStage + w_group + wn * NT * kTile + (kLineW ? line_byte(h) : mine);
 #pragma unroll
     for (int i = 0; i < NT; ++i) w[i] = {*reinterpret_cast<const u32x4_t *>(p + i * kTile), wsc[i]};
   };
@@ -389,10 +397,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
           if (s + PRE < stages) issue(s + PRE, buf == 0 ? NBUF - 1 : buf - 1);
           if (KS == 1 || s * KS + ks < steps) {
             WeightCodes w[NT];
-            read_w(buf, ks, w);
+            read_w(buf, ks & 1u, w);
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
-              const ActRegs<FMT> a = read_a(buf, ks, j);
+              const ActRegs<FMT> a = read_a(buf, ks & 1u, j);
 #pragma unroll
               for (int i = 0; i < NT; ++i) acc[i][j] = mx_mfma<FMT, t * KS>(WeightRegs<FMT, t * KS>(w[i]), a, acc[i][j]);
             }
@@ -516,7 +524,11 @@ struct Cost {
 // The kernel for few rows works in tiles of 32 x 32 (gated: 16) and splits K
 // eight ways, so it is ahead while its tiles do not fill the chip: 400 x 512
 // outputs, K = 5120, MXFP8 7.7 us against 10.8 with 64 x 64 tiles, 800 x 512
-// 14.5 against 11.1.  Larger tiles cost less per output (MXFP8: 64 x 64 51 ns
+// 14.5 against 11.1.  While 64 x 64 tiles leave compute units idle, 64 x 32 ones
+// on twice as many read the weights faster: 64 x 5120, K = 17408, MXFP4 35.6 ->
+// 24.8 us, MXFP8 41.8 -> 34.1, BF16 55.1 -> 46.6; gated 64 x 8192, K = 5120, MXFP8
+// 22.2 -> 18.0; with two rounds of them 128 x 5120, K = 5120, MXFP8 11.2 with
+// 64 x 64 tiles against 16.7.  Larger tiles cost less per output (MXFP8: 64 x 64 51 ns
 // per 1000 outputs and step, 128 x 128 29, 256 x 256 24) and lose by rounds
 // that they do not fill: 4096 x 5120, K = 5120, MXFP4, is 320 tiles of
 // 256 x 256 (two rounds, 94 us) and 1280 of 128 x 128, two to a compute unit
@@ -527,33 +539,34 @@ template <MxFormat FMT, bool GATED>
 struct Costs;
 template <>
 struct Costs<MxFormat::kBf16, false> {
-  static constexpr Cost v[] = {{32, 32, 258, 240, 1},   {64, 64, 461, 420, 1},    {96, 256, 1364, 1310, 1},
-                               {128, 192, 1435, 1350, 1}, {128, 256, 1777, 1620, 1}};
+  static constexpr Cost v[] = {{32, 32, 258, 240, 1},     {64, 32, 390, 390, 1},     {64, 64, 461, 420, 1},
+                               {96, 256, 1364, 1310, 1}, {128, 192, 1435, 1350, 1}, {128, 256, 1777, 1620, 1}};
 };
 template <>
 struct Costs<MxFormat::kBf16, true> {
-  static constexpr Cost v[] = {{32, 16, 258, 240, 1}, {64, 64, 638, 610, 1}, {96, 128, 1364, 1310, 1}, {128, 128, 1777, 1620, 1}};
+  static constexpr Cost v[] = {{32, 16, 258, 240, 1}, {64, 32, 444, 410, 1}, {64, 64, 638, 610, 1},
+                               {96, 128, 1364, 1310, 1}, {128, 128, 1777, 1620, 1}};
 };
 template <>
 struct Costs<MxFormat::kFp8, false> {
-  static constexpr Cost v[] = {{32, 32, 175, 160, 1},   {64, 64, 260, 210, 2},     {128, 128, 649, 470, 2},
-                               {128, 160, 779, 690, 1}, {256, 160, 1191, 1100, 1}, {256, 224, 1509, 1430, 1},
-                               {256, 256, 1685, 1590, 1}};
+  static constexpr Cost v[] = {{32, 32, 175, 160, 1},     {64, 32, 210, 160, 1},     {64, 64, 260, 210, 2},
+                               {128, 128, 649, 470, 2},   {128, 160, 779, 690, 1},   {256, 160, 1191, 1100, 1},
+                               {256, 224, 1509, 1430, 1}, {256, 256, 1685, 1590, 1}};
 };
 template <>
 struct Costs<MxFormat::kFp8, true> {
-  static constexpr Cost v[] = {{32, 16, 175, 160, 1},  {64, 64, 430, 400, 1},    {128, 64, 649, 470, 2},
-                               {192, 128, 1373, 1250, 1}, {256, 128, 1685, 1590, 1}};
+  static constexpr Cost v[] = {{32, 16, 175, 160, 1}, {64, 32, 335, 300, 1},     {64, 64, 430, 400, 1},
+                               {128, 64, 649, 470, 2}, {192, 128, 1373, 1250, 1}, {256, 128, 1685, 1590, 1}};
 };
 template <>
 struct Costs<MxFormat::kFp4, false> {
-  static constexpr Cost v[] = {{32, 32, 140, 115, 1}, {64, 64, 206, 172, 2}, {128, 128, 509, 377, 2},
-                               {256, 192, 1064, 983, 1}, {256, 256, 1289, 1230, 1}};
+  static constexpr Cost v[] = {{32, 32, 140, 115, 1},  {64, 32, 143, 150, 2},    {64, 64, 206, 172, 2},
+                               {128, 128, 509, 377, 2}, {256, 192, 1064, 983, 1}, {256, 256, 1289, 1230, 1}};
 };
 template <>
 struct Costs<MxFormat::kFp4, true> {
-  static constexpr Cost v[] = {{32, 16, 140, 115, 1}, {64, 64, 331, 285, 2}, {128, 64, 509, 377, 2},
-                               {192, 128, 1076, 987, 1}, {256, 128, 1289, 1230, 1}};
+  static constexpr Cost v[] = {{32, 16, 140, 115, 1}, {64, 32, 230, 160, 1},    {64, 64, 331, 285, 2},
+                               {128, 64, 509, 377, 2}, {192, 128, 1076, 987, 1}, {256, 128, 1289, 1230, 1}};
 };
 
 uint64_t cost_of(const Cost &c, const MxOperands &op, uint32_t cus) {
@@ -579,35 +592,41 @@ hipError_t launch_fmt(const MxOperands &op, uint32_t cus, hipStream_t stream) {
   const uint32_t i = pick<FMT, GATED>(op, cus);
   if (i == 0u) return launch_mx_skinny(op, FMT, GATED, stream);
   if constexpr (FMT == MxFormat::kBf16 && GATED) {
-    if (i == 1u) return launch_cfg<FMT, 64, 128, 1, 4, 2, 1, kPlain, GATED>(op, stream);
-    if (i == 2u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 64, 1, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 64, 128, 1, 4, 2, 1, kPlain, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
     return launch_cfg<FMT, 128, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
   } else if constexpr (FMT == MxFormat::kBf16) {
-    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, kPlain, GATED>(op, stream);
-    if (i == 2u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
-    if (i == 3u) return launch_cfg<FMT, 128, 192, 2, 4, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 32, 2, 1, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 4u) return launch_cfg<FMT, 128, 192, 2, 4, 1, 2, kHalves, GATED>(op, stream);
     return launch_cfg<FMT, 128, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
   } else if constexpr (FMT == MxFormat::kFp4 && GATED) {
-    if (i == 1u) return launch_cfg<FMT, 64, 128, 2, 2, 2, 2, kPlain, GATED>(op, stream);
-    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 1, kPair, GATED>(op, stream);
-    if (i == 3u) return launch_cfg<FMT, 192, 256, 4, 2, 1, 1, kPair, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 1, 4, 2, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 64, 128, 2, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 1, kPair, GATED>(op, stream);
+    if (i == 4u) return launch_cfg<FMT, 192, 256, 4, 2, 1, 1, kPair, GATED>(op, stream);
     return launch_cfg<FMT, 256, 256, 4, 2, 1, 1, kPair, GATED>(op, stream);
   } else if constexpr (FMT == MxFormat::kFp4) {
-    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, kPlain, GATED>(op, stream);
-    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 1, kPair, GATED>(op, stream);
-    if (i == 3u) return launch_cfg<FMT, 256, 192, 4, 2, 1, 1, kPair, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 32, 2, 1, 4, 2, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 1, kPair, GATED>(op, stream);
+    if (i == 4u) return launch_cfg<FMT, 256, 192, 4, 2, 1, 1, kPair, GATED>(op, stream);
     return launch_cfg<FMT, 256, 256, 4, 2, 1, 1, kPair, GATED>(op, stream);
   } else if constexpr (GATED) {
-    if (i == 1u) return launch_cfg<FMT, 64, 128, 2, 2, 2, 2, kPlain, GATED>(op, stream);
-    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, kHalves, GATED>(op, stream);
-    if (i == 3u) return launch_cfg<FMT, 192, 256, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 1, 4, 2, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 64, 128, 2, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 4u) return launch_cfg<FMT, 192, 256, 4, 2, 1, 2, kHalves, GATED>(op, stream);
     return launch_cfg<FMT, 256, 256, 4, 2, 1, 2, kHalves, GATED>(op, stream);
   } else {
-    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, kPlain, GATED>(op, stream);
-    if (i == 2u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, kHalves, GATED>(op, stream);
-    if (i == 3u) return launch_cfg<FMT, 128, 160, 4, 2, 1, 2, kHalves, GATED>(op, stream);
-    if (i == 4u) return launch_cfg<FMT, 256, 160, 4, 2, 1, 2, kHalves, GATED>(op, stream);
-    if (i == 5u) return launch_cfg<FMT, 256, 224, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 32, 2, 1, 4, 2, kPlain, GATED>(op, stream);
+    if (i == 2u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 3u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 4u) return launch_cfg<FMT, 128, 160, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 5u) return launch_cfg<FMT, 256, 160, 4, 2, 1, 2, kHalves, GATED>(op, stream);
+    if (i == 6u) return launch_cfg<FMT, 256, 224, 4, 2, 1, 2, kHalves, GATED>(op, stream);
     return launch_cfg<FMT, 256, 256, 4, 2, 1, 2, kHalves, GATED>(op, stream);
   }
 }
