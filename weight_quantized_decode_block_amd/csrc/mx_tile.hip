@@ -591,19 +591,23 @@ template <MxFormat FMT, bool GATED>
 hipError_t launch_fmt(const MxOperands &op, uint32_t cus, hipStream_t stream) {
   const uint32_t i = pick<FMT, GATED>(op, cus);
   if (i == 0u) return launch_mx_skinny(op, FMT, GATED, stream);
+  // The waves of a 64 x 32 tile's group: two for plain products of codes (64 x
+  // 5120, K = 17408, MXFP4 24.7 us, with four 27.0; MXFP8 34.0 either way), four
+  // where a wave has more to convert or multiply (BF16 64 x 5120, K = 5120 14.2 us,
+  // with two 15.3; gated MXFP4 64 x 8192 14.7, with two 15.2).
   if constexpr (FMT == MxFormat::kBf16 && GATED) {
-    if (i == 1u) return launch_cfg<FMT, 64, 64, 1, 2, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, kPlain, GATED>(op, stream);
     if (i == 2u) return launch_cfg<FMT, 64, 128, 1, 4, 2, 1, kPlain, GATED>(op, stream);
     if (i == 3u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
     return launch_cfg<FMT, 128, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
   } else if constexpr (FMT == MxFormat::kBf16) {
-    if (i == 1u) return launch_cfg<FMT, 64, 32, 2, 1, 2, 2, kPlain, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 32, 4, 1, 2, 2, kPlain, GATED>(op, stream);
     if (i == 2u) return launch_cfg<FMT, 64, 64, 2, 2, 2, 2, kPlain, GATED>(op, stream);
     if (i == 3u) return launch_cfg<FMT, 96, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
     if (i == 4u) return launch_cfg<FMT, 128, 192, 2, 4, 1, 2, kHalves, GATED>(op, stream);
     return launch_cfg<FMT, 128, 256, 1, 8, 1, 2, kHalves, GATED>(op, stream);
   } else if constexpr (FMT == MxFormat::kFp4 && GATED) {
-    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 1, 4, 2, kPlain, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 64, 4, 1, 4, 2, kPlain, GATED>(op, stream);
     if (i == 2u) return launch_cfg<FMT, 64, 128, 2, 2, 2, 2, kPlain, GATED>(op, stream);
     if (i == 3u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 1, kPair, GATED>(op, stream);
     if (i == 4u) return launch_cfg<FMT, 192, 256, 4, 2, 1, 1, kPair, GATED>(op, stream);
@@ -615,7 +619,7 @@ hipError_t launch_fmt(const MxOperands &op, uint32_t cus, hipStream_t stream) {
     if (i == 4u) return launch_cfg<FMT, 256, 192, 4, 2, 1, 1, kPair, GATED>(op, stream);
     return launch_cfg<FMT, 256, 256, 4, 2, 1, 1, kPair, GATED>(op, stream);
   } else if constexpr (GATED) {
-    if (i == 1u) return launch_cfg<FMT, 64, 64, 2, 1, 4, 2, kPlain, GATED>(op, stream);
+    if (i == 1u) return launch_cfg<FMT, 64, 64, 4, 1, 4, 2, kPlain, GATED>(op, stream);
     if (i == 2u) return launch_cfg<FMT, 64, 128, 2, 2, 2, 2, kPlain, GATED>(op, stream);
     if (i == 3u) return launch_cfg<FMT, 128, 128, 4, 2, 1, 2, kHalves, GATED>(op, stream);
     if (i == 4u) return launch_cfg<FMT, 192, 256, 4, 2, 1, 2, kHalves, GATED>(op, stream);
