@@ -6,9 +6,9 @@ Quantisation and its inverse are exact.  Tolerances of the others:
     significands fit 24 bits) are within K * 2^-24 * sum |a w| of the exact sum
     in any order; the store adds half a BF16 step, 2^-8 of the value.  Where
     every partial sum is exact in fp32 the outputs equal the rounded exact sums.
-    (On MXFP8 the matrix instruction drops bits far below the largest product of
-    a step, up to 2^-13.9 of the step's sum of |a w| for values of every binade;
-    normal values under a scale per 32 stay within the bound above.)
+    (On MXFP8 the matrix instruction first cuts the products of 8 consecutive k
+    to the grid of the largest, test_gpu_mx_precision.py; normal values under a
+    scale per 32 stay within the bound above.)
   * gated: the two sums as above; |silu'| <= 1.1; silu itself in fp32, its
     exponential within 2^-16 of its value for arguments to 88, so 2^-16 of the
     result; then the store.
