@@ -325,7 +325,8 @@ int w4a4_gemm(const void *A, const void *AS, const void *W, const void *WS, void
  * w4a16_gated, w4a8_gated, w4a4_gated - both projections of a gated
  * feed-forward block and its activation in one launch:
  *   C[m,n] = bf16( silu(sum_k a[m,k] wg[n,k]) * sum_k a[m,k] wu[n,k] ),
- * silu(x) = x / (1 + exp(-x)), sums as above, activation in fp32.  WG, WGS and WU,
+ * silu(x) = x / (1 + exp(-x)), sums as above, activation in fp32 (within 2^-19 of
+ * its value, also where silu alone is below fp32's range).  WG, WGS and WU,
  * WUS are the gate and up matrices [N][K/2] and their scales; the rest is as
  * for the products above.
  */

@@ -9,9 +9,9 @@ Quantisation and its inverse are exact.  Tolerances of the others:
     (On MXFP8 the matrix instruction first cuts the products of 8 consecutive k
     to the grid of the largest, test_gpu_mx_precision.py; normal values under a
     scale per 32 stay within the bound above.)
-  * gated: the two sums as above; |silu'| <= 1.1; silu itself in fp32, its
-    exponential within 2^-16 of its value for arguments to 88, so 2^-16 of the
-    result; then the store.
+  * gated: the two sums as above; |silu'| <= 1.1; silu itself within 2^-16 of the
+    result (test_gpu_mx_gates.py holds it to 2^-19, far gates included); then the
+    store.
   * norm: the squares' sum has at most 8 * 4 + 6 + 16 additions in a chain and
     the rest of y five roundings: 2^-18 of y covers them.
 """

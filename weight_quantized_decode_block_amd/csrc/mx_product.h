@@ -121,9 +121,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *p, uint3
       (int)((rows - 1u) * pitch + bytes), 0x00020000);
 }
 
-// silu(g) * u.  exp(-g) overflows to infinity for g below -88, where the
-// quotient is the correct -0.
-__device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// silu(g) * u, silu(g) = g / (1 + exp(-g)), within 2^-19 of its value.  With e =
+// exp(-|g| / 2) it is g / (1 + e^2) * u, and for negative g (g e) / (1 + e^2) * (u e):
+// nothing overflows, and a factor underflows only where the whole does, so that
+// a silu below fp32's range still meets a large u (exp(-g) itself is an infinity
+// from g = -88.8 on).  e is the square of s = exp(-|g| / 4), which the hardware's
+// exp2 gives for all g that matter; the argument's rounding, which would grow
+// with |g|, goes back in to first order (c).
+__device__ __forceinline__ float silu_times(float g, float u) {
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  const float x = -0.25f * __builtin_fminf(__builtin_fabsf(g), 1024.0f), t = x * kLog2e;
+  const float c = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -t)) * kLn2;
+  float s = __builtin_amdgcn_exp2f(t);
+  s = __builtin_fmaf(s, c, s);
+  const float e = s * s, d = __builtin_amdgcn_rcpf(__builtin_fmaf(e, e, 1.0f));
+  return g < 0.0f ? g * e * d * (u * e) : g * d * u;
+}
 
 // Four consecutive outputs of row m: one 8-byte store where C and its pitch
 // allow it, else one by one; columns past N are not written.
