@@ -171,7 +171,10 @@ def w8a16_gemv_batch16_strided(A, W, S, C, M: int, N: int, K: int, a_row_stride:
 
 # ---------------------------------------------------- microscaled operators
 _MX_FORMATS = {"mxfp4": MXFP4, "mxfp8": MXFP8, MXFP4: MXFP4, MXFP8: MXFP8}
-_types = None
+_types: dict = {}  # torch's types of values: WQD_TYPE_*
+# torch's types that a kind of operand may have: its own, and integers of its size for plain bits (_here fills them)
+_VALUES, _BF16, _SCALES = set(), set(), set()
+_CODES: dict = {MXFP4: set(), MXFP8: set()}
 
 
 def _sizes(fn: str, bits: int) -> None:
@@ -194,18 +197,20 @@ def _rows_apart(x, pitch: int) -> bool:
     return True
 
 
-def _arg(fn: str, name: str, x, nbytes: int, device: int, size: int = 1, pitch: int = 0) -> int | None:
+def _arg(fn: str, name: str, x, nbytes: int, device: int, kind: set, pitch: int = 0) -> int | None:
     """Device address of an operand.  A tensor must live on `device`, the current
-    one (the call goes to its stream), have `size`-byte elements and its last
-    dimension contiguous, and its memory must reach `nbytes` past its first
+    one (the call goes to its stream), be of one of the types of its `kind` and its
+    last dimension contiguous, and its memory must reach `nbytes` past its first
     element; a view with gaps has its rows `pitch` elements apart.  An integer
     is taken as it is."""
     if x is None or isinstance(x, int):
         return x
     if x.get_device() != device:
         raise ValueError(f"{fn}: {name} is not on the current GPU")
-    if x.element_size() != size:
-        raise ValueError(f"{fn}: {name} must have {size}-byte elements")
+    if x.dtype not in kind:
+        size = 2 if kind is _BF16 else 1
+        raise ValueError(f"{fn}: {name} must have {size}-byte elements of type "
+                         f"{', '.join(sorted(str(t)[6:] for t in kind))}, not {str(x.dtype)[6:]}")
     if x.nbytes < nbytes or not x.is_contiguous():  # perhaps rows of a wider buffer
         if x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
             raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
@@ -226,6 +231,12 @@ def _here(stream) -> tuple[int, int | None]:
     global _raw_device, _raw_stream
     if _raw_device is None:
         import torch
+        _types.update({torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32})
+        _VALUES.update(_types)  # mx_quantize and mx_dequantize tell the library which
+        _BF16.update((torch.bfloat16, torch.int16, torch.uint16))
+        _SCALES.update((torch.float8_e8m0fnu, torch.uint8, torch.int8))
+        _CODES[MXFP8].update((torch.float8_e4m3fn, torch.uint8, torch.int8))
+        _CODES[MXFP4].update((torch.float4_e2m1fn_x2, torch.uint8, torch.int8))
         gpu = torch.cuda.is_available()
         if gpu:
             torch.cuda.init()
@@ -237,12 +248,8 @@ def _here(stream) -> tuple[int, int | None]:
 
 def _type_of(fn: str, x, given: int | None) -> int:
     """WQD_TYPE_* of a tensor's values (an address comes with its type)."""
-    global _types
     if isinstance(x, int) or x is None:
         return TYPE_BF16 if given is None else given
-    if _types is None:
-        import torch
-        _types = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}
     t = _types.get(x.dtype)
     if t is None or given not in (None, t):
         raise ValueError(f"{fn}: values must be BF16, FP16 or FP32, as their tensor is ({x.dtype})")
@@ -266,12 +273,12 @@ def mx_quantize(X, Q, S, fmt, M: int, K: int, x_row_stride: int | None = None, x
     type is the tensor's; with an address pass `x_type` (default BF16)."""
     fn, ld = "mx_quantize", K if x_row_stride is None else x_row_stride
     _sizes(fn, M | K | ld)
+    d, st = _here(stream)
     f, t = _mx_format(fn, fmt), _type_of(fn, X, x_type)
     w = 4 if t == TYPE_FP32 else 2
-    d, st = _here(stream)
-    _check(fn, (_lib or lib()).mx_quantize(_arg(fn, "X", X, _span(M, ld, K, w), d, w, ld), t,
-                                           _arg(fn, "Q", Q, _code_bytes(f, M * K), d, 1, _code_bytes(f, K)),
-                                           _arg(fn, "S", S, M * K // 32, d, 1, K // 32), f, M, K, ld, st))
+    _check(fn, (_lib or lib()).mx_quantize(_arg(fn, "X", X, _span(M, ld, K, w), d, _VALUES, ld), t,
+                                           _arg(fn, "Q", Q, _code_bytes(f, M * K), d, _CODES[f], _code_bytes(f, K)),
+                                           _arg(fn, "S", S, M * K // 32, d, _SCALES, K // 32), f, M, K, ld, st))
 
 
 def mx_dequantize(Q, S, Y, fmt, M: int, K: int, y_row_stride: int | None = None, y_type: int | None = None,
@@ -279,12 +286,12 @@ def mx_dequantize(Q, S, Y, fmt, M: int, K: int, y_row_stride: int | None = None,
     """The values of `fmt` rows, in Y's type."""
     fn, ld = "mx_dequantize", K if y_row_stride is None else y_row_stride
     _sizes(fn, M | K | ld)
+    d, st = _here(stream)
     f, t = _mx_format(fn, fmt), _type_of(fn, Y, y_type)
     w = 4 if t == TYPE_FP32 else 2
-    d, st = _here(stream)
-    _check(fn, (_lib or lib()).mx_dequantize(_arg(fn, "Q", Q, _code_bytes(f, M * K), d, 1, _code_bytes(f, K)),
-                                             _arg(fn, "S", S, M * K // 32, d, 1, K // 32), f,
-                                             _arg(fn, "Y", Y, _span(M, ld, K, w), d, w, ld), t,
+    _check(fn, (_lib or lib()).mx_dequantize(_arg(fn, "Q", Q, _code_bytes(f, M * K), d, _CODES[f], _code_bytes(f, K)),
+                                             _arg(fn, "S", S, M * K // 32, d, _SCALES, K // 32), f,
+                                             _arg(fn, "Y", Y, _span(M, ld, K, w), d, _VALUES, ld), t,
                                              M, K, ld, st))
 
 
@@ -297,11 +304,12 @@ def add_rmsnorm_mx8(X, R, G, H, Y, Q, S, M: int, K: int, eps: float, x_row_strid
     _sizes(fn, M | K | lx | lr)
     rows = _span(M, lr, K, 2)
     d, st = _here(stream)
-    _check(fn, (_lib or lib()).add_rmsnorm_mx8(_arg(fn, "X", X, _span(M, lx, K, 2), d, 2, lx),
-                                               _arg(fn, "R", R, rows, d, 2, lr),
-                                               _arg(fn, "G", G, 2 * K, d, 2), _arg(fn, "H", H, rows, d, 2, lr),
-                                               _arg(fn, "Y", Y, 2 * M * K, d, 2, K), _arg(fn, "Q", Q, M * K, d, 1, K),
-                                               _arg(fn, "S", S, M * K // 32, d, 1, K // 32), M, K, lx, lr, eps, st))
+    _check(fn, (_lib or lib()).add_rmsnorm_mx8(_arg(fn, "X", X, _span(M, lx, K, 2), d, _BF16, lx),
+                                               _arg(fn, "R", R, rows, d, _BF16, lr),
+                                               _arg(fn, "G", G, 2 * K, d, _BF16), _arg(fn, "H", H, rows, d, _BF16, lr),
+                                               _arg(fn, "Y", Y, 2 * M * K, d, _BF16, K),
+                                               _arg(fn, "Q", Q, M * K, d, _CODES[MXFP8], K),
+                                               _arg(fn, "S", S, M * K // 32, d, _SCALES, K // 32), M, K, lx, lr, eps, st))
 
 
 def _gemm(call, fn: str, fmt: int | None, A, AS, W, WS, C, M, N, K, lda, ldc, stream) -> None:
@@ -310,13 +318,13 @@ def _gemm(call, fn: str, fmt: int | None, A, AS, W, WS, C, M, N, K, lda, ldc, st
     lda = K if lda is None else lda
     _sizes(fn, M | N | K | lda | ldc)
     d, st = _here(stream)
-    w, ws = _arg(fn, "W", W, N * K // 2, d, 1, K // 2), _arg(fn, "WS", WS, N * K // 32, d, 1, K // 32)
-    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, 2, ldc)
+    w, ws = _arg(fn, "W", W, N * K // 2, d, _CODES[MXFP4], K // 2), _arg(fn, "WS", WS, N * K // 32, d, _SCALES, K // 32)
+    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, _BF16, ldc)
     if fmt is None:
-        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, 2, lda), w, ws, c, M, N, K, lda, ldc, st)
+        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda), w, ws, c, M, N, K, lda, ldc, st)
     else:
-        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d, 1, _code_bytes(fmt, K)),
-                  _arg(fn, "AS", AS, M * K // 32, d, 1, K // 32), w, ws, c, M, N, K,
+        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d, _CODES[fmt], _code_bytes(fmt, K)),
+                  _arg(fn, "AS", AS, M * K // 32, d, _SCALES, K // 32), w, ws, c, M, N, K,
                   ldc, st)
     _check(fn, rc)
 
@@ -327,14 +335,14 @@ def _gated(call, fn: str, fmt: int | None, A, AS, WG, WGS, WU, WUS, C, M, N, K, 
     lda = K if lda is None else lda
     _sizes(fn, M | N | K | lda | ldc)
     d, st = _here(stream)
-    w = (_arg(fn, "WG", WG, N * K // 2, d, 1, K // 2), _arg(fn, "WGS", WGS, N * K // 32, d, 1, K // 32),
-         _arg(fn, "WU", WU, N * K // 2, d, 1, K // 2), _arg(fn, "WUS", WUS, N * K // 32, d, 1, K // 32))
-    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, 2, ldc)
+    w = (_arg(fn, "WG", WG, N * K // 2, d, _CODES[MXFP4], K // 2), _arg(fn, "WGS", WGS, N * K // 32, d, _SCALES, K // 32),
+         _arg(fn, "WU", WU, N * K // 2, d, _CODES[MXFP4], K // 2), _arg(fn, "WUS", WUS, N * K // 32, d, _SCALES, K // 32))
+    c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, _BF16, ldc)
     if fmt is None:
-        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, 2, lda), *w, c, M, N, K, lda, ldc, st)
+        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda), *w, c, M, N, K, lda, ldc, st)
     else:
-        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d, 1, _code_bytes(fmt, K)),
-                  _arg(fn, "AS", AS, M * K // 32, d, 1, K // 32), *w, c, M, N, K,
+        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d, _CODES[fmt], _code_bytes(fmt, K)),
+                  _arg(fn, "AS", AS, M * K // 32, d, _SCALES, K // 32), *w, c, M, N, K,
                   ldc, st)
     _check(fn, rc)
 
