@@ -105,3 +105,65 @@ def test_values_tell_their_type(library, fmt):
     for t in (torch.int16, torch.float64):
         with pytest.raises(ValueError, match="BF16, FP16 or FP32"):
             run("mx_quantize", operands()["mx_quantize " + fmt] | dict(X=z(M, K, t=t)))
+
+
+def pitched(name):
+    """(operand, argument that gives its pitch) of the operands that have one."""
+    if name.startswith("mx_quantize"):
+        yield "X", "x_row_stride"
+    elif name.startswith("mx_dequantize"):
+        yield "Y", "y_row_stride"
+    elif name.startswith("add"):
+        yield from (("X", "x_row_stride"), ("R", "r_row_stride"), ("H", "r_row_stride"))
+    else:
+        yield "C", "c_row_stride"
+        if "a16" in name:
+            yield "A", "a_row_stride"
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_rows_of_wider_tensors(library, name):
+    """A wider tensor passes with its pitch and is refused without it, whether
+    whole or as a view of the rows; so is one of twice the width."""
+    own = operands()[name]
+    given = dict(pitched(name))
+    for k, x in own.items():
+        if not torch.is_tensor(x) or x.dim() < 2:
+            continue
+        width = x.shape[1]
+        for extra in (8, width):
+            wide = torch.zeros(x.shape[0], width + extra, dtype=x.dtype)
+            before = len(library.calls)
+            for t in (wide, wide[:, :width]):
+                with pytest.raises(ValueError, match=f"{k}'s rows are not {width} elements apart"):
+                    run(name, own | {k: t})
+            assert len(library.calls) == before
+            if k in given and not (name.startswith("add") and k != "X"):
+                run(name, own | {k: wide, given[k]: width + extra})
+                run(name, own | {k: wide[:, :width], given[k]: width + extra})
+    if name.startswith("add"):
+        wide = torch.zeros(M, K + 8, dtype=BF)
+        run(name, own | dict(R=wide, H=wide, r_row_stride=K + 8))
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_other_shapes_of_the_same_memory(library, name):
+    """Flat tensors and ones larger than the call reaches, rows in several
+    dimensions or in parts, more rows than the call has, and one row of any width."""
+    own = operands()[name]
+    one = own | dict(M=1)
+    for k, x in own.items():
+        if not torch.is_tensor(x) or x.dim() < 2:
+            continue
+        rows, width = x.shape
+        more = torch.zeros(2 * rows, width, dtype=x.dtype)
+        run(name, own | {k: x.reshape(-1)})
+        run(name, own | {k: more.reshape(-1)[: rows * width + 8]})
+        run(name, own | {k: more})
+        run(name, own | {k: more.reshape(2, rows, width)})
+        run(name, own | {k: x.reshape(rows, 2, -1)})
+        run(name, own | {k: more.reshape(1, -1)})
+        run(name, own | {k: x.reshape(rows // 2, 2 * width)})  # just as large
+        if not k.startswith("W"):
+            run(name, one | {k: torch.zeros(rows, width + 8, dtype=x.dtype)})
+    assert len(library.calls) > 0

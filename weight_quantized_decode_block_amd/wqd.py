@@ -197,12 +197,29 @@ def _rows_apart(x, pitch: int) -> bool:
     return True
 
 
+def _check_rows(fn: str, name: str, x, nbytes: int, pitch: int) -> None:
+    """_arg's checks of a tensor that is not contiguous and just as large as the call reaches."""
+    if x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
+        raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
+    apart = f"{fn}: {name}'s rows are not {pitch} elements apart"
+    whole = x.is_contiguous()
+    if not whole and not _rows_apart(x, pitch):
+        raise ValueError(apart)
+    if x.untyped_storage().nbytes() - x.storage_offset() * x.element_size() < nbytes:
+        raise ValueError(f"{fn}: {name} holds fewer than the {nbytes} bytes the call reaches")
+    if whole and x.dim() > 1 and 0 < pitch < nbytes // x.element_size():  # more than one row
+        if x.numel() != x.shape[-1] and pitch % x.shape[-1]:
+            raise ValueError(apart)
+
+
 def _arg(fn: str, name: str, x, nbytes: int, device: int, kind: set, pitch: int = 0) -> int | None:
     """Device address of an operand.  A tensor must live on `device`, the current
     one (the call goes to its stream), be of one of the types of its `kind` and its
     last dimension contiguous, and its memory must reach `nbytes` past its first
-    element; a view with gaps has its rows `pitch` elements apart.  An integer
-    is taken as it is."""
+    element.  Rows lie `pitch` elements apart: those of a view with gaps, and those
+    of a contiguous tensor that is not just as large as the call reaches, where its
+    last dimension is a row or divides one (flat memory and a single row are any
+    shape).  An integer is taken as it is."""
     if x is None or isinstance(x, int):
         return x
     if x.get_device() != device:
@@ -211,13 +228,9 @@ def _arg(fn: str, name: str, x, nbytes: int, device: int, kind: set, pitch: int 
         size = 2 if kind is _BF16 else 1
         raise ValueError(f"{fn}: {name} must have {size}-byte elements of type "
                          f"{', '.join(sorted(str(t)[6:] for t in kind))}, not {str(x.dtype)[6:]}")
-    if x.nbytes < nbytes or not x.is_contiguous():  # perhaps rows of a wider buffer
-        if x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1:
-            raise ValueError(f"{fn}: {name}'s last dimension must be contiguous")
-        if not x.is_contiguous() and not _rows_apart(x, pitch):
-            raise ValueError(f"{fn}: {name}'s rows are not {pitch} elements apart")
-        if x.untyped_storage().nbytes() - x.storage_offset() * x.element_size() < nbytes:
-            raise ValueError(f"{fn}: {name} holds fewer than the {nbytes} bytes the call reaches")
+    n = x.nbytes
+    if not (x.is_contiguous() and (n == nbytes or (n > nbytes and x.dim() and x.shape[-1] == pitch))):
+        _check_rows(fn, name, x, nbytes, pitch)  # perhaps rows of a wider buffer
     return x.data_ptr()
 
 
@@ -318,14 +331,14 @@ def _gemm(call, fn: str, fmt: int | None, A, AS, W, WS, C, M, N, K, lda, ldc, st
     lda = K if lda is None else lda
     _sizes(fn, M | N | K | lda | ldc)
     d, st = _here(stream)
+    a = (_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda) if fmt is None else
+         _arg(fn, "A", A, _code_bytes(fmt, M * K), d, _CODES[fmt], _code_bytes(fmt, K)))
     w, ws = _arg(fn, "W", W, N * K // 2, d, _CODES[MXFP4], K // 2), _arg(fn, "WS", WS, N * K // 32, d, _SCALES, K // 32)
     c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, _BF16, ldc)
     if fmt is None:
-        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda), w, ws, c, M, N, K, lda, ldc, st)
+        rc = call(a, w, ws, c, M, N, K, lda, ldc, st)
     else:
-        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d, _CODES[fmt], _code_bytes(fmt, K)),
-                  _arg(fn, "AS", AS, M * K // 32, d, _SCALES, K // 32), w, ws, c, M, N, K,
-                  ldc, st)
+        rc = call(a, _arg(fn, "AS", AS, M * K // 32, d, _SCALES, K // 32), w, ws, c, M, N, K, ldc, st)
     _check(fn, rc)
 
 
@@ -335,15 +348,15 @@ def _gated(call, fn: str, fmt: int | None, A, AS, WG, WGS, WU, WUS, C, M, N, K, 
     lda = K if lda is None else lda
     _sizes(fn, M | N | K | lda | ldc)
     d, st = _here(stream)
+    a = (_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda) if fmt is None else
+         _arg(fn, "A", A, _code_bytes(fmt, M * K), d, _CODES[fmt], _code_bytes(fmt, K)))
     w = (_arg(fn, "WG", WG, N * K // 2, d, _CODES[MXFP4], K // 2), _arg(fn, "WGS", WGS, N * K // 32, d, _SCALES, K // 32),
          _arg(fn, "WU", WU, N * K // 2, d, _CODES[MXFP4], K // 2), _arg(fn, "WUS", WUS, N * K // 32, d, _SCALES, K // 32))
     c = _arg(fn, "C", C, _span(M, ldc, N, 2), d, _BF16, ldc)
     if fmt is None:
-        rc = call(_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda), *w, c, M, N, K, lda, ldc, st)
+        rc = call(a, *w, c, M, N, K, lda, ldc, st)
     else:
-        rc = call(_arg(fn, "A", A, _code_bytes(fmt, M * K), d, _CODES[fmt], _code_bytes(fmt, K)),
-                  _arg(fn, "AS", AS, M * K // 32, d, _SCALES, K // 32), *w, c, M, N, K,
-                  ldc, st)
+        rc = call(a, _arg(fn, "AS", AS, M * K // 32, d, _SCALES, K // 32), *w, c, M, N, K, ldc, st)
     _check(fn, rc)
 
 
