@@ -167,3 +167,13 @@ def test_other_shapes_of_the_same_memory(library, name):
         if not k.startswith("W"):
             run(name, one | {k: torch.zeros(rows, width + 8, dtype=x.dtype)})
     assert len(library.calls) > 0
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_part_blocks(library, name):
+    """A K that is not whole blocks has the library's status, whatever the tensors."""
+    for k in (0, 1, 48, K + 8):
+        with pytest.raises(wqd.WqdError, match="multiple of 32") as e:
+            run(name, operands()[name] | dict(K=k))
+        assert e.value.code == wqd.WQD_EINVAL
+    assert not library.calls

@@ -177,10 +177,14 @@ _VALUES, _BF16, _SCALES = set(), set(), set()
 _CODES: dict = {MXFP4: set(), MXFP8: set()}
 
 
-def _sizes(fn: str, bits: int) -> None:
-    """`bits`: the sizes and pitches of a call or-ed together; each must fit the C ABI's 32 bits."""
+def _sizes(fn: str, bits: int, K: int) -> None:
+    """`bits`: the sizes and pitches of a call or-ed together; each must fit the C ABI's 32 bits.
+    A K that is not whole blocks is refused here, with the library's status, as a tensor's rows
+    cannot be held against it."""
     if bits >> 32:
         raise ValueError(f"{fn}: sizes and strides must be from 0 to 2^32 - 1")
+    if K % 32 or not K:
+        raise WqdError(fn, WQD_EINVAL, f"{fn}: K={K} is not a positive multiple of 32")
 
 
 def _span(rows: int, pitch: int, width: int, size: int) -> int:
@@ -285,7 +289,7 @@ def mx_quantize(X, Q, S, fmt, M: int, K: int, x_row_stride: int | None = None, x
     """Rows of X to `fmt` ("mxfp4" or "mxfp8") codes Q and scale bytes S.  The
     type is the tensor's; with an address pass `x_type` (default BF16)."""
     fn, ld = "mx_quantize", K if x_row_stride is None else x_row_stride
-    _sizes(fn, M | K | ld)
+    _sizes(fn, M | K | ld, K)
     d, st = _here(stream)
     f, t = _mx_format(fn, fmt), _type_of(fn, X, x_type)
     w = 4 if t == TYPE_FP32 else 2
@@ -298,7 +302,7 @@ def mx_dequantize(Q, S, Y, fmt, M: int, K: int, y_row_stride: int | None = None,
                   stream=None) -> None:
     """The values of `fmt` rows, in Y's type."""
     fn, ld = "mx_dequantize", K if y_row_stride is None else y_row_stride
-    _sizes(fn, M | K | ld)
+    _sizes(fn, M | K | ld, K)
     d, st = _here(stream)
     f, t = _mx_format(fn, fmt), _type_of(fn, Y, y_type)
     w = 4 if t == TYPE_FP32 else 2
@@ -314,7 +318,7 @@ def add_rmsnorm_mx8(X, R, G, H, Y, Q, S, M: int, K: int, eps: float, x_row_strid
     MXFP8 (Q, S) and, unless Y is None, in BF16."""
     fn = "add_rmsnorm_mx8"
     lx, lr = K if x_row_stride is None else x_row_stride, K if r_row_stride is None else r_row_stride
-    _sizes(fn, M | K | lx | lr)
+    _sizes(fn, M | K | lx | lr, K)
     rows = _span(M, lr, K, 2)
     d, st = _here(stream)
     _check(fn, (_lib or lib()).add_rmsnorm_mx8(_arg(fn, "X", X, _span(M, lx, K, 2), d, _BF16, lx),
@@ -329,7 +333,7 @@ def _gemm(call, fn: str, fmt: int | None, A, AS, W, WS, C, M, N, K, lda, ldc, st
     """A product with MXFP4 weights; fmt is that of the activations, None for BF16 rows of pitch lda."""
     ldc = N if ldc is None else ldc
     lda = K if lda is None else lda
-    _sizes(fn, M | N | K | lda | ldc)
+    _sizes(fn, M | N | K | lda | ldc, K)
     d, st = _here(stream)
     a = (_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda) if fmt is None else
          _arg(fn, "A", A, _code_bytes(fmt, M * K), d, _CODES[fmt], _code_bytes(fmt, K)))
@@ -346,7 +350,7 @@ def _gated(call, fn: str, fmt: int | None, A, AS, WG, WGS, WU, WUS, C, M, N, K, 
     """The same for the pair of products of a gated block."""
     ldc = N if ldc is None else ldc
     lda = K if lda is None else lda
-    _sizes(fn, M | N | K | lda | ldc)
+    _sizes(fn, M | N | K | lda | ldc, K)
     d, st = _here(stream)
     a = (_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda) if fmt is None else
          _arg(fn, "A", A, _code_bytes(fmt, M * K), d, _CODES[fmt], _code_bytes(fmt, K)))
