@@ -24,7 +24,7 @@ class Library:
 @pytest.fixture
 def library(monkeypatch):
     """Host tensors count as the current GPU's, and no library call is made."""
-    wqd._here(0)  # the types' table is filled
+    wqd._here("", 0)  # the types' table is filled
     monkeypatch.setattr(wqd, "_raw_device", lambda: -1)
     monkeypatch.setattr(wqd, "_raw_stream", lambda device: None)
     fake = Library()
@@ -177,3 +177,20 @@ def test_part_blocks(library, name):
             run(name, operands()[name] | dict(K=k))
         assert e.value.code == wqd.WQD_EINVAL
     assert not library.calls
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_streams(library, monkeypatch, name):
+    """A stream of another GPU would run the call there, on this one's memory."""
+    class Stream:
+        def __init__(self, gpu):
+            self.device, self.cuda_stream = torch.device("cuda", gpu), 4096 + gpu
+    monkeypatch.setattr(wqd, "_raw_device", lambda: 1)
+    monkeypatch.setattr(wqd, "_raw_stream", lambda device: 512 + device)
+    addresses = {k: 1 << 20 if torch.is_tensor(x) else x for k, x in operands()[name].items()}
+    for stream, number in ((None, 513), (Stream(1), 4097), (77, 77)):
+        run(name, addresses | dict(stream=stream))
+        assert library.calls[-1][1][-1] == number
+    with pytest.raises(ValueError, match="stream is not the current GPU's"):
+        run(name, addresses | dict(stream=Stream(0)))
+    assert len(library.calls) == 3

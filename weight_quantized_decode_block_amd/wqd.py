@@ -242,9 +242,9 @@ _no_gpu = -2  # no tensor's device
 _raw_device = _raw_stream = None
 
 
-def _here(stream) -> tuple[int, int | None]:
-    """Index of torch's current GPU and the stream of a call: `stream`, or the
-    current one of that GPU."""
+def _here(fn: str, stream) -> tuple[int, int | None]:
+    """Index of torch's current GPU and the stream of a call: `stream`, which must
+    be that GPU's (an integer is taken as it is), or its current one."""
     global _raw_device, _raw_stream
     if _raw_device is None:
         import torch
@@ -260,7 +260,11 @@ def _here(stream) -> tuple[int, int | None]:
         _raw_device = torch._C._cuda_getDevice if gpu else lambda: _no_gpu
         _raw_stream = torch._C._cuda_getCurrentRawStream if gpu else lambda device: None
     device = _raw_device()
-    return device, (_raw_stream(device) if stream is None else _stream(stream))
+    if stream is None:
+        return device, _raw_stream(device)
+    if not isinstance(stream, int) and stream.device.index != device:
+        raise ValueError(f"{fn}: the stream is not the current GPU's")
+    return device, _stream(stream)
 
 
 def _type_of(fn: str, x, given: int | None) -> int:
@@ -290,7 +294,7 @@ def mx_quantize(X, Q, S, fmt, M: int, K: int, x_row_stride: int | None = None, x
     type is the tensor's; with an address pass `x_type` (default BF16)."""
     fn, ld = "mx_quantize", K if x_row_stride is None else x_row_stride
     _sizes(fn, M | K | ld, K)
-    d, st = _here(stream)
+    d, st = _here(fn, stream)
     f, t = _mx_format(fn, fmt), _type_of(fn, X, x_type)
     w = 4 if t == TYPE_FP32 else 2
     _check(fn, (_lib or lib()).mx_quantize(_arg(fn, "X", X, _span(M, ld, K, w), d, _VALUES, ld), t,
@@ -303,7 +307,7 @@ def mx_dequantize(Q, S, Y, fmt, M: int, K: int, y_row_stride: int | None = None,
     """The values of `fmt` rows, in Y's type."""
     fn, ld = "mx_dequantize", K if y_row_stride is None else y_row_stride
     _sizes(fn, M | K | ld, K)
-    d, st = _here(stream)
+    d, st = _here(fn, stream)
     f, t = _mx_format(fn, fmt), _type_of(fn, Y, y_type)
     w = 4 if t == TYPE_FP32 else 2
     _check(fn, (_lib or lib()).mx_dequantize(_arg(fn, "Q", Q, _code_bytes(f, M * K), d, _CODES[f], _code_bytes(f, K)),
@@ -320,7 +324,7 @@ def add_rmsnorm_mx8(X, R, G, H, Y, Q, S, M: int, K: int, eps: float, x_row_strid
     lx, lr = K if x_row_stride is None else x_row_stride, K if r_row_stride is None else r_row_stride
     _sizes(fn, M | K | lx | lr, K)
     rows = _span(M, lr, K, 2)
-    d, st = _here(stream)
+    d, st = _here(fn, stream)
     _check(fn, (_lib or lib()).add_rmsnorm_mx8(_arg(fn, "X", X, _span(M, lx, K, 2), d, _BF16, lx),
                                                _arg(fn, "R", R, rows, d, _BF16, lr),
                                                _arg(fn, "G", G, 2 * K, d, _BF16), _arg(fn, "H", H, rows, d, _BF16, lr),
@@ -334,7 +338,7 @@ def _gemm(call, fn: str, fmt: int | None, A, AS, W, WS, C, M, N, K, lda, ldc, st
     ldc = N if ldc is None else ldc
     lda = K if lda is None else lda
     _sizes(fn, M | N | K | lda | ldc, K)
-    d, st = _here(stream)
+    d, st = _here(fn, stream)
     a = (_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda) if fmt is None else
          _arg(fn, "A", A, _code_bytes(fmt, M * K), d, _CODES[fmt], _code_bytes(fmt, K)))
     w, ws = _arg(fn, "W", W, N * K // 2, d, _CODES[MXFP4], K // 2), _arg(fn, "WS", WS, N * K // 32, d, _SCALES, K // 32)
@@ -351,7 +355,7 @@ def _gated(call, fn: str, fmt: int | None, A, AS, WG, WGS, WU, WUS, C, M, N, K, 
     ldc = N if ldc is None else ldc
     lda = K if lda is None else lda
     _sizes(fn, M | N | K | lda | ldc, K)
-    d, st = _here(stream)
+    d, st = _here(fn, stream)
     a = (_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda) if fmt is None else
          _arg(fn, "A", A, _code_bytes(fmt, M * K), d, _CODES[fmt], _code_bytes(fmt, K)))
     w = (_arg(fn, "WG", WG, N * K // 2, d, _CODES[MXFP4], K // 2), _arg(fn, "WGS", WGS, N * K // 32, d, _SCALES, K // 32),
