@@ -71,12 +71,11 @@ __device__ __forceinline__ rsrc_t bytes_rsrc(const void *p, uint64_t offset, uin
 
 // 16 bytes per lane from voff of the buffer to LDS byte `lds` + 16 * lane.
 // The transfer has no destination registers; it is waited for by count
-// (step_barrier), which the compiler's own waits could not do per buffer.
+// (step_barrier), which the compiler's own waits could not do per buffer.  The
+// LDS address is in m0, which the compiler sets, so that it knows what m0 holds;
+// the transfer wants one instruction between.
 __device__ __forceinline__ void copy_to_lds(uint32_t lds, rsrc_t r, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(lds), "v"(voff), "s"(r)
-               : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "{m0}"(lds), "v"(voff), "s"(r) : "memory");
 }
 
 // Wait until at most N of this wave's transfers are in flight and its LDS
