@@ -242,7 +242,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
   uint32_t wsc[NT], asc[kActScales ? MT : 1];
   auto turn = [&](u32x4_t d, uint32_t shift) __attribute__((always_inline)) {
     const uint32_t lo = __builtin_amdgcn_perm(d.y, d.x, pick), hi = __builtin_amdgcn_perm(d.w, d.z, pick);
-    return (lo | hi << 16) >> shift;
+    return (lo | hi << 16) >> (shift & 31u);  // 32 and more only for a group without a step there
   };
   auto read_scales = [&](uint32_t q) __attribute__((always_inline)) {
     const uint8_t *p = lds + NBUF * kStage + (q & 1u) * kScaleStage;
