@@ -77,7 +77,9 @@ __device__ __forceinline__ f32x4_t mx_mfma(const WeightRegs<FMT, B> &w, const Ac
   }
 }
 
-constexpr uint32_t kMxMaxGrid = 1u << 22;  // workgroups of one launch, which holds fewer than 2^32 threads
+// Workgroups of `threads` threads that one launch may have: half of the 2^32
+// threads that a launch must stay below.
+constexpr uint32_t mx_max_grid(uint32_t threads) { return (1u << 31) / threads; }
 
 // Rows [m, m + rows) of a product.
 inline MxOperands mx_rows(const MxOperands &op, MxFormat fmt, uint32_t m, uint32_t rows) {

@@ -35,6 +35,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/wqd.h"
 #include "mx_common.h"
 #include "mx_product.h"
 #include "wqd_internal.h"
@@ -268,7 +269,9 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const uint8_t *__res
 template <MxFormat FMT, int MMAX, int NT, bool GATED>
 hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
   const uint32_t tiles = (op.N + 16u * NT - 1u) / (16u * NT);
-  const uint32_t rows = kMxMaxGrid / tiles * MMAX;  // N <= 2^24, so at least one chunk
+  constexpr uint32_t kMaxGrid = mx_max_grid(64 * NW);
+  static_assert(kMaxGrid >= WQD_MX_MAX_ROWS / (16u * NT), "a launch holds the widest chunk of rows");
+  const uint32_t rows = kMaxGrid / tiles * MMAX;
   for (uint32_t m = 0; m < op.M; m += rows) {
     const MxOperands part = mx_rows(op, FMT, m, rows);
     const uint32_t chunks = (part.M + MMAX - 1u) / MMAX;

@@ -47,6 +47,7 @@
 
 #include <atomic>
 
+#include "../../include/wqd.h"
 #include "mx_common.h"
 #include "mx_product.h"
 #include "wqd_internal.h"
@@ -500,7 +501,9 @@ hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
   if (attr != hipSuccess) return attr;
   const uint32_t bno = GATED ? BN / 2 : BN;
   const uint32_t tn = (op.N + bno - 1u) / bno;
-  const uint32_t rows = kMxMaxGrid / tn * BM;  // a launch holds fewer than 2^32 threads
+  constexpr uint32_t kMaxGrid = mx_max_grid(64 * WM * WN * KS);
+  static_assert(kMaxGrid >= WQD_MX_MAX_ROWS / (GATED ? BN / 2 : BN), "a launch holds the widest row of tiles");
+  const uint32_t rows = kMaxGrid / tn * BM;
   for (uint32_t m = 0; m < op.M; m += rows) {
     const MxOperands part = mx_rows(op, FMT, m, rows);
     const uint32_t grid = tn * ((part.M + BM - 1u) / BM);
