@@ -12,8 +12,9 @@ Quantisation and its inverse are exact.  Tolerances of the others:
   * gated: the two sums as above; |silu'| <= 1.1; silu itself within 2^-16 of the
     result (test_gpu_mx_gates.py holds it to 2^-19, far gates included); then the
     store.
-  * norm: the squares' sum has at most 8 * 4 + 6 + 16 additions in a chain and
-    the rest of y five roundings: 2^-18 of y covers them.
+  * norm: y is computed in 64 bits and rounded to fp32 once, 2^-24; check_norm's
+    2^-18 leaves room for 32-bit sums (test_gpu_mx_paths.py holds it to the one
+    rounding).
 """
 import numpy as np
 import pytest
@@ -261,8 +262,9 @@ def test_product_exact_sums(fmt, M, N, K):
 
 
 # The tile sizes are chosen by M, N and the format (csrc/mx_tile.hip, Costs): with 256 compute units these
-# outputs meet every one of them, for products and gated pairs of each format, with ragged last tiles; the
-# K have 4, 5, 6, 7 and 9 steps of 128, so the last group of four is full and partial, pairs whole and half.
+# outputs, those of NARROW below and of test_gpu_mx_paths.py meet every one of them, for products and gated
+# pairs of each format (test_mx_paths.py checks that), with ragged last tiles; the K have 4, 5, 6, 7 and 9
+# steps of 128, so the last group of four is full and partial, pairs whole and half.
 MANY = [(33, 4164, 640), (65, 12493, 512), (65, 16714, 896), (67, 8321, 1152), (98, 16549, 768), (130, 16408, 640),
         (132, 13672, 512), (257, 13829, 896), (293, 16391, 640), (385, 12515, 1152), (397, 16447, 640),
         (482, 10850, 768), (528, 16458, 512), (645, 16512, 896), (781, 14341, 640)]
