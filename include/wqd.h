@@ -251,8 +251,9 @@ int mx_quantize(const void *X, uint32_t x_type, void *Q, void *S, uint32_t forma
 
 /*
  * mx_dequantize - the values of MXFP4 or MXFP8 rows: code * 2^(s - 127) in
- * fp32, rounded to nearest even to y_type (exact in FP32, and in BF16 but for
- * values beyond its range).  Arguments as for mx_quantize; Y is 16-byte
+ * fp32, rounded to nearest even to y_type.  Exact in FP32 and BF16 but for values
+ * beyond their range: 2^128 and more are infinities, and BF16 has no bits below
+ * 2^-133.  Arguments as for mx_quantize; Y is 16-byte
  * aligned and its pitch whole 16-byte pieces; padding is not written.
  */
 int mx_dequantize(const void *Q, const void *S, uint32_t format, void *Y, uint32_t y_type,
@@ -309,6 +310,11 @@ int add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *
  * the sum: where a sum cancels it can be more than the output's own rounding.
  * The groups' sums add in fp32.  4-bit activations lose nothing so (products of
  * their codes are within 9 exponents), BF16 ones no more than fp32 does.
+ *
+ * BF16 activations: the weights enter as BF16 values, so those of 2^128 and more
+ * (codes of 4 and 6 under scale byte 253, of 2 and more under 254; mx_quantize
+ * writes neither) are infinities, as mx_dequantize has them.  The other forms
+ * apply the scales to the products.
  *
  * A NaN or infinity in an activation row, or a scale of 255, reaches that
  * row's (column's) outputs only.  The same call gives the same bits each time;

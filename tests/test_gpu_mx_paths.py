@@ -130,3 +130,27 @@ def test_norm_of_far_values(M):
     for eps in (0.0, 1e-6):
         got = norm_gpu(X, None, G, M, K, eps)
         check_rounded_once(X, None, G, K, eps, got)
+
+
+@pytest.mark.parametrize("M,N", [(2, 16), (64, 6000)])
+@pytest.mark.parametrize("fmt", ACTS)
+def test_weights_beyond_bf16(fmt, M, N):
+    """Scale bytes 253 and 254 over every code, activations of 2^-100: quantised
+    ones give the finite products, BF16 ones take weights of 2^128 and more as
+    infinities."""
+    K = 512
+    w, ws = np.zeros((N, K // 2), np.uint8), np.full((N, K // 32), 127, np.uint8)
+    w[:, 16] = np.arange(N) % 8  # k 32
+    ws[:, 1] = np.where(np.arange(N) % 16 < 8, 253, 254)
+    if fmt == "bf16":
+        a, s = np.zeros((M, K)), None
+        a[:, 32] = 2.0 ** -100
+        a = gen.bf16_bits(a)
+    else:
+        a = np.zeros((M, K if fmt == "mxfp8" else K // 2), np.uint8)
+        a[:, 32 if fmt == "mxfp8" else 16] = 0x38 if fmt == "mxfp8" else 2
+        s = np.full((M, K // 32), 27, np.uint8)
+    c = gen.bf16_values(product_gpu(fmt, a, s, (w, ws), N, K)).astype(np.float64)
+    v = ref.values(w, ws, "mxfp4")[:, 32]
+    want = np.where(v >= 2.0 ** 128, np.inf, v * 2.0 ** -100) if fmt == "bf16" else v * 2.0 ** -100
+    assert np.array_equal(c, np.resize(want, (M, N)))
