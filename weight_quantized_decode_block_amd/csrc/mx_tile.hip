@@ -27,9 +27,9 @@
 //   * Large tiles run the two halves of the waves half a step apart (kHalves):
 //     4096 x 17408, K = 5120, MXFP8 380 -> 312 us; 1000 x 5120, K = 17408, BF16
 //     207 -> 188.  Small tiles, bound by the latency of a step, give the steps
-//     in turn to two groups of waves (KS = 2): 64 x 5120, K = 5120, MXFP8 14.8 ->
-//     9.7 us, and the narrowest ones, 64 x 32, to four (MXFP8 and MXFP4; of
-//     64 x 64 four are no faster than two).
+//     in turn to two groups of waves (KS = 2): tiles of 64 x 64 over 64 x 5120, K =
+//     5120, MXFP8 14.8 -> 9.7 us; the narrowest ones, 64 x 32, which serve that
+//     size now, to four (MXFP8 and MXFP4; of 64 x 64 four are no faster than two).
 //   * BF16 activations: the weights are converted between the matrix
 //     instructions that use them, and 8 waves side by side in n convert each
 //     weight once (the conversions, 7.5 cycles each, otherwise cost as much as
@@ -40,8 +40,10 @@
 //
 // What bounds it: with all compute units on random operands the chip lowers its
 // clock (matrix instructions alone reach 4.3 PFLOP/s on FP4 x FP8, 8 on FP4 x
-// FP4, 2.1 on BF16); 4096 x 17408, K = 5120, MXFP8 runs at 2.56 PFLOP/s, 4096 x
-// 5120, K = 5120, MXFP4 at 3.0, 1000 x 5120, K = 17408, BF16 at 1.18.
+// FP4, 2.1 on BF16); 4096 x 17408, K = 5120, MXFP8 runs at 2.53 PFLOP/s, 4096 x
+// 5120, K = 5120, MXFP4 at 3.0, 1000 x 5120, K = 17408, BF16 at 1.17.  64 rows are
+// bound by the latency of their steps (64 x 5120, K = 17408: matrix units 12 to 19
+// % busy, weights read at 1.2 to 2.7 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -578,7 +580,10 @@ uint64_t cost_of(const Cost &c, const MxOperands &op, uint32_t cus) {
 }
 
 // The index of the least cost; 0, the kernel for few rows, up to 32 rows (its
-// own row tiles) and for K below the four steps that scales are staged in.
+// own row tiles) and for K below the four steps that scales are staged in here.
+// There the few-row kernel is all there is, and many rows are slow in it: 4096 x
+// 17408, K = 256, BF16 1036 us, MXFP8 722, MXFP4 350, with K = 512 in tiles 101,
+// 65 and 54 us.
 template <MxFormat FMT, bool GATED>
 uint32_t pick(const MxOperands &op, uint32_t cus) {
   using C = Costs<FMT, GATED>;
