@@ -21,7 +21,7 @@ def costs(fmt, gated):
 
 
 def pick(table, M, N, K):
-    if M <= 32 or K < 512:
+    if M <= 32:
         return 0
 
     def cost(c):
@@ -41,7 +41,7 @@ def launches(fmt, gated):
 
 
 def shapes_of(gated):
-    both = base.MANY + base.NARROW + paths.FEW + paths.SHORT + paths.LARGE + paths.THIN
+    both = base.MANY + base.NARROW + paths.FEW + paths.SHORT + paths.SHORT_TILES + paths.LARGE + paths.THIN
     if not gated:
         return {f: both + base.SHAPES for f in FMT}
     return {f: both + (paths.GATED_64 if f == "mxfp8" else []) for f in FMT}
@@ -60,7 +60,8 @@ def test_every_kernel_is_tested(fmt, gated):
         assert len(shapes) >= 2, (fmt, gated, tile, shapes)
         if i:  # outputs in part tiles; a last group of four steps in part
             assert any(M % tile[0] and N % tile[1] for M, N, _ in shapes), (fmt, gated, tile, shapes)
-            assert any(K // 128 % 4 for _, _, K in shapes), (fmt, gated, tile, shapes)
+            assert any(K // 128 % 4 for _, _, K in shapes if K > 512), (fmt, gated, tile, shapes)
+            assert {128, 384} <= {K for _, _, K in shapes}, (fmt, gated, tile, shapes)
 
 
 def test_every_height_of_the_few_row_kernel_is_tested():

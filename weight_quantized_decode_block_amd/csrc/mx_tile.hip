@@ -18,7 +18,8 @@
 //     both sides 435 -> 377 ns a step).  Rows past the matrix repeat its last
 //     row; their outputs are not stored.
 //   * Scales.  16 bytes per row cover four steps; they are staged the same way
-//     one group of four steps ahead.  A wave reads them once per group and
+//     one group of four steps ahead (of K below 512, whose rows of scales are
+//     shorter, before the first step).  A wave reads them once per group and
 //     turns them so that byte t of a lane's register is its k block in step t,
 //     which the matrix instruction's byte select takes directly.
 //   * A wave waits for its own transfers of a stage (later ones stay in flight)
@@ -111,7 +112,10 @@ constexpr uint32_t lds_bytes() {
   return (PRE + 1) * kStageBytes<FMT, BM, BN, KS, MODE> + 2 * kAllScaleRows<FMT, BM, BN, GATED> * 16;
 }
 
-template <MxFormat FMT, int BM, int BN, int WM, int WN, int KS, int PRE, int MODE, bool GATED>
+// SHORT: K below the four steps that scales are staged in.  A kernel of its own:
+// with the choice made inside it, the schedule of the others changes (1000 x 5120,
+// K = 17408, BF16 150 -> 152 us).
+template <MxFormat FMT, int BM, int BN, int WM, int WN, int KS, int PRE, int MODE, bool GATED, bool SHORT>
 __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands op) {
   static_assert(MODE != kHalves || (KS == 1 && WM * WN == 8), "two waves per SIMD");
   constexpr uint32_t kGroupWaves = WM * WN, kWaves = kGroupWaves * KS;
@@ -233,6 +237,20 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
     }
   };
 
+  // the same of rows of 4, 8 or 12 bytes: step by step through registers, to the
+  // end of their 16
+  [[maybe_unused]] auto put_short_scales = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < SN; ++i) {
+      const uint32_t p = all_wave + (uint32_t)i * kWaves;
+      if (p >= kScaleRows / 64u) continue;
+      const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(
+          reinterpret_cast<void *>((uint64_t)sr[i].y << 32 | sr[i].x), (short)0, (int)sr[i].z, 0x00020000);
+      uint32_t *to = reinterpret_cast<uint32_t *>(lds + NBUF * kStage + p * kUnit + lane * 16u) + 4u - steps;
+      for (uint32_t t = 0; t < steps; ++t) to[t] = __builtin_amdgcn_raw_buffer_load_b32(from, soff[i] + 4u * t, 0, 0);
+    }
+  };
+
   const uint32_t wm = wave / WN, wn = wave % WN;  // this wave's part of the tile
   f32x4_t acc[NT][MT];
 #pragma unroll
@@ -292,7 +310,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mx_tile_kernel(MxOperands o
     return a;
   };
 
-  issue_scales(0);
+  if constexpr (SHORT)
+    put_short_scales();
+  else
+    issue_scales(0);
   mx_unroll<0, PRE>([&](auto d) __attribute__((always_inline)) {
     constexpr uint32_t s = decltype(d)::value;
     if (s < stages) issue(s, s);
@@ -495,11 +516,13 @@ hipError_t allow_lds(const void *kern, std::atomic<uint64_t> &ready) {
 
 template <MxFormat FMT, int BM, int BN, int WM, int WN, int KS, int PRE, int MODE, bool GATED>
 hipError_t launch_cfg(const MxOperands &op, hipStream_t stream) {
-  constexpr auto kern = mx_tile_kernel<FMT, BM, BN, WM, WN, KS, PRE, MODE, GATED>;
+  const bool short_k = op.K < 512u;
+  const auto kern = short_k ? mx_tile_kernel<FMT, BM, BN, WM, WN, KS, PRE, MODE, GATED, true>
+                            : mx_tile_kernel<FMT, BM, BN, WM, WN, KS, PRE, MODE, GATED, false>;
   constexpr uint32_t kLds = lds_bytes<FMT, BM, BN, KS, PRE, MODE, GATED>();
   static_assert(kLds <= 160 * 1024, "one workgroup's LDS");
-  static std::atomic<uint64_t> ready;  // devices on which the kernel may use that much LDS
-  const hipError_t attr = allow_lds(reinterpret_cast<const void *>(kern), ready);
+  static std::atomic<uint64_t> ready[2];  // devices on which the kernel may use that much LDS
+  const hipError_t attr = allow_lds(reinterpret_cast<const void *>(kern), ready[short_k]);
   if (attr != hipSuccess) return attr;
   const uint32_t bno = GATED ? BN / 2 : BN;
   const uint32_t tn = (op.N + bno - 1u) / bno;
@@ -580,14 +603,15 @@ uint64_t cost_of(const Cost &c, const MxOperands &op, uint32_t cus) {
 }
 
 // The index of the least cost; 0, the kernel for few rows, up to 32 rows (its
-// own row tiles) and for K below the four steps that scales are staged in here.
-// There the few-row kernel is all there is, and many rows are slow in it: 4096 x
-// 17408, K = 256, BF16 1036 us, MXFP8 722, MXFP4 350, with K = 512 in tiles 101,
-// 65 and 54 us.
+// own row tiles).  The costs of a step serve K below 512 too, where the few-row
+// kernel leaves five to seven of its eight waves without a step: from 33 x 512 to
+// 4096 x 17408 outputs the choice was never more than 5 % behind it, and ahead
+// wherever it takes tiles (64 x 5120, K = 256, BF16 9.5 -> 4.2 us; 4096 x 17408
+// 1035 -> 80, MXFP8 719 -> 58, MXFP4 349 -> 48).
 template <MxFormat FMT, bool GATED>
 uint32_t pick(const MxOperands &op, uint32_t cus) {
   using C = Costs<FMT, GATED>;
-  if (op.M <= 32u || op.K < 512u) return 0u;
+  if (op.M <= 32u) return 0u;
   uint32_t best = 0;
   for (uint32_t i = 1; i < sizeof(C::v) / sizeof(Cost); ++i)
     if (cost_of(C::v[i], op, cus) < cost_of(C::v[best], op, cus)) best = i;
