@@ -188,9 +188,10 @@ def test_streams(library, monkeypatch, name):
     monkeypatch.setattr(wqd, "_raw_device", lambda: 1)
     monkeypatch.setattr(wqd, "_raw_stream", lambda device: 512 + device)
     addresses = {k: 1 << 20 if torch.is_tensor(x) else x for k, x in operands()[name].items()}
-    for stream, number in ((None, 513), (Stream(1), 4097), (77, 77)):
+    bare = type("Bare", (), {"cuda_stream": 99})()
+    for stream, number in ((None, 513), (Stream(1), 4097), (77, 77), (bare, 99)):
         run(name, addresses | dict(stream=stream))
         assert library.calls[-1][1][-1] == number
     with pytest.raises(ValueError, match="stream is not the current GPU's"):
         run(name, addresses | dict(stream=Stream(0)))
-    assert len(library.calls) == 3
+    assert len(library.calls) == 4

@@ -244,7 +244,8 @@ _raw_device = _raw_stream = None
 
 def _here(fn: str, stream) -> tuple[int, int | None]:
     """Index of torch's current GPU and the stream of a call: `stream`, which must
-    be that GPU's (an integer is taken as it is), or its current one."""
+    be that GPU's (an integer, or an object that names no GPU, is taken as it is),
+    or its current one."""
     global _raw_device, _raw_stream
     if _raw_device is None:
         import torch
@@ -262,8 +263,10 @@ def _here(fn: str, stream) -> tuple[int, int | None]:
     device = _raw_device()
     if stream is None:
         return device, _raw_stream(device)
-    if not isinstance(stream, int) and stream.device.index != device:
-        raise ValueError(f"{fn}: the stream is not the current GPU's")
+    if not isinstance(stream, int):
+        gpu = getattr(getattr(stream, "device", None), "index", None)
+        if gpu not in (None, device):
+            raise ValueError(f"{fn}: the stream is not the current GPU's")
     return device, _stream(stream)
 
 
