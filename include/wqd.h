@@ -344,6 +344,135 @@ int w4a8_gated(const void *A, const void *AS, const void *WG, const void *WGS, c
 int w4a4_gated(const void *A, const void *AS, const void *WG, const void *WGS, const void *WU, const void *WUS,
                void *C, uint32_t M, uint32_t N, uint32_t K, uint32_t c_row_stride, hipStream_t stream);
 
+/* ----------------------------------- 4-bit integer weights, routed experts */
+
+/*
+ * A matrix of 4-bit integer weights:
+ *   w[n,k] = (q[n,k] - z[n,k/group]) * s[n,k/group],
+ *   q  codes 0 .. 15;  s  FP16 or BF16 [N][K/group];  z  uint8 [N][K/group], or
+ *   NULL: 8 everywhere;  group  32, 64 or 128.
+ * Scales and zero points lie row by row; the codes are laid out once, by
+ * i4_pack, in tiles of 16 rows x 128 k (rows padded to whole tiles):
+ *   uint8 [ceil(N/16)][K/128][1024]; byte 256 g + 16 n + 4 j + b of a tile (g, j, b
+ *   0 .. 3, n 0 .. 15) holds the codes of row n of the tile at k = 32 j + 8 g + i, for
+ *   b = 0 .. 3 of i = 0 and 2, 4 and 6, 1 and 3, 5 and 7, the first in the low nibble.
+ * Several matrices of one size (experts) lie one after another: codes at
+ * i4_packed_bytes(N, K) apart, scales and zero points [E][N][K/group].
+ *
+ * i4_pack - codes of `count` matrices, uint8 [count][N][K/2] with the even k in
+ * the low nibble (4-byte aligned), to that layout in W (16-byte aligned,
+ * count * i4_packed_bytes(N, K) bytes; not Q).
+ */
+int i4_pack(const void *Q, void *W, uint32_t N, uint32_t K, uint32_t count, hipStream_t stream);
+
+/* Bytes of a matrix's laid-out codes: ceil(N/16) * 16 * K/2, or 0 if K % 128 != 0. */
+size_t i4_packed_bytes(uint32_t N, uint32_t K);
+
+/*
+ * i4a16_gemm, i4a16_gated - products with 4-bit integer weights:
+ *   C[m,n] = bf16( sum_k a[m,k] * w[n,k] ),
+ *   C[m,n] = bf16( silu(sum_k a[m,k] wg[n,k]) * sum_k a[m,k] wu[n,k] ).
+ * Products are exact and sums fp32; up to a group's scale, sums of a * (16 + q)
+ * and of a are formed, so activations from 2^116 on may overflow.  A row that holds an
+ * infinity or NaN has no finite output; which of the two it has is not defined.
+ *
+ *   A   device, BF16, row m at A + m * a_row_stride, 16-byte aligned
+ *   W, WS, WZ  device, laid-out codes (16-byte aligned), scales (2 * 128/group
+ *       bytes aligned) and zero points (128/group bytes aligned) or NULL; of a gated
+ *       product both matrices have zero points or neither
+ *   C   device, BF16, row m at C + m * c_row_stride, 2-byte aligned; only
+ *       columns < N of rows < M are written
+ *   M   rows, from one to a long prompt (0: nothing is launched), at most
+ *       WQD_MX_MAX_ROWS;  N  1 .. WQD_MX_MAX_ROWS
+ *   K   a positive multiple of 128, at most WQD_MX_MAX_K
+ *   scale_type    WQD_TYPE_FP16 or WQD_TYPE_BF16
+ *   a_row_stride  >= K, a multiple of 8, at most WQD_MX_MAX_STRIDE;  c_row_stride >= N
+ */
+int i4a16_gemm(const void *A, const void *W, const void *WS, const void *WZ, void *C,
+               uint32_t M, uint32_t N, uint32_t K, uint32_t group, uint32_t scale_type,
+               uint32_t a_row_stride, uint32_t c_row_stride, hipStream_t stream);
+int i4a16_gated(const void *A, const void *WG, const void *WGS, const void *WGZ,
+                const void *WU, const void *WUS, const void *WUZ, void *C,
+                uint32_t M, uint32_t N, uint32_t K, uint32_t group, uint32_t scale_type,
+                uint32_t a_row_stride, uint32_t c_row_stride, hipStream_t stream);
+
+#define WQD_MOE_SOFTMAX      0
+#define WQD_MOE_SIGMOID      1
+#define WQD_MOE_MAX_EXPERTS  1024        /* largest E */
+#define WQD_MOE_MAX_TOP_K    32          /* largest top_k */
+#define WQD_MOE_MAX_PAIRS    (1u << 24)  /* largest T * top_k */
+
+/*
+ * moe_route - each token's experts and their weights.
+ *   score = softmax over the token's logits, or their sigmoid;  choice value =
+ *   score + bias[e], or without a bias the logit itself.  With groups > 1 the experts
+ *   are `groups` equal runs, and only those of the top_groups best are chosen
+ *   from; a group's value is the sum of its group_top (1 or 2) largest score (+
+ *   bias) values.  The top_k largest choice values win, in falling order; among equals
+ *   the lowest index (of experts, and of groups) comes first.  weight = score
+ *   (without the bias), over the sum of the chosen scores if `renormalize`, times scale.
+ * Scores and choice values are 64-bit.  An expert whose logit, or bias, is NaN or minus
+ * infinity is never chosen; a logit of plus infinity counts as the largest fp32
+ * value.  Slots for which no expert is left get id -1 and weight 0, as does the
+ * weight where the chosen scores sum to 0 and are to be renormalised.
+ *
+ *   logits      device, BF16, FP16 or FP32 (logits_type: WQD_TYPE_*), row t at
+ *               logits + t * row_stride, row_stride >= E
+ *   bias        device, fp32 [E], or NULL
+ *   ids         device, int32 [T][top_k];  weights  device, fp32 [T][top_k]
+ *   T           tokens (0: nothing is launched), T * top_k <= WQD_MOE_MAX_PAIRS
+ *   E           1 .. WQD_MOE_MAX_EXPERTS;  top_k  1 .. min(E, WQD_MOE_MAX_TOP_K)
+ *   groups      1 .. 64, divides E;  top_groups  1 .. groups, and its experts
+ *               at least top_k
+ *   scale       finite
+ */
+int moe_route(const void *logits, uint32_t logits_type, const float *bias, int32_t *ids, float *weights,
+              uint32_t T, uint32_t E, uint32_t top_k, uint32_t row_stride, uint32_t scoring, uint32_t groups,
+              uint32_t top_groups, uint32_t group_top, int renormalize, float scale, hipStream_t stream);
+
+/*
+ * moe_lists - each expert's pairs.  Pair p = t * top_k + slot belongs to expert
+ * ids[p]; ids outside 0 .. E-1 (padded tokens, experts of another GPU) belong to
+ * none.  order[offsets[e]] .. order[offsets[e+1] - 1] are expert e's pairs in
+ * ascending order; from offsets[E] on order holds -1.
+ *   order  device, int32 [T * top_k];  offsets  device, int32 [E + 1] (written
+ *   for T = 0 too)
+ */
+int moe_lists(const int32_t *ids, int32_t *order, int32_t *offsets, uint32_t T, uint32_t top_k, uint32_t E,
+              hipStream_t stream);
+
+/*
+ * i4a16_experts_gated - the gated product of every token with each of its
+ * experts' matrices, a row per pair:
+ *   H[p,n] = bf16( silu(sum_k a[t,k] wg[e,n,k]) * sum_k a[t,k] wu[e,n,k] ),
+ *   p = t * top_k + slot, e = ids[p].  Rows of pairs without an expert are not written.
+ * i4a16_experts_down - the experts' last products and their weighted sum:
+ *   C[t,n] = bf16( sum_slot weights[p] * sum_k h[p,k] w[e,n,k] ),
+ *   slots without an expert left out; sums fp32.
+ *
+ * order and offsets are moe_lists' of the same ids, or both NULL: then every
+ * pair is multiplied by itself, which reads an expert's matrices once for
+ * each of its pairs and is the faster way for a few tokens only.
+ *
+ *   A    device, BF16 [T] rows of K, pitch a_row_stride;  H  device, BF16
+ *        [T * top_k][N] (the gated product's output), [T * top_k][K] (the last
+ *        one's input), 16-byte aligned as an input
+ *   WG, WGS, WGZ, WU, WUS, WUZ, W, WS, WZ  device, E matrices each, as above
+ *   Y    device, fp32 [T * top_k][N], 16-byte aligned: scratch, used with lists only
+ *        (NULL without); two calls that may run at once need one each
+ *   C    device, BF16, row t at C + t * c_row_stride
+ *   The rest is as for the products and moe_route.
+ */
+int i4a16_experts_gated(const void *A, const int32_t *ids, const int32_t *order, const int32_t *offsets,
+                        const void *WG, const void *WGS, const void *WGZ,
+                        const void *WU, const void *WUS, const void *WUZ, void *H,
+                        uint32_t T, uint32_t top_k, uint32_t E, uint32_t N, uint32_t K, uint32_t group,
+                        uint32_t scale_type, uint32_t a_row_stride, hipStream_t stream);
+int i4a16_experts_down(const void *H, const int32_t *ids, const float *weights, const int32_t *order,
+                       const int32_t *offsets, const void *W, const void *WS, const void *WZ, float *Y, void *C,
+                       uint32_t T, uint32_t top_k, uint32_t E, uint32_t N, uint32_t K, uint32_t group,
+                       uint32_t scale_type, uint32_t c_row_stride, hipStream_t stream);
+
 /* ----------------------------------------------------------- host helpers */
 
 /* Bytes of a packed Q2_0 matrix: N * (K/128) * 34, or 0 if K % 128 != 0. */

@@ -7,6 +7,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,8 +17,9 @@ LIB = os.path.join(PKG, "libwqd.so")
 # bench-only helper (a plain read of a buffer: the read ceiling bench.py reports)
 BENCH_LIB = os.path.join(PKG, "libwqd_bench.so")
 SOURCES = ["api.cpp", "pack.cpp", "q2_0_mfma.hip", "q2_0_valu.hip", "w8a16_gemm_m16.hip", "w8a16_gemv.hip",
-           "mx_quant.hip", "mx_skinny.hip", "mx_tile.hip"]
+           "mx_quant.hip", "mx_skinny.hip", "mx_tile.hip", "i4_pack.hip", "i4_skinny.hip", "moe_route.hip"]
 ARCH = "gfx950"
+JOBS = 6  # sources compiled at once
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
@@ -37,12 +40,17 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-x", "hip", *srcs, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(JOBS) as pool:
+        objs = [os.path.join(objects, s + ".o") for s in SOURCES]
+        cmds = [[hipcc(), *compile_flags, "-I", os.path.join(ROOT, "include"), "-x", "hip", "-c", os.path.join(CSRC, s), "-o", o]
+                for s, o in zip(SOURCES, objs)]
+        cmds.append([hipcc(), f"--offload-arch={ARCH}", "-shared", *objs, "-o", tmp])
+        if verbose:
+            print("\n".join(" ".join(c) for c in cmds), flush=True)
+        list(pool.map(lambda c: subprocess.run(c, check=True), cmds[:-1]))
+        subprocess.run(cmds[-1], check=True)
     os.replace(tmp, LIB)
     tmp = BENCH_LIB + ".tmp"
     cmd = [hipcc(), *HIPCC_FLAGS, "-x", "hip", os.path.join(CSRC, "bench_read.hip"), "-o", tmp]

@@ -190,6 +190,82 @@ wqd::MxOperands mx_operands(const void *A, const void *AS, const void *W, const 
   return {A, AS, W, WS, WU, WUS, M, N, K, lda, {static_cast<uint16_t *>(C), ldc, 0u}};
 }
 
+// Checks shared by the products with 4-bit integer weights: matrices (`both`:
+// two of them), their scales and zero points, and what the kernels' sizes assume.
+int validate_i4(const char *fn, const wqd::I4Operands &op, bool both, uint32_t scale_type) {
+  if (!op.w.W || !op.w.S || (both && (!op.up.W || !op.up.S)))
+    return fail(WQD_ENULL, "%s: weights and scales must be non-NULL", fn);
+  if (both && !op.w.Z != !op.up.Z)
+    return fail(WQD_ENULL, "%s: zero points of both matrices must be given or be NULL", fn);
+  if (op.N == 0) return fail(WQD_EINVAL, "%s: N must be >= 1", fn);
+  if (op.K == 0 || op.K % 128u != 0) return fail(WQD_EINVAL, "%s: K=%u is not a positive multiple of 128", fn, op.K);
+  if (op.group != 32u && op.group != 64u && op.group != 128u)
+    return fail(WQD_EINVAL, "%s: group=%u is not 32, 64 or 128", fn, op.group);
+  if (scale_type != WQD_TYPE_FP16 && scale_type != WQD_TYPE_BF16)
+    return fail(WQD_EINVAL, "%s: scale type %u is neither FP16 nor BF16", fn, scale_type);
+  if (op.K > WQD_MX_MAX_K) return fail(WQD_EUNSUPPORTED, "%s: K=%u above %u", fn, op.K, (unsigned)WQD_MX_MAX_K);
+  if (op.N > WQD_MX_MAX_ROWS) return fail(WQD_EUNSUPPORTED, "%s: N=%u above %u", fn, op.N, (unsigned)WQD_MX_MAX_ROWS);
+  if (op.lda < op.K || op.ldc < op.N)
+    return fail(WQD_EINVAL, "%s: row strides must cover the rows (%u < K=%u or %u < N=%u)", fn, op.lda, op.K, op.ldc, op.N);
+  if (op.lda % 8u != 0)
+    return fail(WQD_EINVAL, "%s: a_row_stride=%u is not a multiple of 8 (16-byte activation rows)", fn, op.lda);
+  if (op.lda > WQD_MX_MAX_STRIDE)
+    return fail(WQD_EUNSUPPORTED, "%s: a_row_stride=%u above %u", fn, op.lda, (unsigned)WQD_MX_MAX_STRIDE);
+  const uintptr_t values = 128u / op.group;  // of a row's 128 k, read at once
+  if (!aligned(op.A, 16)) return fail(WQD_EALIGN, "%s: activations must be 16-byte aligned", fn);
+  if (!aligned(op.w.W, 16) || !aligned(op.up.W, 16)) return fail(WQD_EALIGN, "%s: weights must be 16-byte aligned", fn);
+  if (!aligned(op.w.S, 2 * values) || !aligned(op.up.S, 2 * values))
+    return fail(WQD_EALIGN, "%s: scales must be %u-byte aligned", fn, (unsigned)(2 * values));
+  if (!aligned(op.w.Z, values) || !aligned(op.up.Z, values))
+    return fail(WQD_EALIGN, "%s: zero points must be %u-byte aligned", fn, (unsigned)values);
+  if (!aligned(op.C, 2)) return fail(WQD_EALIGN, "%s: C must be 2-byte aligned", fn);
+  return WQD_OK;
+}
+
+int run_i4_product(const char *fn, wqd::I4Operands op, uint32_t scale_type, hipStream_t stream) {
+  if (op.M && (!op.A || !op.C)) return fail(WQD_ENULL, "%s: A and C must be non-NULL", fn);
+  if (int rc = validate_i4(fn, op, op.gated, scale_type)) return rc;
+  if (op.M > WQD_MX_MAX_ROWS) return fail(WQD_EUNSUPPORTED, "%s: M=%u above %u", fn, op.M, (unsigned)WQD_MX_MAX_ROWS);
+  if (op.M == 0) return WQD_OK;  // no rows: nothing to launch
+  if (int rc = check_device(fn)) return rc;
+  (void)hipGetLastError();
+  return check_launch(fn, wqd::launch_i4_skinny(op, op.gated, stream));
+}
+
+// Sizes of a routed call.
+int validate_routes(const char *fn, uint32_t T, uint32_t top_k, uint32_t E) {
+  if (E == 0 || E > WQD_MOE_MAX_EXPERTS)
+    return fail(WQD_EINVAL, "%s: E=%u is not from 1 to %u", fn, E, (unsigned)WQD_MOE_MAX_EXPERTS);
+  if (top_k == 0 || top_k > E || top_k > WQD_MOE_MAX_TOP_K)
+    return fail(WQD_EINVAL, "%s: top_k=%u is not from 1 to E=%u and %u", fn, top_k, E, (unsigned)WQD_MOE_MAX_TOP_K);
+  if ((uint64_t)T * top_k > WQD_MOE_MAX_PAIRS)
+    return fail(WQD_EUNSUPPORTED, "%s: T=%u tokens with top_k=%u are too many for one call", fn, T, top_k);
+  return WQD_OK;
+}
+
+int run_i4_experts(const char *fn, wqd::I4Operands op, uint32_t scale_type, hipStream_t stream) {
+  if (op.T && (!op.A || !op.C || !op.ids || (!op.gated && !op.weights)))
+    return fail(WQD_ENULL, "%s: activations, ids, weights and outputs must be non-NULL", fn);
+  if (op.T && !op.order != !op.offsets) return fail(WQD_ENULL, "%s: order and offsets must both be given or both be NULL", fn);
+  if (op.T && !op.gated && op.order && !op.Y) return fail(WQD_ENULL, "%s: Y must be non-NULL where lists are given", fn);
+  if (int rc = validate_routes(fn, op.T, op.top_k, op.E)) return rc;
+  if (int rc = validate_i4(fn, op, op.gated, scale_type)) return rc;
+  if (!aligned(op.ids, 4) || !aligned(op.order, 4) || !aligned(op.offsets, 4) || !aligned(op.weights, 4))
+    return fail(WQD_EALIGN, "%s: ids, weights and lists must be 4-byte aligned", fn);
+  if (!aligned(op.Y, 16)) return fail(WQD_EALIGN, "%s: Y must be 16-byte aligned", fn);
+  if (op.T == 0) return WQD_OK;
+  if (wqd::i4_experts_grid(op) > wqd::i4_experts_max_grid())
+    return fail(WQD_EUNSUPPORTED, "%s: T=%u tokens of top_k=%u experts times N=%u are too many for one call", fn, op.T, op.top_k, op.N);
+  if (int rc = check_device(fn)) return rc;
+  (void)hipGetLastError();
+  if (int rc = check_launch(fn, wqd::launch_i4_experts_skinny(op, stream))) return rc;
+  return !op.gated && op.order ? check_launch(fn, wqd::launch_moe_combine(op, stream)) : WQD_OK;
+}
+
+wqd::I4Matrix i4_matrix(const void *W, const void *S, const void *Z) {
+  return {static_cast<const uint8_t *>(W), static_cast<const uint16_t *>(S), static_cast<const uint8_t *>(Z)};
+}
+
 // 16-row tiles per workgroup in w8a16_gemm_m16_n64: 64 weight rows each.
 constexpr uint32_t kN64Band = 4;
 
@@ -401,6 +477,126 @@ int w4a4_gated(const void *A, const void *AS, const void *WG, const void *WGS, c
                uint32_t M, uint32_t N, uint32_t K, uint32_t c_row_stride, hipStream_t stream) {
   return run_mx_product("w4a4_gated", mx_operands(A, AS, WG, WGS, WU, WUS, C, M, N, K, K, c_row_stride),
                         wqd::MxFormat::kFp4, true, stream);
+}
+
+int i4_pack(const void *Q, void *W, uint32_t N, uint32_t K, uint32_t count, hipStream_t stream) {
+  static const char fn[] = "i4_pack";
+  if (count && (!Q || !W)) return fail(WQD_ENULL, "%s: Q and W must be non-NULL", fn);
+  if (N == 0) return fail(WQD_EINVAL, "%s: N must be >= 1", fn);
+  if (K == 0 || K % 128u != 0) return fail(WQD_EINVAL, "%s: K=%u is not a positive multiple of 128", fn, K);
+  if (K > WQD_MX_MAX_K) return fail(WQD_EUNSUPPORTED, "%s: K=%u above %u", fn, K, (unsigned)WQD_MX_MAX_K);
+  if (N > WQD_MX_MAX_ROWS) return fail(WQD_EUNSUPPORTED, "%s: N=%u above %u", fn, N, (unsigned)WQD_MX_MAX_ROWS);
+  if (count > WQD_MOE_MAX_EXPERTS)
+    return fail(WQD_EUNSUPPORTED, "%s: count=%u above %u", fn, count, (unsigned)WQD_MOE_MAX_EXPERTS);
+  if (!aligned(Q, 4)) return fail(WQD_EALIGN, "%s: Q must be 4-byte aligned", fn);
+  if (!aligned(W, 16)) return fail(WQD_EALIGN, "%s: W must be 16-byte aligned", fn);
+  if (count == 0) return WQD_OK;
+  if (int rc = check_device(fn)) return rc;
+  (void)hipGetLastError();
+  return check_launch(fn, wqd::launch_i4_pack(Q, W, N, K, count, stream));
+}
+
+size_t i4_packed_bytes(uint32_t N, uint32_t K) {
+  if (K % 128u != 0) return 0;
+  return (static_cast<size_t>(N) + 15u) / 16u * 16u * (K / 2u);
+}
+
+int i4a16_gemm(const void *A, const void *W, const void *WS, const void *WZ, void *C, uint32_t M, uint32_t N, uint32_t K,
+               uint32_t group, uint32_t scale_type, uint32_t a_row_stride, uint32_t c_row_stride, hipStream_t stream) {
+  wqd::I4Operands op = {};
+  op.A = static_cast<const uint16_t *>(A);
+  op.w = i4_matrix(W, WS, WZ);
+  op.C = static_cast<uint16_t *>(C);
+  op.M = M, op.N = N, op.K = K, op.lda = a_row_stride, op.ldc = c_row_stride, op.group = group;
+  op.scale_bf16 = scale_type == WQD_TYPE_BF16;
+  return run_i4_product("i4a16_gemm", op, scale_type, stream);
+}
+
+int i4a16_gated(const void *A, const void *WG, const void *WGS, const void *WGZ, const void *WU, const void *WUS,
+                const void *WUZ, void *C, uint32_t M, uint32_t N, uint32_t K, uint32_t group, uint32_t scale_type,
+                uint32_t a_row_stride, uint32_t c_row_stride, hipStream_t stream) {
+  wqd::I4Operands op = {};
+  op.A = static_cast<const uint16_t *>(A);
+  op.w = i4_matrix(WG, WGS, WGZ);
+  op.up = i4_matrix(WU, WUS, WUZ);
+  op.C = static_cast<uint16_t *>(C);
+  op.M = M, op.N = N, op.K = K, op.lda = a_row_stride, op.ldc = c_row_stride, op.group = group;
+  op.scale_bf16 = scale_type == WQD_TYPE_BF16;
+  op.gated = true;
+  return run_i4_product("i4a16_gated", op, scale_type, stream);
+}
+
+int moe_route(const void *logits, uint32_t logits_type, const float *bias, int32_t *ids, float *weights, uint32_t T,
+              uint32_t E, uint32_t top_k, uint32_t row_stride, uint32_t scoring, uint32_t groups, uint32_t top_groups,
+              uint32_t group_top, int renormalize, float scale, hipStream_t stream) {
+  static const char fn[] = "moe_route";
+  if (T && (!logits || !ids || !weights)) return fail(WQD_ENULL, "%s: logits, ids and weights must be non-NULL", fn);
+  if (int rc = validate_routes(fn, T, top_k, E)) return rc;
+  if (logits_type != WQD_TYPE_BF16 && logits_type != WQD_TYPE_FP16 && logits_type != WQD_TYPE_FP32)
+    return fail(WQD_EINVAL, "%s: type %u of the logits is not BF16, FP16 or FP32", fn, logits_type);
+  if (scoring != WQD_MOE_SOFTMAX && scoring != WQD_MOE_SIGMOID)
+    return fail(WQD_EINVAL, "%s: scoring %u is neither softmax nor sigmoid", fn, scoring);
+  if (row_stride < E) return fail(WQD_EINVAL, "%s: row_stride=%u below E=%u", fn, row_stride, E);
+  if (groups == 0 || groups > 64u || E % groups != 0)
+    return fail(WQD_EINVAL, "%s: groups=%u is not from 1 to 64 or does not divide E=%u", fn, groups, E);
+  if (top_groups == 0 || top_groups > groups || top_k > top_groups * (E / groups))
+    return fail(WQD_EINVAL, "%s: top_groups=%u of %u groups do not hold top_k=%u experts", fn, top_groups, groups, top_k);
+  if (group_top != 1u && group_top != 2u) return fail(WQD_EINVAL, "%s: group_top=%u is neither 1 nor 2", fn, group_top);
+  if (!std::isfinite(scale)) return fail(WQD_EINVAL, "%s: scale must be finite", fn);
+  const uintptr_t size = logits_type == WQD_TYPE_FP32 ? 4 : 2;
+  if (!aligned(logits, size) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return fail(WQD_EALIGN, "%s: operands must be aligned to their elements", fn);
+  if (T == 0) return WQD_OK;
+  if (int rc = check_device(fn)) return rc;
+  (void)hipGetLastError();
+  return check_launch(fn, wqd::launch_moe_route({logits, bias, ids, weights, logits_type, T, E, top_k, row_stride,
+                                                 scoring == WQD_MOE_SIGMOID ? 1u : 0u, groups, top_groups, group_top,
+                                                 renormalize ? 1u : 0u, scale}, stream));
+}
+
+int moe_lists(const int32_t *ids, int32_t *order, int32_t *offsets, uint32_t T, uint32_t top_k, uint32_t E,
+              hipStream_t stream) {
+  static const char fn[] = "moe_lists";
+  if (!offsets || (T && (!ids || !order))) return fail(WQD_ENULL, "%s: ids, order and offsets must be non-NULL", fn);
+  if (int rc = validate_routes(fn, T, top_k, E)) return rc;
+  if (!aligned(ids, 4) || !aligned(order, 4) || !aligned(offsets, 4))
+    return fail(WQD_EALIGN, "%s: ids, order and offsets must be 4-byte aligned", fn);
+  if (int rc = check_device(fn)) return rc;
+  (void)hipGetLastError();
+  return check_launch(fn, wqd::launch_moe_lists(ids, order, offsets, T * top_k, E, stream));
+}
+
+int i4a16_experts_gated(const void *A, const int32_t *ids, const int32_t *order, const int32_t *offsets, const void *WG,
+                        const void *WGS, const void *WGZ, const void *WU, const void *WUS, const void *WUZ, void *H,
+                        uint32_t T, uint32_t top_k, uint32_t E, uint32_t N, uint32_t K, uint32_t group,
+                        uint32_t scale_type, uint32_t a_row_stride, hipStream_t stream) {
+  wqd::I4Operands op = {};
+  op.A = static_cast<const uint16_t *>(A);
+  op.w = i4_matrix(WG, WGS, WGZ);
+  op.up = i4_matrix(WU, WUS, WUZ);
+  op.C = static_cast<uint16_t *>(H);
+  op.ids = ids, op.order = order, op.offsets = offsets;
+  op.N = N, op.K = K, op.lda = a_row_stride, op.ldc = N, op.group = group;
+  op.scale_bf16 = scale_type == WQD_TYPE_BF16;
+  op.T = T, op.top_k = top_k, op.E = E;
+  op.gated = true;
+  return run_i4_experts("i4a16_experts_gated", op, scale_type, stream);
+}
+
+int i4a16_experts_down(const void *H, const int32_t *ids, const float *weights, const int32_t *order,
+                       const int32_t *offsets, const void *W, const void *WS, const void *WZ, float *Y, void *C,
+                       uint32_t T, uint32_t top_k, uint32_t E, uint32_t N, uint32_t K, uint32_t group,
+                       uint32_t scale_type, uint32_t c_row_stride, hipStream_t stream) {
+  wqd::I4Operands op = {};
+  op.A = static_cast<const uint16_t *>(H);
+  op.w = i4_matrix(W, WS, WZ);
+  op.C = static_cast<uint16_t *>(C);
+  op.Y = Y;
+  op.ids = ids, op.order = order, op.offsets = offsets, op.weights = weights;
+  op.N = N, op.K = K, op.lda = K, op.ldc = c_row_stride, op.group = group;
+  op.scale_bf16 = scale_type == WQD_TYPE_BF16;
+  op.T = T, op.top_k = top_k, op.E = E;
+  return run_i4_experts("i4a16_experts_down", op, scale_type, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,285 @@
+// A router's choice of experts, the experts' lists of tokens and the weighted
+// sum of the experts' outputs, for gfx950 (MI355X).
+//
+// Choice (moe_route_kernel): a wave takes a token; lane l holds experts l V ..
+// l V + V - 1, so the lowest lane among equals has the lowest expert.  Scores
+// and what is chosen by (score + bias) are 64-bit: a rounding to fewer bits would
+// swap experts whose values differ by less.  The top_k rounds are a maximum over
+// the wave each (DPP steps, no LDS).
+//
+// Lists (moe_lists_kernel): a workgroup per expert counts the pairs of all
+// lower experts, which is where its own list begins, and writes its pairs in
+// ascending order; no atomics, no second launch, no workspace.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/wqd.h"
+#include "i4_common.h"
+#include "mx_product.h"
+
+namespace wqd {
+namespace {
+
+constexpr double kNone = -__builtin_huge_val();
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double from_lane(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
+  const uint32_t l = (uint32_t)__builtin_amdgcn_update_dpp((int)lo, (int)lo, CTRL, ROWS, 0xF, false);
+  const uint32_t h = (uint32_t)__builtin_amdgcn_update_dpp((int)hi, (int)hi, CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+}
+__device__ __forceinline__ double read_lane(double x, uint32_t lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t l = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, (int)lane);
+  const uint32_t h = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), (int)lane);
+  return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+}
+// Largest value of a wave, none of them NaN
+__device__ __forceinline__ double wave_max(double x) {
+  x = __builtin_fmax(x, from_lane<0x111, 0xF>(x));  // from 1, 2, 4 and 8 lanes below in a row of 16
+  x = __builtin_fmax(x, from_lane<0x112, 0xF>(x));
+  x = __builtin_fmax(x, from_lane<0x114, 0xF>(x));
+  x = __builtin_fmax(x, from_lane<0x118, 0xF>(x));
+  x = __builtin_fmax(x, from_lane<0x142, 0xA>(x));  // the last lane of a row to the next row
+  x = __builtin_fmax(x, from_lane<0x143, 0xC>(x));  // lane 31 to the upper half
+  return read_lane(x, 63u);
+}
+// Sum over a wave, the same in every lane
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
+  return x;
+}
+
+template <int V>
+__global__ __launch_bounds__(256) void moe_route_kernel(MoeRoute op) {
+  extern __shared__ __attribute__((aligned(16))) double shared[];  // of a choice by groups: each wave's values
+  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t t = blockIdx.x * 4u + wave;
+  if (t >= op.T) return;  // no barriers below
+
+  // An expert whose logit is NaN or minus infinity, or whose bias is, is never chosen.
+  double p[V], key[V];
+  double top = kNone;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const uint32_t e = lane * V + v;
+    float x = __builtin_nanf("");
+    if (e < op.E) {
+      const uint64_t at = (uint64_t)t * op.ld + e;
+      if (op.type == WQD_TYPE_FP32)
+        x = static_cast<const float *>(op.logits)[at];
+      else if (op.type == WQD_TYPE_BF16)
+        x = __uint_as_float((uint32_t) static_cast<const uint16_t *>(op.logits)[at] << 16);
+      else
+        x = (float)static_cast<const _Float16 *>(op.logits)[at];
+    }
+    x = x > 3.402823466e38f ? 3.402823466e38f : x;  // an infinity is the largest value
+    key[v] = x > -__builtin_inff() ? (double)x : kNone;
+    top = __builtin_fmax(top, key[v]);
+  }
+  top = wave_max(top);
+  if (op.sigmoid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] = 1.0 / (1.0 + exp(-key[v]));
+  } else {
+    double sum = 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      p[v] = key[v] > kNone ? exp(key[v] - top) : 0.0;
+      sum += p[v];
+    }
+    sum = wave_sum(sum);
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] = p[v] / sum;
+  }
+  // Without a bias the order is that of the logits.
+  if (op.bias) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t e = lane * V + v;
+      const double b = e < op.E ? (double)op.bias[e] : kNone;
+      key[v] = key[v] > kNone && b > kNone ? p[v] + b : kNone;
+    }
+  }
+
+  if (op.groups > 1u) {
+    // The groups of the largest sums of their group_top largest values; a lane takes a group.
+    const uint32_t size = op.E / op.groups;
+    double *mine = shared + wave * op.E;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t e = lane * V + v;
+      if (e < op.E) mine[e] = op.bias || op.group_top == 1u || !(key[v] > kNone) ? key[v] : p[v];
+    }
+    double first = kNone, second = kNone;
+    if (lane < op.groups) {
+      for (uint32_t i = 0; i < size; ++i) {
+        const double x = mine[lane * size + i];
+        second = __builtin_fmax(second, __builtin_fmin(first, x));
+        first = __builtin_fmax(first, x);
+      }
+    }
+    const double score = op.group_top == 2u && second > kNone ? first + second : first;
+    uint32_t ahead = 0;
+    for (uint32_t i = 0; i < op.groups; ++i) {
+      const double x = read_lane(score, i);
+      ahead += x > score || (x == score && i < lane) ? 1u : 0u;
+    }
+    const uint64_t in = __ballot(lane < op.groups && ahead < op.top_groups);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t e = lane * V + v;
+      if (e < op.E && !(in >> (e / size) & 1u)) key[v] = kNone;
+    }
+  }
+
+  uint32_t taken = 0, id = ~0u;  // this lane's experts that are taken; the choice of slot `lane`
+  double weight = 0.0, sum = 0.0;
+  for (uint32_t s = 0; s < op.top_k; ++s) {
+    double best = kNone, score = 0.0;
+    uint32_t at = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (!(taken >> v & 1u) && key[v] > best) {
+        best = key[v];
+        score = p[v];
+        at = v;
+      }
+    const double m = wave_max(best);
+    if (!(m > kNone)) break;
+    const uint32_t l = (uint32_t)__builtin_ctzll(__ballot(best == m));
+    const uint32_t e = (uint32_t)__builtin_amdgcn_readlane((int)at, (int)l) + l * V;
+    const double w = read_lane(score, l);
+    if (lane == l) taken |= 1u << at;
+    if (lane == s) {
+      id = e;
+      weight = w;
+    }
+    sum += w;
+  }
+  if (lane < op.top_k) {
+    if (op.renormalize) weight = sum > 0.0 ? weight / sum : 0.0;
+    op.ids[(uint64_t)t * op.top_k + lane] = (int32_t)id;
+    op.weights[(uint64_t)t * op.top_k + lane] = (float)(weight * (double)op.scale);
+  }
+}
+
+template <int V>
+hipError_t launch_route(const MoeRoute &op, hipStream_t stream) {
+  hipLaunchKernelGGL((moe_route_kernel<V>), dim3((op.T + 3u) / 4u), dim3(256), op.groups > 1u ? 4u * op.E * 8u : 0u, stream, op);
+  return hipGetLastError();
+}
+
+constexpr uint32_t kListWaves = 16, kBatch = 8;  // kBatch loads of a wave in flight
+
+// Workgroup e < E writes expert e's list; workgroup E the lists' end and what is behind it.
+__global__ __launch_bounds__(64 * kListWaves) void moe_lists_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ order,
+                                                                    int32_t *__restrict__ offsets, uint32_t pairs, uint32_t E) {
+  __shared__ uint32_t counts[2][kListWaves];
+  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), e = blockIdx.x;
+  // each wave its own stretch of pairs, in whole rounds of 64
+  const uint32_t each = ((pairs + 63u) / 64u + kListWaves - 1u) / kListWaves * 64u;
+  const uint32_t from = wave * each < pairs ? wave * each : pairs, to = pairs - from < each ? pairs : from + each;
+  uint32_t below = 0, own = 0;
+  for (uint32_t i0 = from + lane; i0 < to; i0 += 64u * kBatch) {
+    uint32_t id[kBatch];
+#pragma unroll
+    for (uint32_t b = 0; b < kBatch; ++b) id[b] = i0 + b * 64u < to ? (uint32_t)ids[i0 + b * 64u] : ~0u;
+#pragma unroll
+    for (uint32_t b = 0; b < kBatch; ++b) {
+      below += id[b] < e ? 1u : 0u;
+      own += id[b] == e ? 1u : 0u;
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    below += (uint32_t)__shfl_xor((int)below, d);
+    own += (uint32_t)__shfl_xor((int)own, d);
+  }
+  if (lane == 0u) {
+    counts[0][wave] = below;
+    counts[1][wave] = own;
+  }
+  __syncthreads();
+  uint32_t start = 0, place = 0;
+  for (uint32_t w = 0; w < kListWaves; ++w) {
+    start += counts[0][w];
+    place += w < wave ? counts[1][w] : 0u;
+  }
+  if (threadIdx.x == 0u) offsets[e] = (int32_t)start;
+  if (e == E) {
+    for (uint32_t i = start + threadIdx.x; i < pairs; i += 64u * kListWaves) order[i] = -1;
+    return;
+  }
+  place += start;
+  for (uint32_t i0 = from; i0 < to; i0 += 64u * kBatch) {
+    uint32_t id[kBatch];
+#pragma unroll
+    for (uint32_t b = 0; b < kBatch; ++b) {
+      const uint32_t p = i0 + b * 64u + lane;
+      id[b] = p < to ? (uint32_t)ids[p] : ~0u;
+    }
+#pragma unroll
+    for (uint32_t b = 0; b < kBatch; ++b) {
+      const uint64_t set = __ballot(id[b] == e);
+      const uint32_t before = __builtin_amdgcn_mbcnt_hi((uint32_t)(set >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)set, 0u));
+      if (id[b] == e) order[place + before] = (int32_t)(i0 + b * 64u + lane);
+      place += (uint32_t)__builtin_popcountll(set);
+    }
+  }
+}
+
+// A thread adds four columns of a token's rows in slot order; slots without an
+// expert of these are passed over.
+__global__ __launch_bounds__(256) void moe_combine_kernel(I4Operands op) {
+  const uint32_t pieces = (op.N + 3u) / 4u;
+  const uint64_t x = (uint64_t)blockIdx.x * 256u + threadIdx.x;
+  const uint32_t t = (uint32_t)(x / pieces), n = (uint32_t)(x - (uint64_t)t * pieces) * 4u;
+  if (t >= op.T) return;
+  float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (uint32_t s = 0; s < op.top_k; ++s) {
+    const uint32_t p = t * op.top_k + s;
+    if ((uint32_t)op.ids[p] >= op.E) continue;
+    const float w = op.weights[p];
+    const float *y = op.Y + (uint64_t)p * op.N + n;
+    if (op.N % 4u == 0u) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t *>(y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(w, v[i], c[i]);
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i)
+        if (n + i < op.N) c[i] = __builtin_fmaf(w, y[i], c[i]);
+    }
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i)
+    if (n + i < op.N) op.C[(uint64_t)t * op.ldc + n + i] = (uint16_t)bf16x2_rne(c[i], 0.0f);
+}
+
+}  // namespace
+
+hipError_t launch_moe_route(const MoeRoute &op, hipStream_t stream) {
+  if (op.E <= 64u) return launch_route<1>(op, stream);
+  if (op.E <= 128u) return launch_route<2>(op, stream);
+  if (op.E <= 256u) return launch_route<4>(op, stream);
+  if (op.E <= 512u) return launch_route<8>(op, stream);
+  return launch_route<16>(op, stream);
+}
+
+hipError_t launch_moe_lists(const int32_t *ids, int32_t *order, int32_t *offsets, uint32_t pairs, uint32_t E,
+                            hipStream_t stream) {
+  hipLaunchKernelGGL(moe_lists_kernel, dim3(E + 1u), dim3(64 * kListWaves), 0, stream, ids, order, offsets, pairs, E);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const I4Operands &op, hipStream_t stream) {
+  const uint64_t threads = (uint64_t)op.T * ((op.N + 3u) / 4u);
+  hipLaunchKernelGGL(moe_combine_kernel, dim3((uint32_t)((threads + 255u) / 256u)), dim3(256), 0, stream, op);
+  return hipGetLastError();
+}
+
+}  // namespace wqd

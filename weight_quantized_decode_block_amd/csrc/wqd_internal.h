@@ -99,4 +99,56 @@ hipError_t launch_mx_dequantize(const void *Q, const void *S, bool fp4, void *Y,
 hipError_t launch_add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *Y, void *Q, void *S,
                                   uint32_t M, uint32_t K, uint32_t ldx, uint32_t ldr, float eps, hipStream_t stream);
 
+// A matrix of 4-bit integer weights (or several, one after another): codes laid
+// out in tiles, scales [N][K/group] in FP16 or BF16, zero points likewise or null.
+struct I4Matrix {
+  const uint8_t *W;
+  const uint16_t *S;
+  const uint8_t *Z;
+};
+
+// Operands of products with such weights.  Dense: M rows of A, to C.  Routed (E
+// > 0): ids and weights [T][top_k], lists (order, offsets) or null; A's rows are
+// tokens (gated) or pairs, C's are pairs (gated) or tokens, Y's are pairs.
+// Shapes validated by the caller.
+struct I4Operands {
+  const uint16_t *A;
+  I4Matrix w, up;  // up: of a gated product
+  uint16_t *C;
+  float *Y;
+  const int32_t *ids, *order, *offsets;
+  const float *weights;
+  uint32_t M, N, K, lda, ldc, group, scale_bf16;
+  uint32_t T, top_k, E;
+  bool gated;
+};
+
+// Enqueue a dense product (i4_tile.hip chooses the kernel; launch_i4_skinny is
+// the one for few rows, which takes any size).
+hipError_t launch_i4_skinny(const I4Operands &op, bool gated, hipStream_t stream);
+
+// Enqueue the experts' products: gated (C gets a row per pair), or the last ones
+// (with lists: Y gets a row per pair; without: C gets each token's weighted sum).
+uint64_t i4_experts_grid(const I4Operands &op);  // workgroups of that launch, and the most that one may have
+uint64_t i4_experts_max_grid();
+hipError_t launch_i4_experts_skinny(const I4Operands &op, hipStream_t stream);
+
+// Enqueue the layout of `count` matrices' codes.
+hipError_t launch_i4_pack(const void *Q, void *W, uint32_t N, uint32_t K, uint32_t count, hipStream_t stream);
+
+// A router's operands; shapes validated by the caller.
+struct MoeRoute {
+  const void *logits;
+  const float *bias;
+  int32_t *ids;
+  float *weights;
+  uint32_t type, T, E, top_k, ld, sigmoid, groups, top_groups, group_top, renormalize;
+  float scale;
+};
+hipError_t launch_moe_route(const MoeRoute &op, hipStream_t stream);
+hipError_t launch_moe_lists(const int32_t *ids, int32_t *order, int32_t *offsets, uint32_t pairs, uint32_t E,
+                            hipStream_t stream);
+// C[t] = sum of a token's rows of Y, weighted, in slot order
+hipError_t launch_moe_combine(const I4Operands &op, hipStream_t stream);
+
 }  // namespace wqd

@@ -26,6 +26,7 @@ Q2_0_BATCHM_MAX_M = 8
 W8A16_MAX_M = 16
 MXFP4, MXFP8 = 4, 8  # WQD_MXFP4, WQD_MXFP8
 TYPE_BF16, TYPE_FP16, TYPE_FP32 = range(3)  # WQD_TYPE_*
+MOE_SOFTMAX, MOE_SIGMOID = range(2)  # WQD_MOE_*
 Q2_0_TIER_WIDTHS = (1, 2, 4, 6, 8)  # WQD_Q2_0_TIER_WIDTHS, narrowest first
 
 _lib = None
@@ -69,6 +70,18 @@ def lib() -> ctypes.CDLL:
     for f in (L.mx_quantize, L.mx_dequantize, L.add_rmsnorm_mx8, L.w4a16_gemm, L.w4a8_gemm, L.w4a4_gemm,
               L.w4a16_gated, L.w4a8_gated, L.w4a4_gated):
         f.restype = ctypes.c_int
+    i32, f32 = ctypes.c_int, ctypes.c_float
+    L.i4_pack.argtypes = [vp, vp, u32, u32, u32, vp]
+    L.i4a16_gemm.argtypes = [vp] * 5 + [u32] * 7 + [vp]
+    L.i4a16_gated.argtypes = [vp] * 8 + [u32] * 7 + [vp]
+    L.moe_route.argtypes = [vp, u32, vp, vp, vp] + [u32] * 8 + [i32, f32, vp]
+    L.moe_lists.argtypes = [vp, vp, vp, u32, u32, u32, vp]
+    L.i4a16_experts_gated.argtypes = [vp] * 11 + [u32] * 8 + [vp]
+    L.i4a16_experts_down.argtypes = [vp] * 10 + [u32] * 8 + [vp]
+    for f in (L.i4_pack, L.i4a16_gemm, L.i4a16_gated, L.moe_route, L.moe_lists, L.i4a16_experts_gated, L.i4a16_experts_down):
+        f.restype = ctypes.c_int
+    L.i4_packed_bytes.argtypes = [u32, u32]
+    L.i4_packed_bytes.restype = sz
     L.q2_0_packed_bytes.argtypes = [u32, u32]
     L.q2_0_packed_bytes.restype = sz
     L.q2_0_pack.argtypes = [vp, vp, u32, u32, vp]
@@ -175,6 +188,7 @@ _types: dict = {}  # torch's types of values: WQD_TYPE_*
 # torch's types that a kind of operand may have: its own, and integers of its size for plain bits (_here fills them)
 _VALUES, _BF16, _SCALES = set(), set(), set()
 _CODES: dict = {MXFP4: set(), MXFP8: set()}
+_BYTES, _I4_SCALES, _INT32, _FP32 = set(), set(), set(), set()
 
 
 def _sizes(fn: str, bits: int, K: int) -> None:
@@ -229,7 +243,7 @@ def _arg(fn: str, name: str, x, nbytes: int, device: int, kind: set, pitch: int 
     if x.get_device() != device:
         raise ValueError(f"{fn}: {name} is not on the current GPU")
     if x.dtype not in kind:
-        size = 2 if kind is _BF16 else 1
+        size = max(t.itemsize for t in kind)
         raise ValueError(f"{fn}: {name} must have {size}-byte elements of type "
                          f"{', '.join(sorted(str(t)[6:] for t in kind))}, not {str(x.dtype)[6:]}")
     n = x.nbytes
@@ -255,6 +269,10 @@ def _here(fn: str, stream) -> tuple[int, int | None]:
         _SCALES.update((torch.float8_e8m0fnu, torch.uint8, torch.int8))
         _CODES[MXFP8].update((torch.float8_e4m3fn, torch.uint8, torch.int8))
         _CODES[MXFP4].update((torch.float4_e2m1fn_x2, torch.uint8, torch.int8))
+        _BYTES.update((torch.uint8, torch.int8))
+        _I4_SCALES.update((torch.float16, torch.bfloat16))
+        _INT32.add(torch.int32)
+        _FP32.add(torch.float32)
         gpu = torch.cuda.is_available()
         if gpu:
             torch.cuda.init()
@@ -398,6 +416,150 @@ def w4a8_gated(A, AS, WG, WGS, WU, WUS, C, M: int, N: int, K: int, c_row_stride:
 def w4a4_gated(A, AS, WG, WGS, WU, WUS, C, M: int, N: int, K: int, c_row_stride: int | None = None,
                stream=None) -> None:
     _gated((_lib or lib()).w4a4_gated, "w4a4_gated", MXFP4, A, AS, WG, WGS, WU, WUS, C, M, N, K, None, c_row_stride, stream)
+
+
+# ------------------------- 4-bit integer weights, routed experts
+_SCORING = {"softmax": MOE_SOFTMAX, "sigmoid": MOE_SIGMOID, MOE_SOFTMAX: MOE_SOFTMAX, MOE_SIGMOID: MOE_SIGMOID}
+
+
+def _i4_sizes(fn: str, bits: int, K: int, group: int) -> None:
+    """As _sizes, for K in whole tiles of 128 and a group that divides them."""
+    if bits < 0 or bits >> 32:
+        raise ValueError(f"{fn}: sizes and strides must be from 0 to 2^32 - 1")
+    if K % 128 or not K:
+        raise WqdError(fn, WQD_EINVAL, f"{fn}: K={K} is not a positive multiple of 128")
+    if group not in (32, 64, 128):
+        raise WqdError(fn, WQD_EINVAL, f"{fn}: group={group} is not 32, 64 or 128")
+
+
+def _i4_scale_type(fn: str, given: int | None, *scales) -> int:
+    """WQD_TYPE_* of the scales (an address comes with its type, FP16 unless told)."""
+    t = given
+    for s in scales:
+        if s is None or isinstance(s, int):
+            continue
+        own = _types.get(s.dtype)
+        if own not in (TYPE_FP16, TYPE_BF16) or t not in (None, own):
+            raise ValueError(f"{fn}: scales must all be FP16 or all BF16, as their tensors are ({str(s.dtype)[6:]})")
+        t = own
+    return TYPE_FP16 if t is None else t
+
+
+def _i4_matrix(fn: str, name: str, W, S, Z, E: int, N: int, K: int, group: int, d: int) -> tuple:
+    """Addresses of E matrices' codes, scales and zero points."""
+    rows = -(-N // 16) * 16
+    g = K // group
+    return (_arg(fn, name, W, E * rows * K // 2, d, _BYTES), _arg(fn, name + "S", S, 2 * E * N * g, d, _I4_SCALES, g),
+            _arg(fn, name + "Z", Z, E * N * g, d, _BYTES, g))
+
+
+def i4_packed_bytes(N: int, K: int) -> int:
+    """Bytes of a matrix's laid-out codes."""
+    return int(lib().i4_packed_bytes(N, K))
+
+
+def i4_pack(Q, W, N: int, K: int, count: int = 1, stream=None) -> None:
+    """Codes of `count` matrices, two a byte with the even k in the low nibble, to
+    the layout that the products read."""
+    fn = "i4_pack"
+    _i4_sizes(fn, N | K | count, K, 128)
+    d, st = _here(fn, stream)
+    _check(fn, (_lib or lib()).i4_pack(_arg(fn, "Q", Q, count * N * K // 2, d, _BYTES, K // 2),
+                                       _arg(fn, "W", W, count * (-(-N // 16) * 16) * K // 2, d, _BYTES), N, K, count, st))
+
+
+def i4a16_gemm(A, W, WS, WZ, C, M: int, N: int, K: int, group: int, a_row_stride: int | None = None,
+               c_row_stride: int | None = None, scale_type: int | None = None, stream=None) -> None:
+    """C = A W^T, W in laid-out codes W, scales WS and zero points WZ (None: 8)."""
+    fn = "i4a16_gemm"
+    lda, ldc = K if a_row_stride is None else a_row_stride, N if c_row_stride is None else c_row_stride
+    _i4_sizes(fn, M | N | K | lda | ldc, K, group)
+    d, st = _here(fn, stream)
+    t = _i4_scale_type(fn, scale_type, WS)
+    _check(fn, (_lib or lib()).i4a16_gemm(_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda),
+                                          *_i4_matrix(fn, "W", W, WS, WZ, 1, N, K, group, d),
+                                          _arg(fn, "C", C, _span(M, ldc, N, 2), d, _BF16, ldc), M, N, K, group, t, lda, ldc, st))
+
+
+def i4a16_gated(A, WG, WGS, WGZ, WU, WUS, WUZ, C, M: int, N: int, K: int, group: int, a_row_stride: int | None = None,
+                c_row_stride: int | None = None, scale_type: int | None = None, stream=None) -> None:
+    """C = silu(A WG^T) * (A WU^T)."""
+    fn = "i4a16_gated"
+    lda, ldc = K if a_row_stride is None else a_row_stride, N if c_row_stride is None else c_row_stride
+    _i4_sizes(fn, M | N | K | lda | ldc, K, group)
+    d, st = _here(fn, stream)
+    t = _i4_scale_type(fn, scale_type, WGS, WUS)
+    _check(fn, (_lib or lib()).i4a16_gated(_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda),
+                                           *_i4_matrix(fn, "WG", WG, WGS, WGZ, 1, N, K, group, d),
+                                           *_i4_matrix(fn, "WU", WU, WUS, WUZ, 1, N, K, group, d),
+                                           _arg(fn, "C", C, _span(M, ldc, N, 2), d, _BF16, ldc), M, N, K, group, t, lda, ldc, st))
+
+
+def moe_route(logits, bias, ids, weights, T: int, E: int, top_k: int, scoring="softmax", groups: int = 1,
+              top_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+              row_stride: int | None = None, logits_type: int | None = None, stream=None) -> None:
+    """Each token's experts and their weights from its logits; `scoring` is "softmax"
+    or "sigmoid", bias [E] or None.  The type of the logits is the tensor's; with
+    an address pass `logits_type` (default BF16)."""
+    fn, ld = "moe_route", E if row_stride is None else row_stride
+    _moe_sizes(fn, T, E, top_k, ld, groups, top_groups, group_top)
+    if not isinstance(scoring, (str, int)) or scoring not in _SCORING:
+        raise ValueError(f"{fn}: scoring {scoring!r} is neither 'softmax' nor 'sigmoid'")
+    d, st = _here(fn, stream)
+    t = _type_of(fn, logits, logits_type)
+    _check(fn, (_lib or lib()).moe_route(_arg(fn, "logits", logits, _span(T, ld, E, 4 if t == TYPE_FP32 else 2), d, _VALUES, ld), t,
+                                         _arg(fn, "bias", bias, 4 * E, d, _FP32), _arg(fn, "ids", ids, 4 * T * top_k, d, _INT32, top_k),
+                                         _arg(fn, "weights", weights, 4 * T * top_k, d, _FP32, top_k), T, E, top_k, ld,
+                                         _SCORING[scoring], groups, top_groups, group_top, bool(renormalize), scale, st))
+
+
+def _moe_sizes(fn: str, *sizes: int) -> None:
+    for n in sizes:
+        if n >> 32:
+            raise ValueError(f"{fn}: sizes and strides must be from 0 to 2^32 - 1")
+
+
+def moe_lists(ids, order, offsets, T: int, top_k: int, E: int, stream=None) -> None:
+    """Each expert's pairs (token * top_k + slot), expert by expert."""
+    fn = "moe_lists"
+    _moe_sizes(fn, T, top_k, E)
+    d, st = _here(fn, stream)
+    _check(fn, (_lib or lib()).moe_lists(_arg(fn, "ids", ids, 4 * T * top_k, d, _INT32, top_k),
+                                         _arg(fn, "order", order, 4 * T * top_k, d, _INT32),
+                                         _arg(fn, "offsets", offsets, 4 * (E + 1), d, _INT32), T, top_k, E, st))
+
+
+def i4a16_experts_gated(A, ids, order, offsets, WG, WGS, WGZ, WU, WUS, WUZ, H, T: int, top_k: int, E: int, N: int, K: int,
+                        group: int, a_row_stride: int | None = None, scale_type: int | None = None, stream=None) -> None:
+    """A row of H per pair: the gated product of the token's row with its expert's
+    matrices.  order and offsets are moe_lists', or both None for a few tokens."""
+    fn, lda = "i4a16_experts_gated", K if a_row_stride is None else a_row_stride
+    _i4_sizes(fn, T | top_k | E | N | K | lda, K, group)
+    d, st = _here(fn, stream)
+    t = _i4_scale_type(fn, scale_type, WGS, WUS)
+    pairs = T * top_k
+    _check(fn, (_lib or lib()).i4a16_experts_gated(
+        _arg(fn, "A", A, _span(T, lda, K, 2), d, _BF16, lda), _arg(fn, "ids", ids, 4 * pairs, d, _INT32, top_k),
+        _arg(fn, "order", order, 4 * pairs, d, _INT32), _arg(fn, "offsets", offsets, 4 * (E + 1), d, _INT32),
+        *_i4_matrix(fn, "WG", WG, WGS, WGZ, E, N, K, group, d), *_i4_matrix(fn, "WU", WU, WUS, WUZ, E, N, K, group, d),
+        _arg(fn, "H", H, 2 * pairs * N, d, _BF16, N), T, top_k, E, N, K, group, t, lda, st))
+
+
+def i4a16_experts_down(H, ids, weights, order, offsets, W, WS, WZ, Y, C, T: int, top_k: int, E: int, N: int, K: int,
+                       group: int, c_row_stride: int | None = None, scale_type: int | None = None, stream=None) -> None:
+    """The weighted sum over each token's experts of its pairs' rows of H times their
+    matrices.  With lists Y is scratch, fp32 [T * top_k][N]; without it may be None."""
+    fn, ldc = "i4a16_experts_down", N if c_row_stride is None else c_row_stride
+    _i4_sizes(fn, T | top_k | E | N | K | ldc, K, group)
+    d, st = _here(fn, stream)
+    t = _i4_scale_type(fn, scale_type, WS)
+    pairs = T * top_k
+    _check(fn, (_lib or lib()).i4a16_experts_down(
+        _arg(fn, "H", H, 2 * pairs * K, d, _BF16, K), _arg(fn, "ids", ids, 4 * pairs, d, _INT32, top_k),
+        _arg(fn, "weights", weights, 4 * pairs, d, _FP32, top_k), _arg(fn, "order", order, 4 * pairs, d, _INT32),
+        _arg(fn, "offsets", offsets, 4 * (E + 1), d, _INT32), *_i4_matrix(fn, "W", W, WS, WZ, E, N, K, group, d),
+        _arg(fn, "Y", Y, 4 * pairs * N, d, _FP32, N), _arg(fn, "C", C, _span(T, ldc, N, 2), d, _BF16, ldc),
+        T, top_k, E, N, K, group, t, ldc, st))
 
 
 # ------------------------------------------------------------ host helpers
