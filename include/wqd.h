@@ -351,22 +351,28 @@ int w4a4_gated(const void *A, const void *AS, const void *WG, const void *WGS, c
  *   w[n,k] = (q[n,k] - z[n,k/group]) * s[n,k/group],
  *   q  codes 0 .. 15;  s  FP16 or BF16 [N][K/group];  z  uint8 [N][K/group], or
  *   NULL: 8 everywhere;  group  32, 64 or 128.
- * Scales and zero points lie row by row; the codes are laid out once, by
- * i4_pack, in tiles of 16 rows x 128 k (rows padded to whole tiles):
- *   uint8 [ceil(N/16)][K/128][1024]; byte 256 g + 16 n + 4 j + b of a tile (g, j, b
- *   0 .. 3, n 0 .. 15) holds the codes of row n of the tile at k = 32 j + 8 g + i, for
- *   b = 0 .. 3 of i = 0 and 2, 4 and 6, 1 and 3, 5 and 7, the first in the low nibble.
- * Several matrices of one size (experts) lie one after another: codes at
- * i4_packed_bytes(N, K) apart, scales and zero points [E][N][K/group].
+ * The three are laid out once, by i4_pack, in tiles of 16 rows (padded with zeros
+ * to whole tiles) x 128 k, row tile by row tile:
+ *   codes   uint8 [ceil(N/16)][K/128][1024]; byte 256 g + 16 n + 4 j + b of a tile (g, j,
+ *           b 0 .. 3, n 0 .. 15) holds the codes of row n at k = 32 j + 8 g + i, for b = 0
+ *           .. 3 of i = 0 and 2, 4 and 6, 1 and 3, 5 and 7, the first in the low nibble
+ *   scales  [ceil(N/16)][K/128][16][128/group], zero points likewise (uint8)
+ * Several matrices of one size (experts) lie one after another.
  *
- * i4_pack - codes of `count` matrices, uint8 [count][N][K/2] with the even k in
- * the low nibble (4-byte aligned), to that layout in W (16-byte aligned,
- * count * i4_packed_bytes(N, K) bytes; not Q).
+ * i4_pack - `count` matrices, codes uint8 [count][N][K/2] with the even k in the low
+ * nibble, scales and zero points [count][N][K/group], to that layout; the scales'
+ * type does not matter here.
+ *   Q, S, Z     device, 4-, 2- and 1-byte aligned; Z and WZ may both be NULL
+ *   W, WS, WZ   device, 16-byte aligned; count * i4_packed_rows(N) rows of K/2 bytes, K/group
+ *               scales and K/group bytes; not the inputs
+ *   K  a positive multiple of 128, at most WQD_MX_MAX_K;  N  1 .. WQD_MX_MAX_ROWS;
+ *   count  at most WQD_MOE_MAX_EXPERTS (0: nothing is launched)
  */
-int i4_pack(const void *Q, void *W, uint32_t N, uint32_t K, uint32_t count, hipStream_t stream);
+int i4_pack(const void *Q, const void *S, const void *Z, void *W, void *WS, void *WZ,
+            uint32_t N, uint32_t K, uint32_t group, uint32_t count, hipStream_t stream);
 
-/* Bytes of a matrix's laid-out codes: ceil(N/16) * 16 * K/2, or 0 if K % 128 != 0. */
-size_t i4_packed_bytes(uint32_t N, uint32_t K);
+/* Rows of a laid-out matrix: N rounded up to a multiple of 16. */
+uint32_t i4_packed_rows(uint32_t N);
 
 /*
  * i4a16_gemm, i4a16_gated - products with 4-bit integer weights:
@@ -377,9 +383,8 @@ size_t i4_packed_bytes(uint32_t N, uint32_t K);
  * infinity or NaN has no finite output; which of the two it has is not defined.
  *
  *   A   device, BF16, row m at A + m * a_row_stride, 16-byte aligned
- *   W, WS, WZ  device, laid-out codes (16-byte aligned), scales (2 * 128/group
- *       bytes aligned) and zero points (128/group bytes aligned) or NULL; of a gated
- *       product both matrices have zero points or neither
+ *   W, WS, WZ  device, laid-out codes, scales and zero points (or NULL), 16-byte
+ *       aligned; of a gated product both matrices have zero points or neither
  *   C   device, BF16, row m at C + m * c_row_stride, 2-byte aligned; only
  *       columns < N of rows < M are written
  *   M   rows, from one to a long prompt (0: nothing is launched), at most

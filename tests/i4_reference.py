@@ -17,13 +17,25 @@ def laid_out(codes: torch.Tensor) -> torch.Tensor:
     """Codes [E, N, K] in the tiles that include/wqd.h describes, byte by byte."""
     E, N, K = codes.shape
     out = torch.zeros(E, (N + 15) // 16, K // 128, 1024, dtype=torch.uint8)
-    first, second = (0, 4, 1, 5), (2, 6, 3, 7)
+    first, second = (0, 4, 1, 5), (2, 6, 3, 7)  # of byte b
+    row = torch.zeros(E, (N + 15) // 16 * 16, K, dtype=torch.uint8)
+    row[:, :N] = codes
+    row = row.view(E, -1, 16, K // 128, 4, 4, 8)  # k = 32 j + 8 g + i
+    at = out.view(E, -1, K // 128, 4, 16, 4, 4)  # g, n, j, b
+    for g in range(4):
+        for j in range(4):
+            for b in range(4):
+                at[:, :, :, g, :, j, b] = (row[..., j, g, first[b]] | row[..., j, g, second[b]] << 4).transpose(2, 3)
+    return out.view(E, -1)
+
+
+def tiles(x: torch.Tensor, K: int) -> torch.Tensor:
+    """Scales or zero points [E, N, K/group] in the order of the codes' tiles."""
+    E, N, G = x.shape
+    per = G * 128 // K
+    out = torch.zeros(E, (N + 15) // 16, K // 128, 16, per, dtype=x.dtype)
     for n in range(N):
-        row = codes[:, n].view(E, K // 128, 4, 4, 8)  # k = 32 j + 8 g + i
-        for g in range(4):
-            for j in range(4):
-                for b in range(4):
-                    out[:, n // 16, :, 256 * g + 16 * (n % 16) + 4 * j + b] = row[:, :, j, g, first[b]] | row[:, :, j, g, second[b]] << 4
+        out[:, n // 16, :, n % 16] = x[:, n].view(E, K // 128, per)
     return out.view(E, -1)
 
 
@@ -60,7 +72,7 @@ class Weights:
         return (self.codes.double() + 32 + r(self.zero())) * r(self.s.double().abs())
 
     def operands(self, device="cuda"):
-        return (laid_out(self.codes).to(device), self.s.to(device), None if self.z is None else self.z.to(device))
+        return (laid_out(self.codes).to(device), tiles(self.s, self.K).to(device), None if self.z is None else tiles(self.z, self.K).to(device))
 
 
 def silu(x):

@@ -30,15 +30,18 @@ def untouched(C, M, N):
     return bool((C[M:] == CANARY).all() and (C[:M, N:] == CANARY).all())
 
 
-@pytest.mark.parametrize("E,N,K", [(1, 1, 128), (1, 16, 256), (3, 17, 384), (2, 100, 1152)])
-def test_pack(E, N, K):
-    codes = torch.randint(0, 16, (E, N, K), generator=ref.generator(E, N, K), dtype=torch.uint8)
-    size = wqd.i4_packed_bytes(N, K)
-    assert size == -(-N // 16) * 16 * K // 2
-    W = torch.full((E * size + 32,), 0xA5, dtype=torch.uint8, device="cuda")
-    wqd.i4_pack(ref.rows_of_pairs(codes).cuda(), W, N, K, E)
-    W = W.cpu()
-    assert torch.equal(W[: E * size], ref.laid_out(codes).flatten()) and bool((W[E * size:] == 0xA5).all())
+@pytest.mark.parametrize("scale,zeros", [("fp16", True), ("bf16", False)])
+@pytest.mark.parametrize("E,N,K,group", [(1, 1, 128, 128), (1, 16, 256, 64), (3, 17, 384, 32), (2, 100, 1152, 64), (5, 33, 128, 128)])
+def test_pack(E, N, K, group, scale, zeros):
+    w = ref.Weights(ref.generator(E, N, K), E, N, K, group, zeros, scale)
+    n = E * wqd.i4_packed_rows(N) * K
+    W = torch.full((n // 2 + 32,), 0xA5, dtype=torch.uint8, device="cuda")
+    S = torch.full((n // group + 32,), CANARY, dtype=w.s.dtype, device="cuda")
+    Z = torch.full((n // group + 32,), 0xA5, dtype=torch.uint8, device="cuda") if zeros else None
+    wqd.i4_pack(ref.rows_of_pairs(w.codes).cuda(), w.s.cuda(), w.z.cuda() if zeros else None, W, S, Z, N, K, group, E)
+    for got, want, size, fill in zip((W, S, Z), w.operands("cpu"), (n // 2, n // group, n // group), (0xA5, CANARY, 0xA5)):
+        if want is not None:
+            assert torch.equal(got[:size].cpu(), want.flatten()) and bool((got[size:] == fill).all())
 
 
 @pytest.mark.parametrize("scale", ["fp16", "bf16"])

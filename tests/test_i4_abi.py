@@ -7,7 +7,7 @@ from weight_quantized_decode_block_amd import wqd
 P = 0x7F0000000000  # 16-byte aligned, never dereferenced
 OK, EINVAL, ENULL, EALIGN, EUNSUPPORTED = wqd.WQD_OK, wqd.WQD_EINVAL, wqd.WQD_ENULL, wqd.WQD_EALIGN, wqd.WQD_EUNSUPPORTED
 
-PACK = dict(Q=P, W=P, N=17, K=256, count=2)
+PACK = dict(Q=P, S=P, Z=P, W=P, WS=P, WZ=P, N=17, K=256, group=64, count=2)
 GEMM = dict(A=P, W=P, WS=P, WZ=P, C=P, M=3, N=17, K=256, group=64, t=1, lda=256, ldc=17)
 GATED = dict(A=P, W=P, WS=P, WZ=P, WU=P, WUS=P, WUZ=P, C=P, M=3, N=17, K=256, group=64, t=1, lda=256, ldc=17)
 ROUTE = dict(logits=P, t=2, bias=P, ids=P, weights=P, T=5, E=64, top_k=4, ld=64, scoring=0, groups=8, top_groups=2, group_top=2, renorm=1, scale=1.0)
@@ -34,8 +34,7 @@ def refused(fn, change, code, frag):
     (dict(K=0), EINVAL, "multiple of 128"), (dict(K=192), EINVAL, "multiple of 128"), (dict(group=16), EINVAL, "group"),
     (dict(group=256), EINVAL, "group"), (dict(t=2), EINVAL, "scale type"), (dict(t=3), EINVAL, "scale type"),
     (dict(K=(1 << 20) + 128, lda=(1 << 20) + 128), EUNSUPPORTED, "above"), (dict(N=(1 << 24) + 1, ldc=(1 << 24) + 1), EUNSUPPORTED, "above"),
-    (dict(W=P + 8), EALIGN, "weights"), (dict(WS=P + 2), EALIGN, "scales"), (dict(WS=P + 4, group=32), EALIGN, "scales"),
-    (dict(WZ=P + 1), EALIGN, "zero points"), (dict(WZ=P + 2, group=32), EALIGN, "zero points"),
+    (dict(W=P + 8), EALIGN, "weights"), (dict(WS=P + 8), EALIGN, "scales"), (dict(WZ=P + 8), EALIGN, "zero points"),
 ])
 def test_product_refusals(fn, change, code, frag):
     refused(fn, {k: v for k, v in change.items() if k in CALLS[fn]}, code, frag)
@@ -51,7 +50,9 @@ def test_product_refusals(fn, change, code, frag):
     ("i4a16_gated", dict(WUZ=P + 1), EALIGN, "zero points"), ("i4a16_experts_gated", dict(WUZ=None), ENULL, "both"),
     ("i4_pack", dict(Q=None), ENULL, "non-NULL"), ("i4_pack", dict(W=None), ENULL, "non-NULL"), ("i4_pack", dict(N=0), EINVAL, "N must"),
     ("i4_pack", dict(K=64), EINVAL, "multiple of 128"), ("i4_pack", dict(count=1025), EUNSUPPORTED, "count"), ("i4_pack", dict(Q=P + 2), EALIGN, "Q must"),
-    ("i4_pack", dict(W=P + 8), EALIGN, "W must"), ("i4_pack", dict(K=(1 << 20) + 128), EUNSUPPORTED, "above"), ("i4_pack", dict(N=(1 << 24) + 1), EUNSUPPORTED, "above"),
+    ("i4_pack", dict(W=P + 8), EALIGN, "16-byte"), ("i4_pack", dict(WS=P + 8), EALIGN, "16-byte"), ("i4_pack", dict(WZ=P + 8), EALIGN, "16-byte"),
+    ("i4_pack", dict(S=None), ENULL, "non-NULL"), ("i4_pack", dict(WS=None), ENULL, "non-NULL"), ("i4_pack", dict(Z=None), ENULL, "both"),
+    ("i4_pack", dict(WZ=None), ENULL, "both"), ("i4_pack", dict(group=96), EINVAL, "group"), ("i4_pack", dict(S=P + 1), EALIGN, "2-byte"), ("i4_pack", dict(K=(1 << 20) + 128), EUNSUPPORTED, "above"), ("i4_pack", dict(N=(1 << 24) + 1), EUNSUPPORTED, "above"),
 ])
 def test_refusals_of_one_form(fn, change, code, frag):
     refused(fn, change, code, frag)
@@ -94,7 +95,7 @@ def test_experts_refusals(fn, change, code, frag):
 
 def test_nothing_to_do():
     """No rows, no tokens, no matrices: nothing is launched, and what holds them may be NULL; the rest is checked."""
-    assert call("i4_pack", dict(count=0, Q=None, W=None)) == OK
+    assert call("i4_pack", dict(count=0, Q=None, S=None, Z=None, W=None, WS=None, WZ=None)) == OK
     for fn in PRODUCTS[:2]:
         assert call(fn, dict(M=0, A=None, C=None)) == OK
         assert call(fn, dict(M=0, W=None)) == ENULL
@@ -105,6 +106,5 @@ def test_nothing_to_do():
     assert call("i4a16_experts_down", dict(T=0, group=48)) == EINVAL
 
 
-def test_packed_bytes():
-    assert wqd.i4_packed_bytes(1, 128) == 1024 and wqd.i4_packed_bytes(17, 256) == 4096 and wqd.i4_packed_bytes(16, 100) == 0
-    assert wqd.i4_packed_bytes(1 << 24, 1 << 20) == 1 << 43
+def test_packed_rows():
+    assert [wqd.i4_packed_rows(n) for n in (1, 16, 17, 1 << 24)] == [16, 16, 32, 1 << 24]

@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "libwqd.so")
 # bench-only helper (a plain read of a buffer: the read ceiling bench.py reports)
 BENCH_LIB = os.path.join(PKG, "libwqd_bench.so")
 SOURCES = ["api.cpp", "pack.cpp", "q2_0_mfma.hip", "q2_0_valu.hip", "w8a16_gemm_m16.hip", "w8a16_gemv.hip",
-           "mx_quant.hip", "mx_skinny.hip", "mx_tile.hip", "i4_pack.hip", "i4_skinny.hip", "moe_route.hip"]
+           "mx_quant.hip", "mx_skinny.hip", "mx_tile.hip", "i4_pack.hip", "i4_skinny.hip", "i4_tile.hip", "moe_route.hip"]
 ARCH = "gfx950"
 JOBS = 6  # sources compiled at once
 

@@ -211,13 +211,11 @@ int validate_i4(const char *fn, const wqd::I4Operands &op, bool both, uint32_t s
     return fail(WQD_EINVAL, "%s: a_row_stride=%u is not a multiple of 8 (16-byte activation rows)", fn, op.lda);
   if (op.lda > WQD_MX_MAX_STRIDE)
     return fail(WQD_EUNSUPPORTED, "%s: a_row_stride=%u above %u", fn, op.lda, (unsigned)WQD_MX_MAX_STRIDE);
-  const uintptr_t values = 128u / op.group;  // of a row's 128 k, read at once
   if (!aligned(op.A, 16)) return fail(WQD_EALIGN, "%s: activations must be 16-byte aligned", fn);
   if (!aligned(op.w.W, 16) || !aligned(op.up.W, 16)) return fail(WQD_EALIGN, "%s: weights must be 16-byte aligned", fn);
-  if (!aligned(op.w.S, 2 * values) || !aligned(op.up.S, 2 * values))
-    return fail(WQD_EALIGN, "%s: scales must be %u-byte aligned", fn, (unsigned)(2 * values));
-  if (!aligned(op.w.Z, values) || !aligned(op.up.Z, values))
-    return fail(WQD_EALIGN, "%s: zero points must be %u-byte aligned", fn, (unsigned)values);
+  if (!aligned(op.w.S, 16) || !aligned(op.up.S, 16)) return fail(WQD_EALIGN, "%s: scales must be 16-byte aligned", fn);
+  if (!aligned(op.w.Z, 16) || !aligned(op.up.Z, 16))
+    return fail(WQD_EALIGN, "%s: zero points must be 16-byte aligned", fn);
   if (!aligned(op.C, 2)) return fail(WQD_EALIGN, "%s: C must be 2-byte aligned", fn);
   return WQD_OK;
 }
@@ -229,7 +227,7 @@ int run_i4_product(const char *fn, wqd::I4Operands op, uint32_t scale_type, hipS
   if (op.M == 0) return WQD_OK;  // no rows: nothing to launch
   if (int rc = check_device(fn)) return rc;
   (void)hipGetLastError();
-  return check_launch(fn, wqd::launch_i4_skinny(op, op.gated, stream));
+  return check_launch(fn, wqd::launch_i4_product(op, stream));
 }
 
 // Sizes of a routed call.
@@ -254,11 +252,11 @@ int run_i4_experts(const char *fn, wqd::I4Operands op, uint32_t scale_type, hipS
     return fail(WQD_EALIGN, "%s: ids, weights and lists must be 4-byte aligned", fn);
   if (!aligned(op.Y, 16)) return fail(WQD_EALIGN, "%s: Y must be 16-byte aligned", fn);
   if (op.T == 0) return WQD_OK;
-  if (wqd::i4_experts_grid(op) > wqd::i4_experts_max_grid())
+  if (!wqd::i4_experts_fit(op))
     return fail(WQD_EUNSUPPORTED, "%s: T=%u tokens of top_k=%u experts times N=%u are too many for one call", fn, op.T, op.top_k, op.N);
   if (int rc = check_device(fn)) return rc;
   (void)hipGetLastError();
-  if (int rc = check_launch(fn, wqd::launch_i4_experts_skinny(op, stream))) return rc;
+  if (int rc = check_launch(fn, wqd::launch_i4_experts(op, stream))) return rc;
   return !op.gated && op.order ? check_launch(fn, wqd::launch_moe_combine(op, stream)) : WQD_OK;
 }
 
@@ -479,27 +477,29 @@ int w4a4_gated(const void *A, const void *AS, const void *WG, const void *WGS, c
                         wqd::MxFormat::kFp4, true, stream);
 }
 
-int i4_pack(const void *Q, void *W, uint32_t N, uint32_t K, uint32_t count, hipStream_t stream) {
+int i4_pack(const void *Q, const void *S, const void *Z, void *W, void *WS, void *WZ, uint32_t N, uint32_t K,
+            uint32_t group, uint32_t count, hipStream_t stream) {
   static const char fn[] = "i4_pack";
-  if (count && (!Q || !W)) return fail(WQD_ENULL, "%s: Q and W must be non-NULL", fn);
+  if (count && (!Q || !S || !W || !WS)) return fail(WQD_ENULL, "%s: Q, S, W and WS must be non-NULL", fn);
+  if (count && !Z != !WZ) return fail(WQD_ENULL, "%s: Z and WZ must both be given or both be NULL", fn);
   if (N == 0) return fail(WQD_EINVAL, "%s: N must be >= 1", fn);
   if (K == 0 || K % 128u != 0) return fail(WQD_EINVAL, "%s: K=%u is not a positive multiple of 128", fn, K);
+  if (group != 32u && group != 64u && group != 128u)
+    return fail(WQD_EINVAL, "%s: group=%u is not 32, 64 or 128", fn, group);
   if (K > WQD_MX_MAX_K) return fail(WQD_EUNSUPPORTED, "%s: K=%u above %u", fn, K, (unsigned)WQD_MX_MAX_K);
   if (N > WQD_MX_MAX_ROWS) return fail(WQD_EUNSUPPORTED, "%s: N=%u above %u", fn, N, (unsigned)WQD_MX_MAX_ROWS);
   if (count > WQD_MOE_MAX_EXPERTS)
     return fail(WQD_EUNSUPPORTED, "%s: count=%u above %u", fn, count, (unsigned)WQD_MOE_MAX_EXPERTS);
-  if (!aligned(Q, 4)) return fail(WQD_EALIGN, "%s: Q must be 4-byte aligned", fn);
-  if (!aligned(W, 16)) return fail(WQD_EALIGN, "%s: W must be 16-byte aligned", fn);
+  if (!aligned(Q, 4) || !aligned(S, 2)) return fail(WQD_EALIGN, "%s: Q must be 4-byte and S 2-byte aligned", fn);
+  if (!aligned(W, 16) || !aligned(WS, 16) || !aligned(WZ, 16))
+    return fail(WQD_EALIGN, "%s: W, WS and WZ must be 16-byte aligned", fn);
   if (count == 0) return WQD_OK;
   if (int rc = check_device(fn)) return rc;
   (void)hipGetLastError();
-  return check_launch(fn, wqd::launch_i4_pack(Q, W, N, K, count, stream));
+  return check_launch(fn, wqd::launch_i4_pack(Q, i4_matrix(static_cast<uint8_t *>(W), WS, WZ), S, Z, N, K, group, count, stream));
 }
 
-size_t i4_packed_bytes(uint32_t N, uint32_t K) {
-  if (K % 128u != 0) return 0;
-  return (static_cast<size_t>(N) + 15u) / 16u * 16u * (K / 2u);
-}
+uint32_t i4_packed_rows(uint32_t N) { return N > WQD_MX_MAX_ROWS ? 0u : (N + 15u) / 16u * 16u; }
 
 int i4a16_gemm(const void *A, const void *W, const void *WS, const void *WZ, void *C, uint32_t M, uint32_t N, uint32_t K,
                uint32_t group, uint32_t scale_type, uint32_t a_row_stride, uint32_t c_row_stride, hipStream_t stream) {

@@ -6,6 +6,9 @@
 // order: lane (n, g) = (lane % 16, lane / 16) has the 16 bytes at 16 * lane, and
 // dword j of them is k = 32 j + 8 g .. + 7 of row n.  Nibbles p and p + 4 of a
 // dword are elements 2p and 2p + 1, so that one shift and one mask give a pair.
+// A tile's scales and zero points are [16 rows][128/group]: one piece of memory
+// too.  Row by row, as they come, a load touches a line for each of 16 rows, and these
+// cost more than the codes: 1 x 5120, K = 5120 8.0 us, laid out so 6.4 (with the kernels of then).
 #pragma once
 
 #include "mx_common.h"
@@ -34,32 +37,33 @@ __device__ __forceinline__ float i4_scale(uint32_t bits, bool bf) {
   return bf ? b : h;
 }
 
-// The scales (zero points) of a row's 128 k: NG of them, one load (rows of
-// scales are whole such loads, so it is aligned).
+// The scales (zero points) of a row of a tile: NG of them, one load.
 template <int NG>
 struct I4Groups {
   uint32_t s[NG == 4 ? 2 : 1], z;
 };
 template <int NG, bool ZEROS>
-__device__ __forceinline__ I4Groups<NG> i4_load_groups(const uint16_t *s, const uint8_t *z, uint32_t at) {
+__device__ __forceinline__ I4Groups<NG> i4_load_groups(const uint16_t *s, const uint8_t *z, uint32_t row) {
   I4Groups<NG> r;
+  s += row * NG;
+  z += row * NG;
   if constexpr (NG == 4) {
-    const u32x2_t v = *reinterpret_cast<const u32x2_t *>(s + at);
+    const u32x2_t v = *reinterpret_cast<const u32x2_t *>(s);
     r.s[0] = v.x;
     r.s[1] = v.y;
   } else if constexpr (NG == 2) {
-    r.s[0] = *reinterpret_cast<const uint32_t *>(s + at);
+    r.s[0] = *reinterpret_cast<const uint32_t *>(s);
   } else {
-    r.s[0] = s[at];
+    r.s[0] = *s;
   }
   if constexpr (!ZEROS)
     r.z = 0x08080808u;
   else if constexpr (NG == 4)
-    r.z = *reinterpret_cast<const uint32_t *>(z + at);
+    r.z = *reinterpret_cast<const uint32_t *>(z);
   else if constexpr (NG == 2)
-    r.z = *reinterpret_cast<const uint16_t *>(z + at);
+    r.z = *reinterpret_cast<const uint16_t *>(z);
   else
-    r.z = z[at];
+    r.z = *z;
   return r;
 }
 template <int NG>
@@ -76,16 +80,15 @@ __device__ __forceinline__ float i4_zero_of(const I4Groups<NG> &x, int i) {
 // they are; false past the last one.  All lanes of a wave call it.  Places are
 // held to the pairs that there are, whatever the lists say.
 template <uint32_t CHUNK>
-__device__ __forceinline__ bool i4_find_chunk(const I4Operands &op, uint32_t chunk, uint32_t lane, uint32_t &expert,
-                                              uint32_t &first, uint32_t &rows) {
-  const uint32_t pairs = op.T * op.top_k;
+__device__ __forceinline__ bool i4_find_chunk(const int32_t *offsets, uint32_t E, uint32_t pairs, uint32_t chunk,
+                                              uint32_t lane, uint32_t &expert, uint32_t &first, uint32_t &rows) {
   uint32_t before = 0;
-  for (uint32_t e0 = 0; e0 < op.E; e0 += 64u) {
+  for (uint32_t e0 = 0; e0 < E; e0 += 64u) {
     const uint32_t e = e0 + lane;
     uint32_t lo = 0, hi = 0;
-    if (e < op.E) {
-      lo = (uint32_t)op.offsets[e];
-      hi = (uint32_t)op.offsets[e + 1u];
+    if (e < E) {
+      lo = (uint32_t)offsets[e];
+      hi = (uint32_t)offsets[e + 1u];
     }
     lo = lo < pairs ? lo : pairs;
     hi = hi < pairs ? hi : pairs;

@@ -26,7 +26,10 @@
 namespace wqd {
 namespace {
 
-constexpr int NW = 8;  // waves of a workgroup
+// Waves of a workgroup, and steps in flight.  4 or 16 waves, and 1, 3, 4 or 6 steps, are slower at most sizes
+// (1 x 5120, K = 5120 6.0 us; 16 waves 7.9, 4 waves 7.3, 3 steps 6.3, 4 steps 6.4): the registers of a deeper
+// ring keep further workgroups off the compute unit.
+constexpr int NW = 8, DEPTH = 2;
 
 // Where a workgroup's rows come from.
 constexpr int kDense = 0;  // rows m0 ..
@@ -34,64 +37,70 @@ constexpr int kLists = 1;  // rows of one expert's list
 constexpr int kPairs = 2;  // one row, of one token and slot
 constexpr int kSum = 3;    // one token's slots, one after another, weighted and added
 
-template <int MMAX, bool GATED, int NG, bool ZEROS, int ROWS, int DEPTH>
-__global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(I4Operands op) {
-  constexpr int MT = (MMAX + 15) / 16, G = GATED ? 2 : 1, SA = (MMAX + 3) / 4;
+// What is not needed before the first loads.
+struct Rest {
+  const uint8_t *ZU;
+  uint16_t *C;
+  float *Y;
+  const int32_t *ids, *order, *offsets;
+  const float *weights;
+  uint32_t ldc, scale_bf16, top_k, E;
+};
+
+// NT: 16-row weight tiles of a workgroup (of either matrix); the arguments up to
+// SU are in registers when a wave starts.  M: rows, or tokens.
+template <int MMAX, int NT, bool GATED, int NG, bool ZEROS, int ROWS>
+__global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__restrict__ W, const uint16_t *__restrict__ S,
+                                                            const uint16_t *__restrict__ A, uint32_t K, uint32_t N,
+                                                            uint32_t M, uint32_t lda, const uint8_t *__restrict__ Z,
+                                                            const uint8_t *__restrict__ WU, const uint16_t *__restrict__ SU,
+                                                            Rest op) {
+  constexpr int MT = (MMAX + 15) / 16, G = GATED ? 2 : 1, WT = NT * G, SA = (MMAX + 3) / 4;
   constexpr uint32_t kLanes = MMAX <= 4 ? 16 : 64;  // lanes that end with rows below MMAX
-  constexpr uint32_t kARegion = MMAX * 256, kParts = NW * G * MT * kLanes * 16;
+  constexpr uint32_t kARegion = MMAX * 256, kParts = NW * WT * MT * kLanes * 16;
   constexpr uint32_t kLds = NW * kARegion > kParts ? NW * kARegion : kParts;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
 
   const uint32_t tid = threadIdx.x, lane = tid & 63u, r = lane & 15u, g = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const uint32_t tiles = (op.N + 15u) >> 4, kt = op.K >> 7, pairs = op.T * op.top_k;
+  const uint32_t tiles = (N + 15u) >> 4, kt = K >> 7, tile = blockIdx.x * NT;
 
   // which rows and which matrix
-  uint32_t block = blockIdx.x, tile, first = 0, rows = 1, expert = 0;
+  uint32_t first = blockIdx.y, rows = 1, expert = 0;  // first: row, place in the lists, pair or token
   if constexpr (ROWS == kDense) {
-    const uint32_t chunks = (op.M + MMAX - 1u) / MMAX;
-    tile = block / chunks;
-    first = (block - tile * chunks) * MMAX;
-    rows = op.M - first < (uint32_t)MMAX ? op.M - first : (uint32_t)MMAX;
+    first *= MMAX;
+    rows = M - first < (uint32_t)MMAX ? M - first : (uint32_t)MMAX;
   } else if constexpr (ROWS == kLists) {
-    const uint32_t chunk = block / tiles;
-    tile = block - chunk * tiles;
-    if (!i4_find_chunk<MMAX>(op, chunk, lane, expert, first, rows)) return;
-  } else {
-    first = block / tiles;  // pair, or token
-    tile = block - first * tiles;
-    if constexpr (ROWS == kPairs) {
-      expert = (uint32_t)op.ids[first];
-      if (expert >= op.E) return;
-    }
+    if (!i4_find_chunk<MMAX>(op.offsets, op.E, M * op.top_k, blockIdx.y, lane, expert, first, rows)) return;
+  } else if constexpr (ROWS == kPairs) {
+    expert = (uint32_t)op.ids[first];
+    if (expert >= op.E) return;
   }
-  // the row of A that row m of this workgroup multiplies, and the row it writes
+  // pair of row m of this workgroup, and the row of A that it multiplies
   auto pair_of = [&](uint32_t m) __attribute__((always_inline)) {
     if constexpr (ROWS == kLists) {
       const uint32_t p = (uint32_t)op.order[first + (m < rows ? m : rows - 1u)];
-      return p < pairs ? p : 0u;
+      return p < M * op.top_k ? p : 0u;
     } else {
       return first;
     }
   };
   auto source = [&](uint32_t m) __attribute__((always_inline)) {
     if constexpr (ROWS == kDense) return first + (m < rows ? m : rows - 1u);
+    if constexpr (ROWS == kSum) return 0u;
     return GATED ? pair_of(m) / op.top_k : pair_of(m);
   };
 
-  // this wave's tiles: of one row of tiles, or of all slots' after another
+  // this wave's steps: the tiles of a row of tiles, or of all slots' after another
   const uint32_t total = ROWS == kSum ? kt * op.top_k : kt;
-  const uint32_t u0 = (uint32_t)((uint64_t)total * wave / NW), u1 = (uint32_t)((uint64_t)total * (wave + 1u) / NW);
-  const uint32_t n = tile * 16u + r, nn = n < op.N ? n : op.N - 1u;
-  const uint32_t srow = op.K / (128u / NG), scale_at = (nn - tile * 16u) * srow;
+  const uint32_t u0 = total * wave / NW, u1 = total * (wave + 1u) / NW;
 
   const u32x4_t *arow[SA];  // of each 16-byte piece that this lane brings
 #pragma unroll
-  for (int i = 0; i < SA; ++i)
-    arow[i] = reinterpret_cast<const u32x4_t *>(op.A + (uint64_t)(ROWS == kSum ? 0u : source(i * 4u + g)) * op.lda) + r;
+  for (int i = 0; i < SA; ++i) arow[i] = reinterpret_cast<const u32x4_t *>(A + (uint64_t)source(i * 4u + g) * lda) + r;
   struct Step {
-    u32x4_t w[G], a[SA];
-    I4Groups<NG> s[G];
+    u32x4_t w[WT], a[SA];
+    I4Groups<NG> s[WT];
     float weight;
     uint32_t here;
   };
@@ -108,37 +117,36 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(I4Operands op) {
       x.here = e < op.E;
       e = x.here ? e : 0u;
       x.weight = op.weights[p];
-      a0 = (uint64_t)p * op.lda / 8u;
+      a0 = (uint64_t)p * lda / 8u;
     }
     // an offset that the compiler cannot follow from step to step: it would keep a pointer for every request in flight
     asm volatile("" : "+s"(t));
-    const uint64_t wt = (((uint64_t)e * tiles + tile) * kt + t) * kI4Tile;
-    const uint64_t st = ((uint64_t)e * op.N + tile * 16u) * srow + t * NG;
 #pragma unroll
-    for (int m = 0; m < G; ++m) {
-      const I4Matrix &mat = m ? op.up : op.w;
-      x.w[m] = *reinterpret_cast<const u32x4_t *>(mat.W + wt + lane * 16u);
-      x.s[m] = i4_load_groups<NG, ZEROS>(mat.S + st, mat.Z + st, scale_at);
+    for (int j = 0; j < WT; ++j) {
+      const uint32_t row = NT == 1 || tile + j / G < tiles ? tile + j / G : tiles - 1u;
+      const uint64_t at = ((uint64_t)e * tiles + row) * kt + t;
+      const bool up = GATED && (j & 1);
+      x.w[j] = *reinterpret_cast<const u32x4_t *>((up ? WU : W) + at * kI4Tile + lane * 16u);
+      x.s[j] = i4_load_groups<NG, ZEROS>((up ? SU : S) + at * (16u * NG), (up ? op.ZU : Z) + at * (16u * NG), r);
     }
 #pragma unroll
     for (int i = 0; i < SA; ++i) x.a[i] = arow[i][a0 + t * 16u];
     return x;
   };
 
-  f32x4_t acc[G][MT];
+  f32x4_t acc[WT][MT];
 #pragma unroll
-  for (int m = 0; m < G; ++m)
+  for (int t = 0; t < WT; ++t)
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[m][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < MT; ++i) acc[t][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   uint8_t *mine = lds + wave * kARegion;
-  const bool bf = op.scale_bf16;
   const u32x4_t one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
   const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, one);
   auto compute = [&](Step x) __attribute__((always_inline)) {
     if (ROWS == kSum && !x.here) return;
     // conversions stay with their own step: of several steps at once they would take twice the registers
 #pragma unroll
-    for (int m = 0; m < G; ++m) asm volatile("" : "+v"(x.w[m]));
+    for (int t = 0; t < WT; ++t) asm volatile("" : "+v"(x.w[t]));
     // Piece p of row m lies in slot p ^ (m % 16): the sixteen lanes that a
     // 16-byte LDS read serves together meet all 64 banks.
 #pragma unroll
@@ -162,14 +170,14 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(I4Operands op) {
           sum[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], ones, sum[q], 0, 0, 0);
       }
 #pragma unroll
-      for (int t = 0; t < G; ++t)
+      for (int t = 0; t < WT; ++t)
 #pragma unroll
         for (int q = 0; q < NG; ++q) {
           f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int j = q * 4 / NG; j < (q + 1) * 4 / NG; ++j)
             p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], i4_biased(x.w[t][j]), p, 0, 0, 0);
-          const float s = i4_scale_of(x.s[t], q, bf) * (ROWS == kSum ? x.weight : 1.0f);
+          const float s = i4_scale_of(x.s[t], q, op.scale_bf16) * (ROWS == kSum ? x.weight : 1.0f);
           const float z = -kI4Bias - i4_zero_of(x.s[t], q);
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[t][i][c] = __builtin_fmaf(s, __builtin_fmaf(z, sum[q][c], p[c]), acc[t][i][c]);
@@ -181,7 +189,8 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(I4Operands op) {
     Step ring[DEPTH];
     mx_unroll<0, DEPTH>([&](auto d) __attribute__((always_inline)) { ring[decltype(d)::value] = load(u0 + decltype(d)::value); });
     uint32_t u = u0;
-    // whole rounds of the ring, so that the compiler's waits count the requests in flight
+    // Whole rounds of the ring without a branch, so that the compiler's waits count the requests in flight; those
+    // past the last step ask for it once more (with a branch around each 1 x 5120, K = 5120 6.4 instead of 6.0 us).
     while (u + DEPTH < u1) {
       mx_unroll<0, DEPTH>([&](auto d) __attribute__((always_inline)) {
         constexpr int D = decltype(d)::value;
@@ -201,63 +210,76 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(I4Operands op) {
   f32x4_t *part = reinterpret_cast<f32x4_t *>(lds);
   if (lane < kLanes) {
 #pragma unroll
-    for (int t = 0; t < G; ++t)
+    for (int t = 0; t < WT; ++t)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) part[((wave * G + t) * MT + i) * kLanes + lane] = acc[t][i];
+      for (int i = 0; i < MT; ++i) part[((wave * WT + t) * MT + i) * kLanes + lane] = acc[t][i];
   }
   __syncthreads();
-  for (uint32_t x = tid; x < kLanes * MT; x += 64u * NW) {
-    const uint32_t l = x % kLanes, i = x / kLanes;
+  for (uint32_t x = tid; x < kLanes * MT * NT; x += 64u * NW) {
+    const uint32_t l = x % kLanes, i = x / kLanes % MT, t = x / (kLanes * MT);
     f32x4_t c[G];
 #pragma unroll
-    for (int t = 0; t < G; ++t) {
-      c[t] = part[(t * MT + i) * kLanes + l];
+    for (int h = 0; h < G; ++h) {
+      c[h] = part[((t * G + h) * MT + i) * kLanes + l];
 #pragma unroll
-      for (uint32_t w = 1; w < NW; ++w) c[t] += part[((w * G + t) * MT + i) * kLanes + l];
+      for (uint32_t w = 1; w < NW; ++w) c[h] += part[((w * WT + t * G + h) * MT + i) * kLanes + l];
     }
-    const uint32_t col = tile * 16u + (l & 15u);
-    if (col >= op.N) continue;
+    const uint32_t col = (tile + t) * 16u + (l & 15u);
+    if (col >= N) continue;
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j) {
       const uint32_t m = i * 16u + 4u * (l >> 4) + j;
       if (m >= rows) continue;
-      const uint64_t at = (uint64_t)(ROWS == kDense || ROWS == kSum ? first + m : pair_of(m)) * op.ldc + col;
-      if constexpr (GATED) {
-        op.C[at] = (uint16_t)bf16x2_rne(silu_times(c[0][j], c[1][j]), 0.0f);
-      } else if constexpr (ROWS == kLists) {
-        op.Y[(uint64_t)pair_of(m) * op.N + col] = c[0][j];
+      if constexpr (ROWS == kLists && !GATED) {
+        op.Y[(uint64_t)pair_of(m) * N + col] = c[0][j];
       } else {
-        op.C[at] = (uint16_t)bf16x2_rne(c[0][j], 0.0f);
+        const float y = GATED ? silu_times(c[0][j], c[G - 1][j]) : c[0][j];
+        op.C[(uint64_t)(ROWS == kLists ? pair_of(m) : first + m) * op.ldc + col] = (uint16_t)bf16x2_rne(y, 0.0f);
       }
     }
   }
 }
 
-template <int MMAX, bool GATED, int NG, int ROWS, int DEPTH>
-hipError_t launch_zeros(const I4Operands &op, uint32_t grid, hipStream_t stream) {
-  if (op.w.Z)
-    hipLaunchKernelGGL((i4_skinny_kernel<MMAX, GATED, NG, true, ROWS, DEPTH>), dim3(grid), dim3(64 * NW), 0, stream, op);
-  else
-    hipLaunchKernelGGL((i4_skinny_kernel<MMAX, GATED, NG, false, ROWS, DEPTH>), dim3(grid), dim3(64 * NW), 0, stream, op);
+// `count`: chunks, pairs or tokens, which are cut into launches that the grid's second dimension holds.
+template <int MMAX, int NT, bool GATED, int NG, bool ZEROS, int ROWS>
+hipError_t launch_kernel(const I4Operands &op, uint32_t count, hipStream_t stream) {
+  const Rest rest = {op.up.Z, op.C, op.Y, op.ids, op.order, op.offsets, op.weights, op.ldc, op.scale_bf16, op.top_k, op.E};
+  hipLaunchKernelGGL((i4_skinny_kernel<MMAX, NT, GATED, NG, ZEROS, ROWS>), dim3((op.N + 16u * NT - 1u) / (16u * NT), count),
+                     dim3(64 * NW), 0, stream, op.w.W, op.w.S, op.A, op.K, op.N, ROWS == kDense ? op.M : op.T, op.lda, op.w.Z,
+                     op.up.W, op.up.S, rest);
   return hipGetLastError();
 }
 
-template <int MMAX, bool GATED, int ROWS, int DEPTH>
-hipError_t launch_cfg(const I4Operands &op, uint32_t grid, hipStream_t stream) {
-  if (op.group == 128u) return launch_zeros<MMAX, GATED, 1, ROWS, DEPTH>(op, grid, stream);
-  if (op.group == 64u) return launch_zeros<MMAX, GATED, 2, ROWS, DEPTH>(op, grid, stream);
-  return launch_zeros<MMAX, GATED, 4, ROWS, DEPTH>(op, grid, stream);
+template <int MMAX, int NT, bool GATED, int ROWS>
+hipError_t launch_cfg(const I4Operands &op, uint32_t count, hipStream_t stream) {
+  const bool z = op.w.Z != nullptr;
+  if (op.group == 128u)
+    return z ? launch_kernel<MMAX, NT, GATED, 1, true, ROWS>(op, count, stream)
+             : launch_kernel<MMAX, NT, GATED, 1, false, ROWS>(op, count, stream);
+  if (op.group == 64u)
+    return z ? launch_kernel<MMAX, NT, GATED, 2, true, ROWS>(op, count, stream)
+             : launch_kernel<MMAX, NT, GATED, 2, false, ROWS>(op, count, stream);
+  return z ? launch_kernel<MMAX, NT, GATED, 4, true, ROWS>(op, count, stream)
+           : launch_kernel<MMAX, NT, GATED, 4, false, ROWS>(op, count, stream);
 }
 
-template <int MMAX, bool GATED, int DEPTH>
+// Chunks (pairs, tokens) of one launch: the grid's second dimension holds 65535, and all its threads are half of 2^32
+// at most.
+template <int NT>
+uint32_t most_of(const I4Operands &op) {
+  const uint32_t fit = mx_max_grid(64 * NW) / ((op.N + 16u * NT - 1u) / (16u * NT));
+  return fit < 65535u ? fit : 65535u;
+}
+
+template <int MMAX, int NT, bool GATED>
 hipError_t launch_dense(const I4Operands &op, hipStream_t stream) {
-  const uint32_t tiles = (op.N + 15u) / 16u, rows = mx_max_grid(64 * NW) / tiles * MMAX;
+  const uint32_t rows = most_of<NT>(op) * MMAX;
   for (uint32_t m = 0; m < op.M; m += rows) {
     I4Operands part = op;
     part.A = op.A + (uint64_t)m * op.lda;
     part.C = op.C + (uint64_t)m * op.ldc;
     part.M = op.M - m < rows ? op.M - m : rows;
-    const hipError_t e = launch_cfg<MMAX, GATED, kDense, DEPTH>(part, tiles * ((part.M + MMAX - 1u) / MMAX), stream);
+    const hipError_t e = launch_cfg<MMAX, NT, GATED, kDense>(part, (part.M + MMAX - 1u) / MMAX, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -265,9 +287,10 @@ hipError_t launch_dense(const I4Operands &op, hipStream_t stream) {
 
 template <bool GATED>
 hipError_t launch_rows(const I4Operands &op, hipStream_t stream) {
-  if (op.M <= 4u) return launch_dense<4, GATED, 4>(op, stream);
-  if (op.M <= 8u) return launch_dense<8, GATED, 3>(op, stream);
-  return launch_dense<16, GATED, 2>(op, stream);
+  constexpr int kWide = GATED ? 1 : 2;
+  if (op.M <= 4u) return launch_dense<4, 1, GATED>(op, stream);
+  if (op.M <= 8u) return launch_dense<8, kWide, GATED>(op, stream);
+  return launch_dense<16, kWide, GATED>(op, stream);
 }
 
 }  // namespace
@@ -276,18 +299,18 @@ hipError_t launch_i4_skinny(const I4Operands &op, bool gated, hipStream_t stream
   return gated ? launch_rows<true>(op, stream) : launch_rows<false>(op, stream);
 }
 
-uint64_t i4_experts_grid(const I4Operands &op) {
-  const uint64_t pairs = (uint64_t)op.T * op.top_k, tiles = (op.N + 15u) / 16u;
-  if (!op.order) return tiles * (op.gated ? pairs : op.T);
-  return tiles * i4_chunks(pairs, op.E, 16u);
+bool i4_experts_fit(const I4Operands &op) {
+  const uint64_t pairs = (uint64_t)op.T * op.top_k;
+  return (op.order ? i4_chunks(pairs, op.E, 16u) : (op.gated ? pairs : op.T)) <= most_of<1>(op);
 }
 
-uint64_t i4_experts_max_grid() { return mx_max_grid(64 * NW); }
-
 hipError_t launch_i4_experts_skinny(const I4Operands &op, hipStream_t stream) {
-  const uint32_t grid = (uint32_t)i4_experts_grid(op);
-  if (op.order) return op.gated ? launch_cfg<16, true, kLists, 2>(op, grid, stream) : launch_cfg<16, false, kLists, 2>(op, grid, stream);
-  return op.gated ? launch_cfg<4, true, kPairs, 4>(op, grid, stream) : launch_cfg<4, false, kSum, 4>(op, grid, stream);
+  const uint32_t pairs = op.T * op.top_k;
+  if (op.order) {
+    const uint32_t chunks = (uint32_t)i4_chunks(pairs, op.E, 16u);
+    return op.gated ? launch_cfg<16, 1, true, kLists>(op, chunks, stream) : launch_cfg<16, 1, false, kLists>(op, chunks, stream);
+  }
+  return op.gated ? launch_cfg<4, 1, true, kPairs>(op, pairs, stream) : launch_cfg<4, 1, false, kSum>(op, op.T, stream);
 }
 
 }  // namespace wqd

@@ -99,8 +99,8 @@ hipError_t launch_mx_dequantize(const void *Q, const void *S, bool fp4, void *Y,
 hipError_t launch_add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *Y, void *Q, void *S,
                                   uint32_t M, uint32_t K, uint32_t ldx, uint32_t ldr, float eps, hipStream_t stream);
 
-// A matrix of 4-bit integer weights (or several, one after another): codes laid
-// out in tiles, scales [N][K/group] in FP16 or BF16, zero points likewise or null.
+// A matrix of 4-bit integer weights (or several, one after another), laid out in
+// tiles: codes, scales in FP16 or BF16, zero points or null.
 struct I4Matrix {
   const uint8_t *W;
   const uint16_t *S;
@@ -125,16 +125,19 @@ struct I4Operands {
 
 // Enqueue a dense product (i4_tile.hip chooses the kernel; launch_i4_skinny is
 // the one for few rows, which takes any size).
+hipError_t launch_i4_product(const I4Operands &op, hipStream_t stream);
 hipError_t launch_i4_skinny(const I4Operands &op, bool gated, hipStream_t stream);
 
 // Enqueue the experts' products: gated (C gets a row per pair), or the last ones
 // (with lists: Y gets a row per pair; without: C gets each token's weighted sum).
-uint64_t i4_experts_grid(const I4Operands &op);  // workgroups of that launch, and the most that one may have
-uint64_t i4_experts_max_grid();
+bool i4_experts_fit(const I4Operands &op);  // whether one launch holds them
+hipError_t launch_i4_experts(const I4Operands &op, hipStream_t stream);
 hipError_t launch_i4_experts_skinny(const I4Operands &op, hipStream_t stream);
 
-// Enqueue the layout of `count` matrices' codes.
-hipError_t launch_i4_pack(const void *Q, void *W, uint32_t N, uint32_t K, uint32_t count, hipStream_t stream);
+// Enqueue the layout of `count` matrices: rows of codes, scales and zero points
+// (or null) to `to`, which is written.
+hipError_t launch_i4_pack(const void *Q, const I4Matrix &to, const void *S, const void *Z, uint32_t N, uint32_t K,
+                          uint32_t group, uint32_t count, hipStream_t stream);
 
 // A router's operands; shapes validated by the caller.
 struct MoeRoute {

@@ -71,7 +71,7 @@ def lib() -> ctypes.CDLL:
               L.w4a16_gated, L.w4a8_gated, L.w4a4_gated):
         f.restype = ctypes.c_int
     i32, f32 = ctypes.c_int, ctypes.c_float
-    L.i4_pack.argtypes = [vp, vp, u32, u32, u32, vp]
+    L.i4_pack.argtypes = [vp] * 6 + [u32] * 4 + [vp]
     L.i4a16_gemm.argtypes = [vp] * 5 + [u32] * 7 + [vp]
     L.i4a16_gated.argtypes = [vp] * 8 + [u32] * 7 + [vp]
     L.moe_route.argtypes = [vp, u32, vp, vp, vp] + [u32] * 8 + [i32, f32, vp]
@@ -80,8 +80,8 @@ def lib() -> ctypes.CDLL:
     L.i4a16_experts_down.argtypes = [vp] * 10 + [u32] * 8 + [vp]
     for f in (L.i4_pack, L.i4a16_gemm, L.i4a16_gated, L.moe_route, L.moe_lists, L.i4a16_experts_gated, L.i4a16_experts_down):
         f.restype = ctypes.c_int
-    L.i4_packed_bytes.argtypes = [u32, u32]
-    L.i4_packed_bytes.restype = sz
+    L.i4_packed_rows.argtypes = [u32]
+    L.i4_packed_rows.restype = u32
     L.q2_0_packed_bytes.argtypes = [u32, u32]
     L.q2_0_packed_bytes.restype = sz
     L.q2_0_pack.argtypes = [vp, vp, u32, u32, vp]
@@ -446,26 +446,29 @@ def _i4_scale_type(fn: str, given: int | None, *scales) -> int:
 
 
 def _i4_matrix(fn: str, name: str, W, S, Z, E: int, N: int, K: int, group: int, d: int) -> tuple:
-    """Addresses of E matrices' codes, scales and zero points."""
-    rows = -(-N // 16) * 16
-    g = K // group
-    return (_arg(fn, name, W, E * rows * K // 2, d, _BYTES), _arg(fn, name + "S", S, 2 * E * N * g, d, _I4_SCALES, g),
-            _arg(fn, name + "Z", Z, E * N * g, d, _BYTES, g))
+    """Addresses of E laid-out matrices' codes, scales and zero points."""
+    n = E * (N + 15 & -16) * K
+    return (_arg(fn, name, W, n // 2, d, _BYTES), _arg(fn, name + "S", S, n // group * 2, d, _I4_SCALES),
+            _arg(fn, name + "Z", Z, n // group, d, _BYTES))
 
 
-def i4_packed_bytes(N: int, K: int) -> int:
-    """Bytes of a matrix's laid-out codes."""
-    return int(lib().i4_packed_bytes(N, K))
+def i4_packed_rows(N: int) -> int:
+    """Rows of a laid-out matrix: N rounded up to a multiple of 16."""
+    return int(lib().i4_packed_rows(N))
 
 
-def i4_pack(Q, W, N: int, K: int, count: int = 1, stream=None) -> None:
-    """Codes of `count` matrices, two a byte with the even k in the low nibble, to
-    the layout that the products read."""
+def i4_pack(Q, S, Z, W, WS, WZ, N: int, K: int, group: int, count: int = 1, stream=None) -> None:
+    """`count` matrices to the layout that the products read: codes Q, two a byte with
+    the even k in the low nibble, scales S and zero points Z (or None, and WZ too)."""
     fn = "i4_pack"
-    _i4_sizes(fn, N | K | count, K, 128)
+    _i4_sizes(fn, N | K | count, K, group)
     d, st = _here(fn, stream)
-    _check(fn, (_lib or lib()).i4_pack(_arg(fn, "Q", Q, count * N * K // 2, d, _BYTES, K // 2),
-                                       _arg(fn, "W", W, count * (-(-N // 16) * 16) * K // 2, d, _BYTES), N, K, count, st))
+    n, g = count * N * K, K // group
+    if not isinstance(S, int) and not isinstance(WS, int) and S is not None and WS is not None and S.dtype != WS.dtype:
+        raise ValueError(f"{fn}: S and WS must have the same type")
+    _check(fn, (_lib or lib()).i4_pack(_arg(fn, "Q", Q, n // 2, d, _BYTES, K // 2), _arg(fn, "S", S, n // group * 2, d, _I4_SCALES, g),
+                                       _arg(fn, "Z", Z, n // group, d, _BYTES, g),
+                                       *_i4_matrix(fn, "W", W, WS, WZ, count, N, K, group, d), N, K, group, count, st))
 
 
 def i4a16_gemm(A, W, WS, WZ, C, M: int, N: int, K: int, group: int, a_row_stride: int | None = None,
