@@ -67,16 +67,22 @@ constexpr uint32_t kStage = BM * 256 + kWaves * NT * (kI4Tile + 32 * NG + (ZEROS
 template <int BM, int NT, int NG, bool ZEROS, int PRE>
 constexpr uint32_t kLdsBytes = (PRE + 1) * kStage<BM, NT, NG, ZEROS>;
 
+// What the conversion keeps in registers: a mask and 1024 twice as FP16, for one
+// instruction that masks and sets, and a one that the compiler does not see, so
+// that a mixed multiply-add widens and subtracts at once.
+struct Constants {
+  uint32_t mask, base;
+  float one;
+};
+
 // 8 codes as the BF16 values of q - z; minus: -(1024 + z)
-__device__ __forceinline__ bf16x8_t i4_values(uint32_t w, float minus, uint32_t mask, uint32_t base) {
+__device__ __forceinline__ bf16x8_t i4_values(uint32_t w, float minus, const Constants &k) {
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
   u32x4_t v;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t x = (w >> (4 * i) & mask) | base;
-    float lo, hi;
-    asm("v_fma_mix_f32 %0, %1, 1.0, %2 op_sel_hi:[1,0,0]" : "=v"(lo) : "v"(x), "v"(minus));
-    asm("v_fma_mix_f32 %0, %1, 1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(hi) : "v"(x), "v"(minus));
-    v[i] = bf16x2_rne(lo, hi);
+    const f16x2_t x = __builtin_bit_cast(f16x2_t, (w >> (4 * i) & k.mask) | k.base);
+    v[i] = bf16x2_rne(__builtin_fmaf((float)x.x, k.one, minus), __builtin_fmaf((float)x.y, k.one, minus));
   }
   return __builtin_bit_cast(bf16x8_t, v);
 }
@@ -176,9 +182,8 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
     u32x4_t w[NT];
     I4Groups<NG> s[NT];
   };
-  uint32_t mask, base16;  // in registers, for one instruction that masks and sets
-  asm volatile("s_mov_b32 %0, 0x000f000f" : "=s"(mask));
-  asm volatile("v_mov_b32 %0, 0x64006400" : "=v"(base16));
+  Constants k = {0x000f000fu, 0x64006400u, 1.0f};
+  asm volatile("" : "+s"(k.mask), "+v"(k.base), "+v"(k.one));
   auto read_codes = [&](uint32_t s) __attribute__((always_inline)) {
     const uint8_t *p = lds + s % NBUF * kBuf;
     Codes c;
@@ -191,9 +196,29 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
   };
   // dword d (0 .. 3) of tile i
   auto convert = [&](const Codes &c, int i, int d, Weights &w) __attribute__((always_inline)) {
-    w.v[i][d] = i4_values(c.w[i][d], -1024.0f - i4_zero_of(c.s[i], d * NG / 4), mask, base16);
+    w.v[i][d] = i4_values(c.w[i][d], -1024.0f - i4_zero_of(c.s[i], d * NG / 4), k);
     asm volatile("" : "+v"(w.v[i][d]));  // here, not where it is used
     if (d * NG % 4 == 0) w.s[i][d * NG / 4] = i4_scale_of(c.s[i], d * NG / 4, op.scale_bf16);
+  };
+  // The sums of the last group that was multiplied, and their scales: they join the
+  // output's while the matrix instructions of the next one run.
+  f32x4_t last[NT];
+  float last_s[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    last[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    last_s[i] = 0.0f;
+  }
+  struct Rows {
+    bf16x8_t v[4];
+  };
+  auto fold = [&](int j) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(last_s[i], last[i][e], acc[i][j][e]);
+      asm volatile("" : "+v"(acc[i][j]));  // here, not where it is used
+    }
   };
   auto step = [&](uint32_t s, const Weights &w, Weights &next) __attribute__((always_inline)) {
     step_barrier<(PRE - 1) * ND>();
@@ -201,9 +226,6 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
     issue_w(s + PRE + 1);
     const Codes c = read_codes(s + 1);
     const uint8_t *p = lds + s % NBUF * kBuf;
-    struct Rows {
-      bf16x8_t v[4];
-    };
     auto read_a = [&](int j) __attribute__((always_inline)) {
       Rows a;
 #pragma unroll
@@ -216,8 +238,8 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
     mx_unroll<0, MT>([&](auto J) __attribute__((always_inline)) {
       constexpr int j = decltype(J)::value;
       if constexpr (j + 1 < MT) a[(j + 1) & 1] = read_a(j + 1);
-#pragma unroll
-      for (int q = 0; q < NG; ++q) {
+      mx_unroll<0, NG>([&](auto Q) __attribute__((always_inline)) {
+        constexpr int q = decltype(Q)::value;
         f32x4_t t[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) t[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -225,15 +247,22 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
         for (int x = q * 4 / NG; x < (q + 1) * 4 / NG; ++x)
 #pragma unroll
           for (int i = 0; i < NT; ++i) t[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j & 1].v[x], w.v[i][x], t[i], 0, 0, 0);
+        fold(q > 0 ? j : (j + MT - 1) % MT);
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(w.s[i][q], t[i][e], acc[i][j][e]);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(acc[i][j]));
-      }
+        for (int i = 0; i < NT; ++i) {
+          last[i] = t[i];
+          last_s[i] = w.s[i][q];
+        }
+      });
 #pragma unroll
       for (int x = j * NT * 4 / MT; x < (j + 1) * NT * 4 / MT; ++x) convert(c, x / 4, x % 4, next);
+      // matrix instructions and the others in turn
+      constexpr int kOther = (8 * NG * NT / 2 + 20 * NT * 4 / MT) / (4 * NT) + 1;
+      __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+      mx_unroll<0, 4 * NT>([&](auto) __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, kOther, 0);
+      });
       __builtin_amdgcn_sched_barrier(0);  // without it the registers of several rounds do not fit
     });
   };
@@ -256,6 +285,7 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
     step(s + 1u, odd, even);
   }
   if (s < kt) step(s, even, odd);
+  fold(MT - 1);
   step_barrier<0>();  // nothing is in flight, and everybody has read the last stage
 
   const uint32_t n = r;
