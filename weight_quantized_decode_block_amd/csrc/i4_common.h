@@ -19,12 +19,12 @@ namespace wqd {
 constexpr uint32_t kI4Tile = 1024;  // bytes of 16 rows x 128 k
 
 // 8 codes as BF16 values 16 + q (exact: q are the upper four fraction bits of
-// [16, 32)): seven integer instructions and no conversion.  The constant is
-// taken back with the sum of the activations.
-__device__ __forceinline__ bf16x8_t i4_biased(uint32_t w) {
-  constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u;
-  const u32x4_t x = {(w << 3 & kMask) | kBase, (w >> 1 & kMask) | kBase, (w >> 5 & kMask) | kBase,
-                     (w >> 9 & kMask) | kBase};
+// [16, 32)): eight integer instructions and no conversion, where the compiler does not
+// know the constants and keeps them in registers.  16 is taken back with the sum of
+// the activations.
+constexpr uint32_t kI4BiasMask = 0x00780078u, kI4BiasBase = 0x41804180u;
+__device__ __forceinline__ bf16x8_t i4_biased(uint32_t w, uint32_t mask, uint32_t base) {
+  const u32x4_t x = {(w << 3 & mask) | base, (w >> 1 & mask) | base, (w >> 5 & mask) | base, (w >> 9 & mask) | base};
   return __builtin_bit_cast(bf16x8_t, x);
 }
 constexpr float kI4Bias = 16.0f;
@@ -112,6 +112,21 @@ __device__ __forceinline__ bool i4_find_chunk(const int32_t *offsets, uint32_t E
     before += total;
   }
   return false;
+}
+
+// How many chunks there are.
+template <uint32_t CHUNK>
+__device__ __forceinline__ uint32_t i4_count_chunks(const int32_t *offsets, uint32_t E, uint32_t pairs, uint32_t lane) {
+  uint32_t sum = 0;
+  for (uint32_t e = lane; e < E; e += 64u) {
+    uint32_t lo = (uint32_t)offsets[e], hi = (uint32_t)offsets[e + 1u];
+    lo = lo < pairs ? lo : pairs;
+    hi = hi < pairs ? hi : pairs;
+    sum += ((hi > lo ? hi - lo : 0u) + CHUNK - 1u) / CHUNK;
+  }
+#pragma unroll
+  for (uint32_t d = 1; d < 64; d *= 2) sum += (uint32_t)__shfl_xor((int)sum, d);
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)sum);
 }
 
 // Chunks that lists of `pairs` pairs over E experts are cut into, at most.

@@ -140,6 +140,8 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__res
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[t][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   uint8_t *mine = lds + wave * kARegion;
+  uint32_t mask = kI4BiasMask, base = kI4BiasBase;
+  asm volatile("" : "+s"(mask), "+v"(base));
   const u32x4_t one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
   const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, one);
   auto compute = [&](Step x) __attribute__((always_inline)) {
@@ -176,7 +178,7 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__res
           f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int j = q * 4 / NG; j < (q + 1) * 4 / NG; ++j)
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], i4_biased(x.w[t][j]), p, 0, 0, 0);
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], i4_biased(x.w[t][j], mask, base), p, 0, 0, 0);
           const float s = i4_scale_of(x.s[t], q, op.scale_bf16) * (ROWS == kSum ? x.weight : 1.0f);
           const float z = -kI4Bias - i4_zero_of(x.s[t], q);
 #pragma unroll

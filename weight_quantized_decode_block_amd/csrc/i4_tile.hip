@@ -2,8 +2,8 @@
 // operations of i4_skinny.hip, bound by the matrix instructions and by what feeds
 // them.
 //
-// A workgroup of 8 waves owns BM rows and 128 NT weight rows (in the gated form
-// 64 NT of both matrices) and walks K in steps of 128.  The waves stand side by side
+// A workgroup of 8 waves owns BM rows and 256 weight rows (in the gated form
+// 128 of both matrices) and walks K in steps of 128.  The waves stand side by side
 // in n, so each converts its own weights only, once; all of them read all activations.
 //
 //   * Staging.  Activations, codes, scales and zero points go straight from memory to
@@ -11,10 +11,16 @@
 //     own transfers by count.  Codes lie in the matrix operand's order, so a lane
 //     reads back what its neighbours brought in whole KB.  Rows past the last one
 //     repeat it; their outputs are not stored.
-//   * Codes become the BF16 values of q - z (exact: integers of at most 8 bits):
-//     1024 + q as FP16 by two integer instructions a pair, minus 1024 + z by
-//     a mixed multiply-add each, and a conversion for two.  A step's codes are converted
-//     between the matrix instructions of the step before.
+//   * Codes become BF16 between the matrix instructions of the step before.  With zero
+//     points, the values of q - z (exact: integers of at most 8 bits): 1024 + q as FP16
+//     by two integer instructions a pair, minus 1024 + z by a mixed multiply-add
+//     each, and a conversion for two.  Without, 16 + q by the two integer instructions
+//     alone (i4_biased), and a group's sums start at -24 times its activations' sum: each
+//     wave forms those of 16 rows for all, a step ahead.
+//   * That is because all instructions of both waves of a SIMD share its issue: beside
+//     a 32 x 32 x 16 matrix instruction (32 cycles) there is room for six others of its
+//     wave, beside a 16 x 16 x 32 one for two.  32 rows are 8 matrix instructions, 16
+//     multiply-adds of scales and 38 conversions, or 16.
 //   * The sums of a group are a matrix accumulator of their own, which the scale
 //     adds to the output's in fp32: nothing but the output is rounded.
 #include <hip/hip_runtime.h>
@@ -42,13 +48,18 @@ __device__ __forceinline__ rsrc_t bytes_rsrc(const void *p, uint64_t offset, uin
   return r;
 }
 
-// 16 (or 4) bytes per lane from voff of the buffer to LDS byte `lds` + 16 (4) *
-// lane.  The transfer has no destination registers; it is waited for by count.
+// 16 bytes per lane from voff of the buffer to LDS byte `lds` + 16 * lane.  The
+// transfer has no destination registers; it is waited for by count.
 __device__ __forceinline__ void copy16_to_lds(uint32_t lds, rsrc_t r, uint32_t voff) {
   asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "{m0}"(lds), "v"(voff), "s"(r) : "memory");
 }
+// The same of 4 bytes for each of the first LANES lanes, where all 64 are active.
+template <int LANES>
 __device__ __forceinline__ void copy4_to_lds(uint32_t lds, rsrc_t r, uint32_t voff) {
-  asm volatile("s_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "{m0}"(lds), "v"(voff), "s"(r) : "memory");
+  asm volatile("s_mov_b64 exec, %3\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds\n\ts_mov_b64 exec, -1"
+               :
+               : "{m0}"(lds), "v"(voff), "s"(r), "s"((1ull << LANES) - 1ull)
+               : "memory");
 }
 
 // Wait until at most N of this wave's transfers are in flight and its LDS
@@ -61,49 +72,43 @@ __device__ __forceinline__ void step_barrier() {
 constexpr int kDense = 0;  // rows m0 ..
 constexpr int kLists = 1;  // rows of one expert's list
 
-// LDS of a stage: activations, codes, scales, zero points (of each wave: NT tiles')
-template <int BM, int NT, int NG, bool ZEROS>
-constexpr uint32_t kStage = BM * 256 + kWaves * NT * (kI4Tile + 32 * NG + (ZEROS ? 16 * NG : 0));
-template <int BM, int NT, int NG, bool ZEROS, int PRE>
-constexpr uint32_t kLdsBytes = (PRE + 1) * kStage<BM, NT, NG, ZEROS>;
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
-// What the conversion keeps in registers: a mask and 1024 twice as FP16, for one
-// instruction that masks and sets, and a one that the compiler does not see, so
-// that a mixed multiply-add widens and subtracts at once.
-struct Constants {
-  uint32_t mask, base;
-  float one;
-};
+// LDS of a stage: activations, and of 16 weight tiles the codes, 128 bytes of
+// scales and 64 of zero points (this step's and what follows them)
+// and the sums of the activations of each group; and three stages
+constexpr uint32_t NBUF = 3;
+template <int BM, int NG, bool ZEROS>
+constexpr uint32_t kStage = BM * 256 + 16 * (kI4Tile + 128 + (ZEROS ? 64 : 0)) + NG * BM * 4;
+// and which pairs the rows are
+template <int BM, int NG, bool ZEROS>
+constexpr uint32_t kLdsBytes = NBUF * kStage<BM, NG, ZEROS> + BM * 4;
 
-// 8 codes as the BF16 values of q - z; minus: -(1024 + z)
-__device__ __forceinline__ bf16x8_t i4_values(uint32_t w, float minus, const Constants &k) {
-  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-  u32x4_t v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const f16x2_t x = __builtin_bit_cast(f16x2_t, (w >> (4 * i) & k.mask) | k.base);
-    v[i] = bf16x2_rne(__builtin_fmaf((float)x.x, k.one, minus), __builtin_fmaf((float)x.y, k.one, minus));
-  }
-  return __builtin_bit_cast(bf16x8_t, v);
-}
-
-template <int BM, int NT, bool GATED, int NG, bool ZEROS, int ROWS, int PRE>
+// WM: waves side by side in m; 8 / WM in n.
+template <int BM, int WM, bool GATED, int NG, bool ZEROS, int ROWS>
 __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uint32_t tm) {
-  static_assert(!GATED || NT == 2, "a wave has a tile of either matrix");
-  constexpr int MT = BM / 16, AU = BM / 32, NBUF = PRE + 1;
-  constexpr int ND = AU + NT * (ZEROS ? 3 : 2);  // transfers of a wave and step
-  constexpr uint32_t BNT = kWaves * NT / (GATED ? 2 : 1);  // 16-column tiles of the output
-  constexpr uint32_t kW = BM * 256, kS = kW + kWaves * NT * kI4Tile, kZ = kS + kWaves * NT * 32 * NG;
-  constexpr uint32_t kBuf = kStage<BM, NT, NG, ZEROS>;
+  static_assert(BM <= 128, "a wave forms the sums of 16 rows");
+  constexpr int MT = BM / WM / 32, NS = WM, AU = BM / 32;  // 32 x 32 tiles of a wave; its transfers of activations
+  constexpr int ND = AU + (ZEROS ? 6 : 4);                  // transfers of a wave and step
+  constexpr uint32_t BNT = GATED ? 8 : 16;                  // 16-column tiles of the output
+  constexpr uint32_t kW = BM * 256, kS = kW + 16 * kI4Tile, kZ = kS + 16 * 128, kSum = kZ + (ZEROS ? 16 * 64 : 0);
+  constexpr uint32_t kBuf = kStage<BM, NG, ZEROS>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
 
-  const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, g = lane >> 4;
+  const uint32_t lane = threadIdx.x & 63u, n5 = lane & 31u, kk = lane >> 5, r = lane & 15u, g = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t wm = wave / (kWaves / WM), wn = wave % (kWaves / WM);
   const uint32_t tiles = (op.N + 15u) >> 4, kt = op.K >> 7, tn = (tiles + BNT - 1u) / BNT;
 
   // Tile of this workgroup: the 8 XCDs, which take workgroups in turn, get
-  // contiguous runs, and tiles run down four rows before the next column.
+  // contiguous runs, and tiles run down four rows before the next column.  Of lists
+  // the grid has more than there are, which would all be the last XCDs'.
+  if constexpr (ROWS == kLists) {
+    const uint32_t chunks = i4_count_chunks<BM>(op.offsets, op.E, op.T * op.top_k, lane);
+    tm = chunks < tm ? chunks : tm;
+    if (blockIdx.x >= tm * tn) return;
+  }
   const uint32_t total = tm * tn, xcd = blockIdx.x & 7u, q8 = total >> 3, rem = total & 7u;
   const uint32_t id = xcd * q8 + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
   const uint32_t band = id / (4u * tn), in_band = id - band * 4u * tn;
@@ -116,10 +121,14 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
   } else {
     if (!i4_find_chunk<BM>(op.offsets, op.E, op.T * op.top_k, chunk, lane, expert, first, rows)) return;
   }
-  auto pair_of = [&](uint32_t m) __attribute__((always_inline)) {
-    const uint32_t p = (uint32_t)op.order[first + (m < rows ? m : rows - 1u)];
-    return p < op.T * op.top_k ? p : 0u;
-  };
+  uint32_t *const pair_of = reinterpret_cast<uint32_t *>(lds + NBUF * kBuf);
+  if constexpr (ROWS == kLists) {
+    if (threadIdx.x < (uint32_t)BM) {
+      const uint32_t p = (uint32_t)op.order[first + (threadIdx.x < rows ? threadIdx.x : rows - 1u)];
+      pair_of[threadIdx.x] = p < op.T * op.top_k ? p : 0u;
+    }
+    __syncthreads();
+  }
 
   // Activations: units of 4 rows x 256 bytes; slot x of row m has piece x ^ (m % 16), so
   // that the sixteen lanes that an LDS read serves together meet all 64 banks.
@@ -130,182 +139,258 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
 #pragma unroll
   for (int i = 0; i < AU; ++i) {
     const uint32_t m = (wave + i * kWaves) * 4u + g;
-    const uint32_t row = ROWS == kDense ? (m < rows ? m : rows - 1u) : (GATED ? pair_of(m) / op.top_k : pair_of(m));
+    const uint32_t row = ROWS == kDense ? (m < rows ? m : rows - 1u) : (GATED ? pair_of[m] / op.top_k : pair_of[m]);
     aoff[i] = row * pitch + (r ^ (m & 15u)) * 16u;
   }
-  // this wave's weight tiles (gated: one of either matrix)
-  const uint32_t t0 = col * BNT + (GATED ? wave : wave * NT);
-  rsrc_t wr[NT], sr[NT], zr[NT];
+  // the two weight tiles that this wave brings (gated: one of either matrix)
+  rsrc_t wr[2], sr[2], zr[2];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const I4Matrix &m = GATED && i ? op.up : op.w;
-    const uint32_t t = t0 + (GATED ? 0u : i);
+    const uint32_t t = col * BNT + (GATED ? wave : wave * 2u + i);
     const uint64_t at = ((uint64_t)expert * tiles + (t < tiles ? t : tiles - 1u)) * kt;
     wr[i] = bytes_rsrc(m.W, at * kI4Tile, kt * kI4Tile);
     sr[i] = bytes_rsrc(m.S, at * (32u * NG), kt * (32u * NG));
     if constexpr (ZEROS) zr[i] = bytes_rsrc(m.Z, at * (16u * NG), kt * (16u * NG));
   }
-  const uint32_t put_w = kW + wave * NT * kI4Tile, put_s = kS + wave * NT * (32 * NG), put_z = kZ + wave * NT * (16 * NG);
-  auto issue_a = [&](uint32_t s) __attribute__((always_inline)) {
-    const uint32_t base = lds0 + s % NBUF * kBuf, k = (s < kt ? s : kt - 1u) * 256u;
-#pragma unroll
-    for (int i = 0; i < AU; ++i) copy16_to_lds(base + (wave + i * kWaves) * 1024u, ar, aoff[i] + k);
-  };
-  auto issue_w = [&](uint32_t s) __attribute__((always_inline)) {
-    const uint32_t base = lds0 + s % NBUF * kBuf, t = s < kt ? s : kt - 1u;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) copy16_to_lds(base + put_w + i * kI4Tile, wr[i], t * kI4Tile + lane * 16u);
-    if (lane < 8u * NG) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i) copy4_to_lds(base + put_s + i * 32 * NG, sr[i], t * (32u * NG) + lane * 4u);
-    }
-    if constexpr (ZEROS) {
-      if (lane < 4u * NG) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) copy4_to_lds(base + put_z + i * 16 * NG, zr[i], t * (16u * NG) + lane * 4u);
-      }
-    }
+  // Transfer i of step s to its stage.  Past the last step it comes once more.
+  // Scales and zero points beyond a tile's row of them are read as zeros and not used.
+  auto issue = [&](int i, uint32_t s, uint32_t stage) __attribute__((always_inline)) {
+    const uint32_t t = s < kt ? s : kt - 1u, h = (i - AU) & 1, to = lds0 + stage;
+    if (i < AU)
+      copy16_to_lds(to + (wave + i * kWaves) * 1024u, ar, aoff[i] + t * 256u);
+    else if (i < AU + 2)
+      copy16_to_lds(to + kW + (wave * 2u + h) * kI4Tile, wr[h], t * kI4Tile + lane * 16u);
+    else if (i < AU + 4)
+      copy4_to_lds<32>(to + kS + (wave * 2u + h) * 128u, sr[h], t * (32u * NG) + lane * 4u);
+    else
+      copy4_to_lds<16>(to + kZ + (wave * 2u + h) * 64u, zr[h], t * (16u * NG) + lane * 4u);
   };
 
-  f32x4_t acc[NT][MT];
+  f32x16_t acc[MT][NS];
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int j = 0; j < MT; ++j)
 #pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[j][i][e] = 0.0f;
 
-  // A step's weights: values and scales
-  struct Weights {
-    bf16x8_t v[NT][4];
-    float s[NT][NG];
-  };
+  // A step's weights of this lane's columns (n5 of each 32): the 16 bytes of chunks
+  // (k = 16 c + 8 kk ..) of even and odd c, scales, zero points
   struct Codes {
-    u32x4_t w[NT];
-    I4Groups<NG> s[NT];
+    u32x4_t w[NS][2];
+    I4Groups<NG> s[NS];
   };
-  Constants k = {0x000f000fu, 0x64006400u, 1.0f};
-  asm volatile("" : "+s"(k.mask), "+v"(k.base), "+v"(k.one));
-  auto read_codes = [&](uint32_t s) __attribute__((always_inline)) {
-    const uint8_t *p = lds + s % NBUF * kBuf;
-    Codes c;
+  uint32_t mask = kI4BiasMask, base = kI4BiasBase;
+  asm volatile("" : "+s"(mask), "+v"(base));
+  auto read_codes = [&](uint32_t stage) __attribute__((always_inline)) {
+    Codes x;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      c.w[i] = *reinterpret_cast<const u32x4_t *>(p + put_w + i * kI4Tile + lane * 16u);
-      c.s[i] = i4_load_groups<NG, ZEROS>(reinterpret_cast<const uint16_t *>(p + put_s + i * 32 * NG), p + put_z + i * 16 * NG, r);
+    for (int i = 0; i < NS; ++i) {
+      const uint32_t t = (wn * NS + i) * 2u + (n5 >> 4);
+      const uint8_t *p = lds + stage;
+#pragma unroll
+      for (uint32_t h = 0; h < 2; ++h)
+        x.w[i][h] = *reinterpret_cast<const u32x4_t *>(p + kW + t * kI4Tile + (2u * h + kk) * 256u + r * 16u);
+      x.s[i] = i4_load_groups<NG, ZEROS>(reinterpret_cast<const uint16_t *>(p + kS + t * 128u), p + kZ + t * 64u, r);
     }
-    return c;
+    return x;
   };
-  // dword d (0 .. 3) of tile i
-  auto convert = [&](const Codes &c, int i, int d, Weights &w) __attribute__((always_inline)) {
-    w.v[i][d] = i4_values(c.w[i][d], -1024.0f - i4_zero_of(c.s[i], d * NG / 4), k);
-    asm volatile("" : "+v"(w.v[i][d]));  // here, not where it is used
-    if (d * NG % 4 == 0) w.s[i][d * NG / 4] = i4_scale_of(c.s[i], d * NG / 4, op.scale_bf16);
-  };
-  // The sums of the last group that was multiplied, and their scales: they join the
-  // output's while the matrix instructions of the next one run.
-  f32x4_t last[NT];
-  float last_s[NT];
+  bf16x8_t a[2][MT], b[2][NS];  // of chunk c in place c % 2
+  auto read_a = [&](uint32_t stage, int c) __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    last[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    last_s[i] = 0.0f;
+    for (int j = 0; j < MT; ++j)
+      a[c & 1][j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t *>(
+          lds + stage + (wm * (MT * 32u) + j * 32u + n5) * 256u + ((2u * c + kk) ^ r) * 16u));
+  };
+  auto convert = [&](const Codes &x, int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      b[c & 1][i] = i4_biased(x.w[i][c & 1][c >> 1], mask, base);
+      asm volatile("" : "+v"(b[c & 1][i]));  // here, not where it is used
+    }
+  };
+  // The sums of the activations of a step's groups (without zero points times -24), of
+  // 16 rows by this wave (of fewer rows two waves write the same): read, multiply, write
+  const uint32_t sum_rows = wave % (BM / 16);
+  u32x4_t sum_a[4];
+  f32x4_t sum_t[NG];
+  auto sums_read = [&](uint32_t stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (uint32_t x = 0; x < 4; ++x)
+      sum_a[x] = *reinterpret_cast<const u32x4_t *>(lds + stage + (sum_rows * 16u + r) * 256u + ((4u * x + g) ^ r) * 16u);
+  };
+  auto sums_form = [&]() __attribute__((always_inline)) {
+    const u32x4_t one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+      sum_t[q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int x = q * 4 / NG; x < (q + 1) * 4 / NG; ++x)
+        sum_t[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, sum_a[x]), __builtin_bit_cast(bf16x8_t, one),
+                                                           sum_t[q], 0, 0, 0);
+    }
+  };
+  auto sums_write = [&](uint32_t stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < NG; ++q)  // the sixteen lanes of a row group hold and write the same
+      *reinterpret_cast<f32x4_t *>(lds + stage + kSum + (q * BM + sum_rows * 16u + g * 4u) * 4u) =
+          ZEROS ? sum_t[q] : sum_t[q] * (-kI4Bias - 8.0f);
+  };
+  // rows 8 (e / 4) + 4 kk + e % 4 of tile j, as a lane's outputs have them
+  auto sums_of = [&](uint32_t stage, int q, int j) __attribute__((always_inline)) {
+    f32x16_t t;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4_t x = *reinterpret_cast<const f32x4_t *>(lds + stage + kSum + (q * BM + wm * (MT * 32u) + j * 32u + i * 8u + kk * 4u) * 4u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[4 * i + e] = x[e];
+    }
+    return t;
+  };
+
+  // The group that is being multiplied, and the scales and zero points of its columns: it
+  // joins the outputs when the next one begins.
+  f32x16_t t[MT][NS];
+  float scale[NS], zero[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    scale[i] = zero[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) t[j][i][e] = 0.0f;
   }
-  struct Rows {
-    bf16x8_t v[4];
+  auto fold = [&](int j, int i, const f32x16_t &z) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      acc[j][i][e] = __builtin_fmaf(scale[i], ZEROS ? __builtin_fmaf(zero[i], z[e], t[j][i][e]) : t[j][i][e], acc[j][i][e]);
+    asm volatile("" : "+v"(acc[j][i]));
   };
-  auto fold = [&](int j) __attribute__((always_inline)) {
+  Codes x;
+  auto step = [&](uint32_t s, uint32_t prev, uint32_t cur, uint32_t nxt) __attribute__((always_inline)) {
+    step_barrier<0>();
+    Codes y;
+    mx_unroll<0, 8>([&](auto C) __attribute__((always_inline)) {
+      constexpr int c = decltype(C)::value, q = c * NG / 8;
+      constexpr bool kFirst = c * NG % 8 == 0;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+      for (int j = 0; j < MT; ++j) {
+        f32x16_t from = {}, z = {};
+        if constexpr (kFirst && ZEROS) z = sums_of(c == 0 ? prev : cur, (q + NG - 1) % NG, j);
+        if constexpr (kFirst && !ZEROS) from = sums_of(cur, q, j);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(last_s[i], last[i][e], acc[i][j][e]);
-      asm volatile("" : "+v"(acc[i][j]));  // here, not where it is used
-    }
-  };
-  auto step = [&](uint32_t s, const Weights &w, Weights &next) __attribute__((always_inline)) {
-    step_barrier<(PRE - 1) * ND>();
-    issue_a(s + PRE);
-    issue_w(s + PRE + 1);
-    const Codes c = read_codes(s + 1);
-    const uint8_t *p = lds + s % NBUF * kBuf;
-    auto read_a = [&](int j) __attribute__((always_inline)) {
-      Rows a;
+        for (int i = 0; i < NS; ++i) {
+          if constexpr (kFirst) fold(j, i, z);
+          if constexpr (kFirst && ZEROS) {
 #pragma unroll
-      for (uint32_t x = 0; x < 4; ++x)
-        a.v[x] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t *>(p + (j * 16u + r) * 256u + ((4u * x + g) ^ r) * 16u));
-      return a;
-    };
-    Rows a[2];
-    a[0] = read_a(0);
-    mx_unroll<0, MT>([&](auto J) __attribute__((always_inline)) {
-      constexpr int j = decltype(J)::value;
-      if constexpr (j + 1 < MT) a[(j + 1) & 1] = read_a(j + 1);
-      mx_unroll<0, NG>([&](auto Q) __attribute__((always_inline)) {
-        constexpr int q = decltype(Q)::value;
-        f32x4_t t[NT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) t[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int x = q * 4 / NG; x < (q + 1) * 4 / NG; ++x)
-#pragma unroll
-          for (int i = 0; i < NT; ++i) t[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j & 1].v[x], w.v[i][x], t[i], 0, 0, 0);
-        fold(q > 0 ? j : (j + MT - 1) % MT);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          last[i] = t[i];
-          last_s[i] = w.s[i][q];
+            for (int e = 0; e < 16; ++e) from[e] = 0.0f;
+          }
+          t[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[c & 1][j], b[c & 1][i], kFirst ? from : t[j][i], 0, 0, 0);
         }
-      });
+      }
+      if constexpr (kFirst) {
 #pragma unroll
-      for (int x = j * NT * 4 / MT; x < (j + 1) * NT * 4 / MT; ++x) convert(c, x / 4, x % 4, next);
-      // matrix instructions and the others in turn
-      constexpr int kOther = (8 * NG * NT / 2 + 20 * NT * 4 / MT) / (4 * NT) + 1;
-      __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-      mx_unroll<0, 4 * NT>([&](auto) __attribute__((always_inline)) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, kOther, 0);
-      });
-      __builtin_amdgcn_sched_barrier(0);  // without it the registers of several rounds do not fit
+        for (int i = 0; i < NS; ++i) {
+          scale[i] = i4_scale_of(x.s[i], q, op.scale_bf16);
+          zero[i] = -kI4Bias - i4_zero_of(x.s[i], q);
+        }
+      }
+      read_a(c < 7 ? cur : nxt, (c + 1) % 8);
+      if constexpr (c == 5) y = read_codes(nxt);
+      convert(c < 7 ? x : y, (c + 1) % 8);
+      if constexpr (c == 2) sums_read(nxt);
+      if constexpr (c == 3) sums_form();
+      if constexpr (c == 5) sums_write(nxt);
+      // a matrix instruction and others in turn
+      if constexpr (!kFirst) {
+        mx_unroll<0, MT * NS>([&](auto) __attribute__((always_inline)) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+        });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      // a share of the next transfers: all at once they hold up what follows
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+        if (i * 4 / ND == c) issue(i, s + 2u, prev);
     });
+    x = y;
   };
 
-  issue_w(0);
-  mx_unroll<0, PRE>([&](auto d) __attribute__((always_inline)) {
-    issue_a(decltype(d)::value);
-    issue_w(decltype(d)::value + 1);
-  });
-  Weights even, odd;
-  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(PRE * ND) : "memory");
-  {
-    const Codes c = read_codes(0);
 #pragma unroll
-    for (int x = 0; x < NT * 4; ++x) convert(c, x / 4, x % 4, even);
+  for (int i = 0; i < ND; ++i) issue(i, 0u, 0u);
+#pragma unroll
+  for (int i = 0; i < ND; ++i) issue(i, 1u, kBuf);
+  step_barrier<ND>();
+  sums_read(0u);
+  sums_form();
+  sums_write(0u);
+  if constexpr (ZEROS) {  // "the step before" has sums of zero
+    for (uint32_t i = threadIdx.x; i < NG * BM; i += 64u * kWaves) *reinterpret_cast<float *>(lds + 2u * kBuf + kSum + i * 4u) = 0.0f;
   }
-  uint32_t s = 0;
-  for (; s + 1u < kt; s += 2u) {
-    step(s, even, odd);
-    step(s + 1u, odd, even);
+  x = read_codes(0u);
+  read_a(0u, 0);
+  convert(x, 0);
+  uint32_t prev = 2 * kBuf, cur = 0, nxt = kBuf;
+  for (uint32_t s = 0; s < kt; ++s) {
+    step(s, prev, cur, nxt);
+    const uint32_t free = prev;
+    prev = cur;
+    cur = nxt;
+    nxt = free;
   }
-  if (s < kt) step(s, even, odd);
-  fold(MT - 1);
-  step_barrier<0>();  // nothing is in flight, and everybody has read the last stage
-
-  const uint32_t n = r;
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
+    f32x16_t z = {};
+    if constexpr (ZEROS) z = sums_of(prev, NG - 1, j);
 #pragma unroll
-    for (uint32_t e = 0; e < 4; ++e) {
-      const uint32_t m = j * 16u + 4u * g + e;
-      if (m >= rows) continue;
-      const uint64_t row = ROWS == kDense ? first + m : pair_of(m);
+    for (int i = 0; i < NS; ++i) fold(j, i, z);
+  }
+  step_barrier<0>();  // nothing is in flight
+
+  if constexpr (ROWS == kLists && !GATED) {  // 128 bytes of a row each half wave
 #pragma unroll
-      for (int i = 0; i < (GATED ? 1 : NT); ++i) {
-        const uint32_t c = (t0 + i) * 16u + n;
-        if (c >= op.N) continue;
-        if constexpr (ROWS == kLists && !GATED) {
-          op.Y[row * op.N + c] = acc[i][j][e];
-        } else {
-          const float y = GATED ? silu_times(acc[0][j][e], acc[NT - 1][j][e]) : acc[i][j][e];
-          op.C[row * op.ldc + c] = (uint16_t)bf16x2_rne(y, 0.0f);
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (uint32_t e = 0; e < 16; ++e) {
+        const uint32_t m = (wm * MT + j) * 32u + 8u * (e >> 2) + 4u * kk + (e & 3u);
+        float *y = op.Y + (uint64_t)pair_of[m] * op.N;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const uint32_t c = col * (BNT * 16u) + (wn * NS + i) * 32u + n5;
+          if (m < rows && c < op.N) y[c] = acc[j][i][e];
         }
+      }
+  } else {
+    // Through LDS, to leave in whole pieces of 16 bytes.  Rows 16 bytes longer than their values.
+    constexpr uint32_t kCols = BNT * 16, kRow = kCols * 2 + 16, kPieces = kCols / 8;
+    static_assert(BM * kRow <= NBUF * kBuf, "outputs fit in the stages");
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (uint32_t e = 0; e < 16; ++e) {
+        const uint32_t m = (wm * MT + j) * 32u + 8u * (e >> 2) + 4u * kk + (e & 3u);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          float y = acc[j][i][e];
+          if constexpr (GATED) y = silu_times(y, __shfl_xor(y, 16));  // the up matrix's column is 16 lanes on
+          const uint32_t c = GATED ? (wn * NS + i) * 16u + r : (wn * NS + i) * 32u + n5;
+          if (!GATED || n5 < 16u) *reinterpret_cast<uint16_t *>(lds + m * kRow + c * 2u) = (uint16_t)bf16x2_rne(y, 0.0f);
+        }
+      }
+    __syncthreads();
+    const bool wide = (reinterpret_cast<uint64_t>(op.C) & 15u) == 0u && op.ldc % 8u == 0u;
+    for (uint32_t x = threadIdx.x; x < rows * kPieces; x += 64u * kWaves) {
+      const uint32_t m = x / kPieces, n = col * kCols + x % kPieces * 8u;
+      if (n >= op.N) continue;
+      const uint8_t *from = lds + m * kRow + x % kPieces * 16u;
+      uint16_t *to = op.C + (uint64_t)(ROWS == kDense ? first + m : pair_of[m]) * op.ldc + n;
+      if (wide && n + 8u <= op.N) {
+        *reinterpret_cast<u32x4_t *>(to) = *reinterpret_cast<const u32x4_t *>(from);
+      } else {
+        for (uint32_t i = 0; i < 8u && n + i < op.N; ++i) to[i] = reinterpret_cast<const uint16_t *>(from)[i];
       }
     }
   }
@@ -323,39 +408,39 @@ hipError_t allow_lds(const void *kern, std::atomic<uint64_t> &ready) {
   return e;
 }
 
-template <int BM, int NT, bool GATED, int NG, bool ZEROS, int ROWS, int PRE>
+template <int BM, int WM, bool GATED, int NG, bool ZEROS, int ROWS>
 hipError_t launch_kernel(const I4Operands &op, uint32_t tm, hipStream_t stream) {
-  const auto kern = i4_tile_kernel<BM, NT, GATED, NG, ZEROS, ROWS, PRE>;
-  constexpr uint32_t kLds = kLdsBytes<BM, NT, NG, ZEROS, PRE>;
+  const auto kern = i4_tile_kernel<BM, WM, GATED, NG, ZEROS, ROWS>;
+  constexpr uint32_t kLds = kLdsBytes<BM, NG, ZEROS>;
   static_assert(kLds <= 160 * 1024, "one workgroup's LDS");
   static std::atomic<uint64_t> ready;  // devices on which the kernel may use that much LDS
   const hipError_t attr = allow_lds(reinterpret_cast<const void *>(kern), ready);
   if (attr != hipSuccess) return attr;
-  constexpr uint32_t kCols = kWaves * NT * 16 / (GATED ? 2 : 1);
+  constexpr uint32_t kCols = kWaves * 16 * (GATED ? 1 : 2);
   hipLaunchKernelGGL(kern, dim3(tm * ((op.N + kCols - 1u) / kCols)), dim3(64 * kWaves), kLds, stream, op, tm);
   return hipGetLastError();
 }
 
-template <int BM, int NT, bool GATED, int ROWS, int PRE>
+template <int BM, int WM, bool GATED, int ROWS>
 hipError_t launch_cfg(const I4Operands &op, uint32_t tm, hipStream_t stream) {
   const bool z = op.w.Z != nullptr;
   if (op.group == 128u)
-    return z ? launch_kernel<BM, NT, GATED, 1, true, ROWS, PRE>(op, tm, stream) : launch_kernel<BM, NT, GATED, 1, false, ROWS, PRE>(op, tm, stream);
+    return z ? launch_kernel<BM, WM, GATED, 1, true, ROWS>(op, tm, stream) : launch_kernel<BM, WM, GATED, 1, false, ROWS>(op, tm, stream);
   if (op.group == 64u)
-    return z ? launch_kernel<BM, NT, GATED, 2, true, ROWS, PRE>(op, tm, stream) : launch_kernel<BM, NT, GATED, 2, false, ROWS, PRE>(op, tm, stream);
-  return z ? launch_kernel<BM, NT, GATED, 4, true, ROWS, PRE>(op, tm, stream) : launch_kernel<BM, NT, GATED, 4, false, ROWS, PRE>(op, tm, stream);
+    return z ? launch_kernel<BM, WM, GATED, 2, true, ROWS>(op, tm, stream) : launch_kernel<BM, WM, GATED, 2, false, ROWS>(op, tm, stream);
+  return z ? launch_kernel<BM, WM, GATED, 4, true, ROWS>(op, tm, stream) : launch_kernel<BM, WM, GATED, 4, false, ROWS>(op, tm, stream);
 }
 
-template <int BM, int NT, bool GATED, int PRE>
+template <int BM, int WM, bool GATED>
 hipError_t launch_dense(const I4Operands &op, hipStream_t stream) {
-  constexpr uint32_t kCols = kWaves * NT * 16 / (GATED ? 2 : 1);
+  constexpr uint32_t kCols = kWaves * 16 * (GATED ? 1 : 2);
   const uint32_t rows = mx_max_grid(64 * kWaves) / ((op.N + kCols - 1u) / kCols) * BM;
   for (uint32_t m = 0; m < op.M; m += rows) {
     I4Operands part = op;
     part.A = op.A + (uint64_t)m * op.lda;
     part.C = op.C + (uint64_t)m * op.ldc;
     part.M = op.M - m < rows ? op.M - m : rows;
-    const hipError_t e = launch_cfg<BM, NT, GATED, kDense, PRE>(part, (part.M + BM - 1u) / BM, stream);
+    const hipError_t e = launch_cfg<BM, WM, GATED, kDense>(part, (part.M + BM - 1u) / BM, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -365,15 +450,20 @@ hipError_t launch_dense(const I4Operands &op, hipStream_t stream) {
 
 hipError_t launch_i4_product(const I4Operands &op, hipStream_t stream) {
   if (op.M <= 64u) return launch_i4_skinny(op, op.gated, stream);
-  return op.gated ? launch_dense<128, 2, true, 1>(op, stream) : launch_dense<128, 2, false, 1>(op, stream);
+  if (op.M <= 64u) return op.gated ? launch_dense<64, 1, true>(op, stream) : launch_dense<64, 1, false>(op, stream);
+  return op.gated ? launch_dense<128, 2, true>(op, stream) : launch_dense<128, 2, false>(op, stream);
 }
 
 hipError_t launch_i4_experts(const I4Operands &op, hipStream_t stream) {
   const uint32_t pairs = op.T * op.top_k;
-  if (!op.order || pairs / op.E < 48u || (uint64_t)(op.gated ? op.T : pairs) * op.lda * 2u >= 1ull << 32)
+  if (!op.order || pairs / op.E < 24u || (uint64_t)(op.gated ? op.T : pairs) * op.lda * 2u >= 1ull << 32)
     return launch_i4_experts_skinny(op, stream);
+  if (pairs / op.E < 200u) {
+    const uint32_t chunks = (uint32_t)i4_chunks(pairs, op.E, 64u);
+    return op.gated ? launch_cfg<64, 1, true, kLists>(op, chunks, stream) : launch_cfg<64, 1, false, kLists>(op, chunks, stream);
+  }
   const uint32_t chunks = (uint32_t)i4_chunks(pairs, op.E, 128u);
-  return op.gated ? launch_cfg<128, 2, true, kLists, 1>(op, chunks, stream) : launch_cfg<128, 2, false, kLists, 1>(op, chunks, stream);
+  return op.gated ? launch_cfg<128, 2, true, kLists>(op, chunks, stream) : launch_cfg<128, 2, false, kLists>(op, chunks, stream);
 }
 
 }  // namespace wqd
