@@ -26,10 +26,9 @@
 namespace wqd {
 namespace {
 
-// Waves of a workgroup, and steps in flight.  4 or 16 waves, and 1, 3, 4 or 6 steps, are slower at most sizes
-// (1 x 5120, K = 5120 6.0 us; 16 waves 7.9, 4 waves 7.3, 3 steps 6.3, 4 steps 6.4): the registers of a deeper
-// ring keep further workgroups off the compute unit.
-constexpr int NW = 8, DEPTH = 2;
+// Waves of a workgroup, but for kSum.  4 or 16 are slower at most sizes (1 x 5120, K = 5120 6.0 us, with 16 waves 7.9,
+// with 4 7.3).
+constexpr int kWaves = 8;
 
 // Where a workgroup's rows come from.
 constexpr int kDense = 0;  // rows m0 ..
@@ -47,9 +46,10 @@ struct Rest {
   uint32_t ldc, scale_bf16, top_k, E;
 };
 
-// NT: 16-row weight tiles of a workgroup (of either matrix); the arguments up to
-// SU are in registers when a wave starts.  M: rows, or tokens.
-template <int MMAX, int NT, bool GATED, int NG, bool ZEROS, int ROWS>
+// NT: 16-row weight tiles of a wave (of either matrix).  KS of the NW waves share K; NW / KS
+// such groups stand side by side.  DEPTH: steps in flight.  The arguments up to SU are in
+// registers when a wave starts.  M: rows, or tokens.
+template <int NW, int MMAX, int NT, int KS, int DEPTH, bool GATED, int NG, bool ZEROS, int ROWS>
 __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__restrict__ W, const uint16_t *__restrict__ S,
                                                             const uint16_t *__restrict__ A, uint32_t K, uint32_t N,
                                                             uint32_t M, uint32_t lda, const uint8_t *__restrict__ Z,
@@ -63,7 +63,8 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__res
 
   const uint32_t tid = threadIdx.x, lane = tid & 63u, r = lane & 15u, g = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const uint32_t tiles = (N + 15u) >> 4, kt = K >> 7, tile = blockIdx.x * NT;
+  const uint32_t tiles = (N + 15u) >> 4, kt = K >> 7, ks = wave % KS;
+  const uint32_t tile0 = blockIdx.x * (NW / KS * NT), tile = tile0 + wave / KS * NT;  // of the workgroup, of this wave
 
   // which rows and which matrix
   uint32_t first = blockIdx.y, rows = 1, expert = 0;  // first: row, place in the lists, pair or token
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__res
 
   // this wave's steps: the tiles of a row of tiles, or of all slots' after another
   const uint32_t total = ROWS == kSum ? kt * op.top_k : kt;
-  const uint32_t u0 = total * wave / NW, u1 = total * (wave + 1u) / NW;
+  const uint32_t u0 = total * ks / KS, u1 = total * (ks + 1u) / KS;
 
   const u32x4_t *arow[SA];  // of each 16-byte piece that this lane brings
 #pragma unroll
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__res
     asm volatile("" : "+s"(t));
 #pragma unroll
     for (int j = 0; j < WT; ++j) {
-      const uint32_t row = NT == 1 || tile + j / G < tiles ? tile + j / G : tiles - 1u;
+      const uint32_t row = tile + j / G < tiles ? tile + j / G : tiles - 1u;
       const uint64_t at = ((uint64_t)e * tiles + row) * kt + t;
       const bool up = GATED && (j & 1);
       x.w[j] = *reinterpret_cast<const u32x4_t *>((up ? WU : W) + at * kI4Tile + lane * 16u);
@@ -217,16 +218,16 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__res
       for (int i = 0; i < MT; ++i) part[((wave * WT + t) * MT + i) * kLanes + lane] = acc[t][i];
   }
   __syncthreads();
-  for (uint32_t x = tid; x < kLanes * MT * NT; x += 64u * NW) {
-    const uint32_t l = x % kLanes, i = x / kLanes % MT, t = x / (kLanes * MT);
+  for (uint32_t x = tid; x < kLanes * MT * NT * (NW / KS); x += 64u * NW) {
+    const uint32_t l = x % kLanes, i = x / kLanes % MT, at = x / (kLanes * MT), t = at % NT, w0 = at / NT * KS;
     f32x4_t c[G];
 #pragma unroll
     for (int h = 0; h < G; ++h) {
-      c[h] = part[((t * G + h) * MT + i) * kLanes + l];
+      c[h] = part[((w0 * WT + t * G + h) * MT + i) * kLanes + l];
 #pragma unroll
-      for (uint32_t w = 1; w < NW; ++w) c[h] += part[((w * WT + t * G + h) * MT + i) * kLanes + l];
+      for (uint32_t w = 1; w < KS; ++w) c[h] += part[(((w0 + w) * WT + t * G + h) * MT + i) * kLanes + l];
     }
-    const uint32_t col = (tile + t) * 16u + (l & 15u);
+    const uint32_t col = (tile0 + at) * 16u + (l & 15u);
     if (col >= N) continue;
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j) {
@@ -242,77 +243,90 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__res
   }
 }
 
-// `count`: chunks, pairs or tokens, which are cut into launches that the grid's second dimension holds.
-template <int MMAX, int NT, bool GATED, int NG, bool ZEROS, int ROWS>
+template <int MMAX, int NT, int KS, int DEPTH, bool GATED, int NG, bool ZEROS, int ROWS>
 hipError_t launch_kernel(const I4Operands &op, uint32_t count, hipStream_t stream) {
+  constexpr int NW = KS > kWaves ? KS : kWaves;
+  constexpr uint32_t kCols = 16 * NT * (NW / KS);
   const Rest rest = {op.up.Z, op.C, op.Y, op.ids, op.order, op.offsets, op.weights, op.ldc, op.scale_bf16, op.top_k, op.E};
-  hipLaunchKernelGGL((i4_skinny_kernel<MMAX, NT, GATED, NG, ZEROS, ROWS>), dim3((op.N + 16u * NT - 1u) / (16u * NT), count),
+  hipLaunchKernelGGL((i4_skinny_kernel<NW, MMAX, NT, KS, DEPTH, GATED, NG, ZEROS, ROWS>), dim3((op.N + kCols - 1u) / kCols, count),
                      dim3(64 * NW), 0, stream, op.w.W, op.w.S, op.A, op.K, op.N, ROWS == kDense ? op.M : op.T, op.lda, op.w.Z,
                      op.up.W, op.up.S, rest);
   return hipGetLastError();
 }
 
-template <int MMAX, int NT, bool GATED, int ROWS>
+// `count`: chunks, pairs or tokens, the grid's second dimension
+template <int MMAX, int NT, int KS, int DEPTH, bool GATED, int ROWS>
 hipError_t launch_cfg(const I4Operands &op, uint32_t count, hipStream_t stream) {
   const bool z = op.w.Z != nullptr;
   if (op.group == 128u)
-    return z ? launch_kernel<MMAX, NT, GATED, 1, true, ROWS>(op, count, stream)
-             : launch_kernel<MMAX, NT, GATED, 1, false, ROWS>(op, count, stream);
+    return z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, 1, true, ROWS>(op, count, stream)
+             : launch_kernel<MMAX, NT, KS, DEPTH, GATED, 1, false, ROWS>(op, count, stream);
   if (op.group == 64u)
-    return z ? launch_kernel<MMAX, NT, GATED, 2, true, ROWS>(op, count, stream)
-             : launch_kernel<MMAX, NT, GATED, 2, false, ROWS>(op, count, stream);
-  return z ? launch_kernel<MMAX, NT, GATED, 4, true, ROWS>(op, count, stream)
-           : launch_kernel<MMAX, NT, GATED, 4, false, ROWS>(op, count, stream);
+    return z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, 2, true, ROWS>(op, count, stream)
+             : launch_kernel<MMAX, NT, KS, DEPTH, GATED, 2, false, ROWS>(op, count, stream);
+  return z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, 4, true, ROWS>(op, count, stream)
+           : launch_kernel<MMAX, NT, KS, DEPTH, GATED, 4, false, ROWS>(op, count, stream);
 }
 
 // Chunks (pairs, tokens) of one launch: the grid's second dimension holds 65535, and all its threads are half of 2^32
 // at most.
-template <int NT>
 uint32_t most_of(const I4Operands &op) {
-  const uint32_t fit = mx_max_grid(64 * NW) / ((op.N + 16u * NT - 1u) / (16u * NT));
+  const uint32_t fit = mx_max_grid(64 * 16) / ((op.N + 15u) / 16u);
   return fit < 65535u ? fit : 65535u;
 }
 
-template <int MMAX, int NT, bool GATED>
+template <int MMAX, int NT, int DEPTH, bool GATED>
 hipError_t launch_dense(const I4Operands &op, hipStream_t stream) {
-  const uint32_t rows = most_of<NT>(op) * MMAX;
+  const uint32_t rows = most_of(op) * MMAX;
   for (uint32_t m = 0; m < op.M; m += rows) {
     I4Operands part = op;
     part.A = op.A + (uint64_t)m * op.lda;
     part.C = op.C + (uint64_t)m * op.ldc;
     part.M = op.M - m < rows ? op.M - m : rows;
-    const hipError_t e = launch_cfg<MMAX, NT, GATED, kDense>(part, (part.M + MMAX - 1u) / MMAX, stream);
+    const hipError_t e = launch_cfg<MMAX, NT, kWaves, DEPTH, GATED, kDense>(part, (part.M + MMAX - 1u) / MMAX, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
+// Steps in flight: two.  More keep further workgroups off the compute unit by their registers (1 x 5120, K = 5120 6.0
+// us, with three 6.3, with four 6.4).
 template <bool GATED>
-hipError_t launch_rows(const I4Operands &op, hipStream_t stream) {
-  constexpr int kWide = GATED ? 1 : 2;
-  if (op.M <= 4u) return launch_dense<4, 1, GATED>(op, stream);
-  if (op.M <= 8u) return launch_dense<8, kWide, GATED>(op, stream);
-  return launch_dense<16, kWide, GATED>(op, stream);
+hipError_t launch_rows(const I4Operands &op, bool wide, hipStream_t stream) {
+  constexpr int kTwo = GATED ? 1 : 2;
+  if (op.M <= 4u) return launch_dense<4, 1, 2, GATED>(op, stream);
+  if (op.M <= 8u) return launch_dense<8, kTwo, 2, GATED>(op, stream);
+  if (!wide) return launch_dense<16, kTwo, 2, GATED>(op, stream);
+  return launch_dense<32, 2 * kTwo, 1, GATED>(op, stream);
 }
 
 }  // namespace
 
-hipError_t launch_i4_skinny(const I4Operands &op, bool gated, hipStream_t stream) {
-  return gated ? launch_rows<true>(op, stream) : launch_rows<false>(op, stream);
+hipError_t launch_i4_skinny(const I4Operands &op, bool wide, hipStream_t stream) {
+  return op.gated ? launch_rows<true>(op, wide, stream) : launch_rows<false>(op, wide, stream);
 }
 
 bool i4_experts_fit(const I4Operands &op) {
   const uint64_t pairs = (uint64_t)op.T * op.top_k;
-  return (op.order ? i4_chunks(pairs, op.E, 16u) : (op.gated ? pairs : op.T)) <= most_of<1>(op);
+  return (op.order ? i4_chunks(pairs, op.E, 16u) : (op.gated ? pairs : op.T)) <= most_of(op);
 }
 
+// With lists two waves share K and four such pairs stand side by side: with all eight on K a wave has a step or two,
+// and a workgroup's start (its expert, its rows, their first values) takes longer than its work (33 tokens of 8 of 64
+// experts, 2048 outputs, K = 1024 72 -> 27 us with two weight tiles for a wave, gated 1024 outputs, K = 2048 49 -> 33).
+// Without, a workgroup has one row: four waves on K below 4096 (1 token, K = 2048 5.8 -> 5.5 us), eight from there on (K = 5120
+// 7.8 -> 5.4); and a token's sum takes sixteen where its workgroups leave compute units idle (1 token, 2048 outputs 7.5
+// -> 6.2 us).
 hipError_t launch_i4_experts_skinny(const I4Operands &op, hipStream_t stream) {
   const uint32_t pairs = op.T * op.top_k;
   if (op.order) {
     const uint32_t chunks = (uint32_t)i4_chunks(pairs, op.E, 16u);
-    return op.gated ? launch_cfg<16, 1, true, kLists>(op, chunks, stream) : launch_cfg<16, 1, false, kLists>(op, chunks, stream);
+    return op.gated ? launch_cfg<16, 1, 2, 2, true, kLists>(op, chunks, stream) : launch_cfg<16, 2, 2, 2, false, kLists>(op, chunks, stream);
   }
-  return op.gated ? launch_cfg<4, 1, true, kPairs>(op, pairs, stream) : launch_cfg<4, 1, false, kSum>(op, op.T, stream);
+  if (op.gated)
+    return op.K < 4096u ? launch_cfg<4, 1, 4, 2, true, kPairs>(op, pairs, stream) : launch_cfg<4, 1, 8, 2, true, kPairs>(op, pairs, stream);
+  return (uint64_t)((op.N + 15u) / 16u) * op.T <= 256u ? launch_cfg<4, 1, 16, 2, false, kSum>(op, op.T, stream)
+                                                      : launch_cfg<4, 1, 8, 1, false, kSum>(op, op.T, stream);
 }
 
 }  // namespace wqd

@@ -446,23 +446,67 @@ hipError_t launch_dense(const I4Operands &op, hipStream_t stream) {
   return hipSuccess;
 }
 
+// What a way to multiply takes, in ns: one round of its tiles over 256 compute units (`first` and
+// `first_step` for each 128 k), and every further one.  Measured at 24 to 1024 rows times 512, 5120 and 17408 outputs,
+// K = 512 to 17408 (MI355X, weights from memory).
+struct Cost {
+  uint32_t bm, bn;  // outputs of a tile, half as many in the gated form
+  uint32_t first, first_step, more, more_step;
+};
+constexpr Cost kCosts[] = {{16, 32, 3000, 70, 600, 88}, {32, 64, 3200, 220, 0, 230}, {64, 256, 3500, 1190, 1500, 1190},
+                           {128, 256, 5000, 1620, 3000, 1620}};
+
+// The same with lists, whose tiles first find their expert and rows: 64 to 2048 tokens of 8 of 64 experts, 2048 outputs,
+// K = 1024, and gated 1024 outputs, K = 2048.
+constexpr Cost kListCosts[] = {{16, 128, 8000, 330, 1300, 330}, {64, 256, 8000, 1190, 6000, 1190}, {128, 256, 10000, 1620, 12000, 1620}};
+
+uint64_t cost_of(const Cost &c, uint64_t tiles, uint32_t steps) {
+  const uint64_t rounds = (tiles + 255u) / 256u;
+  return c.first + c.first_step * steps + (rounds > 1u ? (rounds - 1u) * (c.more + (uint64_t)c.more_step * steps) : 0u);
+}
+
+// Index of the least cost; chunks(bm): tiles of bm rows.
+template <uint32_t COUNT, typename F>
+uint32_t least(const Cost (&costs)[COUNT], const I4Operands &op, F &&chunks) {
+  const uint32_t n = op.gated ? 2u * op.N : op.N;
+  uint64_t best = ~0ull;
+  uint32_t at = 0;
+  for (uint32_t i = 0; i < COUNT; ++i) {
+    const uint64_t x = cost_of(costs[i], chunks(costs[i].bm) * ((n + costs[i].bn - 1u) / costs[i].bn), op.K >> 7);
+    if (x < best) {
+      best = x;
+      at = i;
+    }
+  }
+  return at;
+}
+
 }  // namespace
 
+// 0 and 1 are the kernel for few rows, which splits K eight ways over the waves of a tile: in chunks of 16 rows, and of 32
+// with twice the weight rows, where its activations pass through fewer workgroups (96 x 5120, K = 5120 17.3 -> 12.3 us).
+// Tiles cost less per output and wait for each of their steps: 256 x 5120, K = 5120 30.5 us in chunks, 51 in tiles of 64
+// rows and 70 of 128; 1024 rows 143 in chunks of 16, 103 and 71 in tiles.
 hipError_t launch_i4_product(const I4Operands &op, hipStream_t stream) {
-  if (op.M <= 64u) return launch_i4_skinny(op, op.gated, stream);
-  if (op.M <= 64u) return op.gated ? launch_dense<64, 1, true>(op, stream) : launch_dense<64, 1, false>(op, stream);
+  const uint32_t way = op.M <= 16u ? 0u : least(kCosts, op, [&](uint32_t bm) { return (uint64_t)((op.M + bm - 1u) / bm); });
+  if (way < 2u) return launch_i4_skinny(op, way == 1u, stream);
+  if (way == 2u) return op.gated ? launch_dense<64, 1, true>(op, stream) : launch_dense<64, 1, false>(op, stream);
   return op.gated ? launch_dense<128, 2, true>(op, stream) : launch_dense<128, 2, false>(op, stream);
 }
 
+// The lists' lengths are on the GPU: every expert is taken to have the mean of rows, and a quarter of them a chunk more.
+// Rows of more than 4 GB are beyond the tiles' offsets.
 hipError_t launch_i4_experts(const I4Operands &op, hipStream_t stream) {
-  const uint32_t pairs = op.T * op.top_k;
-  if (!op.order || pairs / op.E < 24u || (uint64_t)(op.gated ? op.T : pairs) * op.lda * 2u >= 1ull << 32)
-    return launch_i4_experts_skinny(op, stream);
-  if (pairs / op.E < 200u) {
-    const uint32_t chunks = (uint32_t)i4_chunks(pairs, op.E, 64u);
-    return op.gated ? launch_cfg<64, 1, true, kLists>(op, chunks, stream) : launch_cfg<64, 1, false, kLists>(op, chunks, stream);
-  }
-  const uint32_t chunks = (uint32_t)i4_chunks(pairs, op.E, 128u);
+  const uint32_t pairs = op.T * op.top_k, busy = pairs < op.E ? pairs : op.E;
+  uint32_t way = 0;
+  if (op.order && (uint64_t)(op.gated ? op.T : pairs) * op.lda * 2u < 1ull << 32)
+    way = least(kListCosts, op, [&](uint32_t bm) {
+      const uint64_t chunks = pairs / bm + busy / 4u;
+      return chunks > busy ? chunks : (uint64_t)busy;
+    });
+  if (way == 0u) return launch_i4_experts_skinny(op, stream);
+  const uint32_t chunks = (uint32_t)i4_chunks(pairs, op.E, way == 1u ? 64u : 128u);
+  if (way == 1u) return op.gated ? launch_cfg<64, 1, true, kLists>(op, chunks, stream) : launch_cfg<64, 1, false, kLists>(op, chunks, stream);
   return op.gated ? launch_cfg<128, 2, true, kLists>(op, chunks, stream) : launch_cfg<128, 2, false, kLists>(op, chunks, stream);
 }
 

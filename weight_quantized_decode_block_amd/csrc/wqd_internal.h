@@ -124,9 +124,9 @@ struct I4Operands {
 };
 
 // Enqueue a dense product (i4_tile.hip chooses the kernel; launch_i4_skinny is
-// the one for few rows, which takes any size).
+// the one for few rows, which takes any size, `wide` in chunks of 32 rows, else 16).
 hipError_t launch_i4_product(const I4Operands &op, hipStream_t stream);
-hipError_t launch_i4_skinny(const I4Operands &op, bool gated, hipStream_t stream);
+hipError_t launch_i4_skinny(const I4Operands &op, bool wide, hipStream_t stream);
 
 // Enqueue the experts' products: gated (C gets a row per pair), or the last ones
 // (with lists: Y gets a row per pair; without: C gets each token's weighted sum).
