@@ -267,8 +267,8 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
       acc[j][i][e] = __builtin_fmaf(scale[i], ZEROS ? __builtin_fmaf(zero[i], z[e], t[j][i][e]) : t[j][i][e], acc[j][i][e]);
     asm volatile("" : "+v"(acc[j][i]));
   };
-  Codes x;
-  auto step = [&](uint32_t s, uint32_t prev, uint32_t cur, uint32_t nxt) __attribute__((always_inline)) {
+  Codes even;
+  auto step = [&](uint32_t s, uint32_t prev, uint32_t cur, uint32_t nxt, const Codes &x, Codes &after) __attribute__((always_inline)) {
     step_barrier<0>();
     Codes y;
     mx_unroll<0, 8>([&](auto C) __attribute__((always_inline)) {
@@ -316,7 +316,7 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
       for (int i = 0; i < ND; ++i)
         if (i * 4 / ND == c) issue(i, s + 2u, prev);
     });
-    x = y;
+    after = y;
   };
 
 #pragma unroll
@@ -330,16 +330,40 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
   if constexpr (ZEROS) {  // "the step before" has sums of zero
     for (uint32_t i = threadIdx.x; i < NG * BM; i += 64u * kWaves) *reinterpret_cast<float *>(lds + 2u * kBuf + kSum + i * 4u) = 0.0f;
   }
-  x = read_codes(0u);
+  even = read_codes(0u);
   read_a(0u, 0);
-  convert(x, 0);
+  convert(even, 0);
   uint32_t prev = 2 * kBuf, cur = 0, nxt = kBuf;
-  for (uint32_t s = 0; s < kt; ++s) {
-    step(s, prev, cur, nxt);
+  auto turn = [&]() __attribute__((always_inline)) {
     const uint32_t free = prev;
     prev = cur;
     cur = nxt;
     nxt = free;
+  };
+  // Two steps an iteration: then no sums are copied from the registers that one step leaves
+  // them in to those that the next expects (1000 x 5120, K = 17408: 225 -> 202 us; 1000 x
+  // 5120, K = 5120 71.5 -> 64.5). With zero points it gains nothing, and with groups of 32 the registers no longer suffice.
+  if constexpr (NG <= 2 && !ZEROS) {
+    Codes odd;
+    uint32_t s = 0;
+    for (; s + 1u < kt; s += 2u) {
+      step(s, prev, cur, nxt, even, odd);
+      turn();
+      step(s + 1u, prev, cur, nxt, odd, even);
+      turn();
+    }
+    if (s < kt) {
+      step(s, prev, cur, nxt, even, odd);
+      turn();
+    }
+  } else {
+    for (uint32_t s = 0; s < kt; ++s) {
+      step(s, prev, cur, nxt, even, even);
+      const uint32_t free = prev;
+      prev = cur;
+      cur = nxt;
+      nxt = free;
+    }
   }
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
@@ -454,11 +478,11 @@ struct Cost {
   uint32_t first, first_step, more, more_step;
 };
 constexpr Cost kCosts[] = {{16, 32, 3000, 70, 600, 88}, {32, 64, 3200, 220, 0, 230}, {64, 256, 3500, 1190, 1500, 1190},
-                           {128, 256, 5000, 1620, 3000, 1620}};
+                           {128, 256, 5000, 1490, 3000, 1490}};
 
 // The same with lists, whose tiles first find their expert and rows: 64 to 2048 tokens of 8 of 64 experts, 2048 outputs,
 // K = 1024, and gated 1024 outputs, K = 2048.
-constexpr Cost kListCosts[] = {{16, 128, 8000, 330, 1300, 330}, {64, 256, 8000, 1190, 6000, 1190}, {128, 256, 10000, 1620, 12000, 1620}};
+constexpr Cost kListCosts[] = {{16, 128, 8000, 330, 1300, 330}, {64, 256, 8000, 1190, 6000, 1190}, {128, 256, 10000, 1540, 12000, 1540}};
 
 uint64_t cost_of(const Cost &c, uint64_t tiles, uint32_t steps) {
   const uint64_t rounds = (tiles + 255u) / 256u;
@@ -486,7 +510,7 @@ uint32_t least(const Cost (&costs)[COUNT], const I4Operands &op, F &&chunks) {
 // 0 and 1 are the kernel for few rows, which splits K eight ways over the waves of a tile: in chunks of 16 rows, and of 32
 // with twice the weight rows, where its activations pass through fewer workgroups (96 x 5120, K = 5120 17.3 -> 12.3 us).
 // Tiles cost less per output and wait for each of their steps: 256 x 5120, K = 5120 30.5 us in chunks, 51 in tiles of 64
-// rows and 70 of 128; 1024 rows 143 in chunks of 16, 103 and 71 in tiles.
+// rows and 70 of 128; 1024 rows 143 in chunks of 16, 103 and 65 in tiles.
 hipError_t launch_i4_product(const I4Operands &op, hipStream_t stream) {
   const uint32_t way = op.M <= 16u ? 0u : least(kCosts, op, [&](uint32_t bm) { return (uint64_t)((op.M + bm - 1u) / bm); });
   if (way < 2u) return launch_i4_skinny(op, way == 1u, stream);
