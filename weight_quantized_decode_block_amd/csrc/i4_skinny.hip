@@ -10,11 +10,12 @@
 //     enter the BF16 matrix instruction as 16 + q (i4_biased), a second one
 //     against ones gives the activations' sum in the same lanes, and the group's
 //     scale meets both in fp32.  All products are exact, sums are fp32.
-//   * A workgroup of 8 waves owns 16 weight rows (of both matrices in the gated
-//     form) and up to MMAX activation rows; a wave has an eighth of K to itself, as
-//     consecutive tiles of 16 x 128 codes, which come in whole KB in the matrix
-//     operand's order.  Its activations come in row order and turn in LDS that is
-//     the wave's own.  The waves meet once, to add their sums in wave order.
+//   * A wave owns NT tiles of 16 weight rows (gated: of both matrices) and up to MMAX
+//     activation rows, and of K an eighth (with experts also a half, a quarter, a
+//     sixteenth): consecutive tiles of 16 x 128 codes, which come in whole KB in the
+//     matrix operand's order.  Its activations come in row order and turn in LDS that is
+//     the wave's own.  The waves meet once, to add their sums in wave order: no atomics,
+//     and no second launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -306,7 +307,7 @@ hipError_t launch_i4_skinny(const I4Operands &op, bool wide, hipStream_t stream)
   return op.gated ? launch_rows<true>(op, wide, stream) : launch_rows<false>(op, wide, stream);
 }
 
-bool i4_experts_fit(const I4Operands &op) {
+bool i4_experts_skinny_fit(const I4Operands &op) {
   const uint64_t pairs = (uint64_t)op.T * op.top_k;
   return (op.order ? i4_chunks(pairs, op.E, 16u) : (op.gated ? pairs : op.T)) <= most_of(op);
 }

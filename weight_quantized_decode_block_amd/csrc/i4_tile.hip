@@ -7,20 +7,21 @@
 // in n, so each converts its own weights only, once; all of them read all activations.
 //
 //   * Staging.  Activations, codes, scales and zero points go straight from memory to
-//     LDS, PRE steps ahead of their use, into PRE + 1 buffers; a wave waits for its
-//     own transfers by count.  Codes lie in the matrix operand's order, so a lane
-//     reads back what its neighbours brought in whole KB.  Rows past the last one
-//     repeat it; their outputs are not stored.
-//   * Codes become BF16 between the matrix instructions of the step before.  With zero
-//     points, the values of q - z (exact: integers of at most 8 bits): 1024 + q as FP16
-//     by two integer instructions a pair, minus 1024 + z by a mixed multiply-add
-//     each, and a conversion for two.  Without, 16 + q by the two integer instructions
-//     alone (i4_biased), and a group's sums start at -24 times its activations' sum: each
-//     wave forms those of 16 rows for all, a step ahead.
-//   * That is because all instructions of both waves of a SIMD share its issue: beside
-//     a 32 x 32 x 16 matrix instruction (32 cycles) there is room for six others of its
-//     wave, beside a 16 x 16 x 32 one for two.  32 rows are 8 matrix instructions, 16
-//     multiply-adds of scales and 38 conversions, or 16.
+//     LDS, two steps ahead of their use, into the third of three stages; a wave asks for
+//     an eighth of each.  Codes lie in the matrix operand's order, so a lane reads back
+//     what its neighbours brought in whole KB.  Rows past the last one repeat it; their
+//     outputs are not stored.
+//   * Codes become BF16 values 16 + q by two integer instructions a pair (i4_biased), a
+//     chunk of 16 k ahead of the matrix instructions that take them.  16 + z goes with the
+//     sums of the activations: without zero points a group's sums start at -24 times them,
+//     with zero points the fold takes (16 + z) times them away.  Each wave forms those of
+//     16 rows for all, by matrix instructions against ones, a step ahead.
+//   * All instructions of both waves of a SIMD share its issue: beside a 32 x 32 x 16
+//     matrix instruction (32 cycles) there is room for six others of its wave, beside a 16
+//     x 16 x 32 one for two.  Hence 32 x 32, and no more than two instructions for a pair of
+//     codes.  Of a step of 128 rows (1.45 us) the matrix instructions take 0.75; without the
+//     folds it would be 0.25 us shorter, without the sums 0.3, the transfers 0.24, the
+//     conversions 0.13.  4096 x 5120, K = 5120 213 us, 1.0 PFLOP/s.
 //   * The sums of a group are a matrix accumulator of their own, which the scale
 //     adds to the output's in fp32: nothing but the output is rounded.
 #include <hip/hip_runtime.h>
@@ -518,16 +519,26 @@ hipError_t launch_i4_product(const I4Operands &op, hipStream_t stream) {
   return op.gated ? launch_dense<128, 2, true>(op, stream) : launch_dense<128, 2, false>(op, stream);
 }
 
+// Whether one launch of tiles of bm rows holds the lists' products.  Rows of more than 4 GB are beyond its offsets.
+static bool i4_tiles_fit(const I4Operands &op, uint32_t bm) {
+  const uint32_t pairs = op.T * op.top_k, cols = kWaves * 16 * (op.gated ? 1 : 2);
+  return (uint64_t)(op.gated ? op.T : pairs) * op.lda * 2u < 1ull << 32 &&
+         i4_chunks(pairs, op.E, bm) * ((op.N + cols - 1u) / cols) <= mx_max_grid(64 * kWaves);
+}
+
+bool i4_experts_fit(const I4Operands &op) { return i4_experts_skinny_fit(op) || (op.order && i4_tiles_fit(op, 128u)); }
+
 // The lists' lengths are on the GPU: every expert is taken to have the mean of rows, and a quarter of them a chunk more.
-// Rows of more than 4 GB are beyond the tiles' offsets.
 hipError_t launch_i4_experts(const I4Operands &op, hipStream_t stream) {
   const uint32_t pairs = op.T * op.top_k, busy = pairs < op.E ? pairs : op.E;
   uint32_t way = 0;
-  if (op.order && (uint64_t)(op.gated ? op.T : pairs) * op.lda * 2u < 1ull << 32)
+  if (op.order && i4_tiles_fit(op, 128u)) {
     way = least(kListCosts, op, [&](uint32_t bm) {
       const uint64_t chunks = pairs / bm + busy / 4u;
       return chunks > busy ? chunks : (uint64_t)busy;
     });
+    if ((way == 0u && !i4_experts_skinny_fit(op)) || (way == 1u && !i4_tiles_fit(op, 64u))) way = 2u;
+  }
   if (way == 0u) return launch_i4_experts_skinny(op, stream);
   const uint32_t chunks = (uint32_t)i4_chunks(pairs, op.E, way == 1u ? 64u : 128u);
   if (way == 1u) return op.gated ? launch_cfg<64, 1, true, kLists>(op, chunks, stream) : launch_cfg<64, 1, false, kLists>(op, chunks, stream);

@@ -234,11 +234,11 @@ __global__ __launch_bounds__(64 * kListWaves) void moe_lists_kernel(const int32_
 
 // A thread adds four columns of a token's rows in slot order; slots without an
 // expert of these are passed over.
-__global__ __launch_bounds__(256) void moe_combine_kernel(I4Operands op) {
+__global__ __launch_bounds__(256) void moe_combine_kernel(I4Operands op, uint64_t from) {
   const uint32_t pieces = (op.N + 3u) / 4u;
-  const uint64_t x = (uint64_t)blockIdx.x * 256u + threadIdx.x;
+  const uint64_t x = from + (uint64_t)blockIdx.x * 256u + threadIdx.x;
   const uint32_t t = (uint32_t)(x / pieces), n = (uint32_t)(x - (uint64_t)t * pieces) * 4u;
-  if (t >= op.T) return;
+  if (x >= (uint64_t)op.T * pieces) return;
   float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (uint32_t s = 0; s < op.top_k; ++s) {
     const uint32_t p = t * op.top_k + s;
@@ -277,9 +277,14 @@ hipError_t launch_moe_lists(const int32_t *ids, int32_t *order, int32_t *offsets
 }
 
 hipError_t launch_moe_combine(const I4Operands &op, hipStream_t stream) {
-  const uint64_t threads = (uint64_t)op.T * ((op.N + 3u) / 4u);
-  hipLaunchKernelGGL(moe_combine_kernel, dim3((uint32_t)((threads + 255u) / 256u)), dim3(256), 0, stream, op);
-  return hipGetLastError();
+  const uint64_t threads = (uint64_t)op.T * ((op.N + 3u) / 4u), most = (uint64_t)mx_max_grid(256) * 256u;
+  for (uint64_t from = 0; from < threads; from += most) {
+    const uint64_t left = threads - from < most ? threads - from : most;
+    hipLaunchKernelGGL(moe_combine_kernel, dim3((uint32_t)((left + 255u) / 256u)), dim3(256), 0, stream, op, from);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace wqd
