@@ -13,9 +13,10 @@
 //     outputs are not stored.
 //   * Codes become BF16 values 16 + q by two integer instructions a pair (i4_biased), a
 //     chunk of 16 k ahead of the matrix instructions that take them.  16 + z goes with the
-//     sums of the activations: without zero points a group's sums start at -24 times them,
-//     with zero points the fold takes (16 + z) times them away.  Each wave forms those of
-//     16 rows for all, by matrix instructions against ones, a step ahead.
+//     sums of the activations: without zero points a group's sums start at -24 times them, with
+//     zero points at -(16 + z) times them, a product of rank one by a matrix instruction, for
+//     which a sum is split into three BF16 values (exact).  Each wave forms those of 16 rows for
+//     all, by matrix instructions against ones, a step ahead.
 //   * All instructions of both waves of a SIMD share its issue: beside a 32 x 32 x 16
 //     matrix instruction (32 cycles) there is room for six others of its wave, beside a 16
 //     x 16 x 32 one for two.  Hence 32 x 32, and no more than two instructions for a pair of
@@ -80,7 +81,7 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 // and the sums of the activations of each group; and three stages
 constexpr uint32_t NBUF = 3;
 template <int BM, int NG, bool ZEROS>
-constexpr uint32_t kStage = BM * 256 + 16 * (kI4Tile + 128 + (ZEROS ? 64 : 0)) + NG * BM * 4;
+constexpr uint32_t kStage = BM * 256 + 16 * (kI4Tile + 128 + (ZEROS ? 64 : 0)) + NG * BM * (ZEROS && NG <= 2 ? 8 : 4);
 // and which pairs the rows are
 template <int BM, int NG, bool ZEROS>
 constexpr uint32_t kLdsBytes = NBUF * kStage<BM, NG, ZEROS> + BM * 4;
@@ -92,6 +93,10 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
   constexpr int MT = BM / WM / 32, NS = WM, AU = BM / 32;  // 32 x 32 tiles of a wave; its transfers of activations
   constexpr int ND = AU + (ZEROS ? 6 : 4);                  // transfers of a wave and step
   constexpr uint32_t BNT = GATED ? 8 : 16;                  // 16-column tiles of the output
+  // Zero points by a matrix instruction (16 + z times the sums of the activations, before a group's products; 1000 x
+  // 5120, K = 17408 229 -> 217 us, 4096 x 5120, K = 5120 in groups of 64 273 -> 268) or, with groups of 32, for which the
+  // sums in three parts do not fit LDS, by a second multiply-add of the fold
+  constexpr bool kOuter = ZEROS && NG <= 2, kFolded = ZEROS && NG > 2;
   constexpr uint32_t kW = BM * 256, kS = kW + 16 * kI4Tile, kZ = kS + 16 * 128, kSum = kZ + (ZEROS ? 16 * 64 : 0);
   constexpr uint32_t kBuf = kStage<BM, NG, ZEROS>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -238,6 +243,26 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
       *reinterpret_cast<f32x4_t *>(lds + stage + kSum + (q * BM + sum_rows * 16u + g * 4u) * 4u) =
           ZEROS ? sum_t[q] : sum_t[q] * (-kI4Bias - 8.0f);
   };
+  // The same as three BF16 values, whose sum it is bit for bit; four lanes write a row each
+  auto sums_split = [&](uint32_t stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+      const float lo = r & 1u ? sum_t[q][1] : sum_t[q][0], hi = r & 1u ? sum_t[q][3] : sum_t[q][2], v = r & 2u ? hi : lo;
+      const uint32_t first = __float_as_uint(v) & 0xffff0000u;
+      const float rest = v - __uint_as_float(first);
+      const uint32_t second = __float_as_uint(rest) & 0xffff0000u;
+      const uint32_t third = __float_as_uint(rest - __uint_as_float(second)) >> 16;
+      if (r < 4u)
+        *reinterpret_cast<u32x2_t *>(lds + stage + kSum + (q * BM + sum_rows * 16u + g * 4u + r) * 8u) = u32x2_t{first >> 16 | second, third};
+    }
+  };
+  // Their products with -(16 + z) of tile (j, i): the lower lanes' k have z, the upper ones' 16
+  auto outer = [&](const u32x2_t &v, const Codes &x, int q, int i) __attribute__((always_inline)) {
+    const uint32_t z = kk ? __float_as_uint(-kI4Bias) >> 16 : __float_as_uint(-i4_zero_of(x.s[i], q)) >> 16;
+    const u32x4_t left = {v.x, v.y, 0u, 0u}, right = {z << 16 | z, z, 0u, 0u};
+    const f32x16_t none = {};
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, left), __builtin_bit_cast(bf16x8_t, right), none, 0, 0, 0);
+  };
   // rows 8 (e / 4) + 4 kk + e % 4 of tile j, as a lane's outputs have them
   auto sums_of = [&](uint32_t stage, int q, int j) __attribute__((always_inline)) {
     f32x16_t t;
@@ -265,7 +290,7 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
   auto fold = [&](int j, int i, const f32x16_t &z) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      acc[j][i][e] = __builtin_fmaf(scale[i], ZEROS ? __builtin_fmaf(zero[i], z[e], t[j][i][e]) : t[j][i][e], acc[j][i][e]);
+      acc[j][i][e] = __builtin_fmaf(scale[i], kFolded ? __builtin_fmaf(zero[i], z[e], t[j][i][e]) : t[j][i][e], acc[j][i][e]);
     asm volatile("" : "+v"(acc[j][i]));
   };
   Codes even;
@@ -278,14 +303,22 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
         f32x16_t from = {}, z = {};
-        if constexpr (kFirst && ZEROS) z = sums_of(c == 0 ? prev : cur, (q + NG - 1) % NG, j);
+        if constexpr (kFirst && kFolded) z = sums_of(c == 0 ? prev : cur, (q + NG - 1) % NG, j);
         if constexpr (kFirst && !ZEROS) from = sums_of(cur, q, j);
+        u32x2_t sum = {};
+        if constexpr (kFirst && kOuter)
+          sum = *reinterpret_cast<const u32x2_t *>(lds + cur + kSum + (q * BM + wm * (MT * 32u) + j * 32u + n5) * 8u);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           if constexpr (kFirst) fold(j, i, z);
-          if constexpr (kFirst && ZEROS) {
+          if constexpr (kFirst && kFolded) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) from[e] = 0.0f;
+          }
+          if constexpr (kFirst && kOuter) {
+            from = outer(sum, x, q, i);
+            asm volatile("" : "+v"(from));
+            if (i == NS - 1) __builtin_amdgcn_sched_barrier(0);  // later ones take registers that are still held
           }
           t[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[c & 1][j], b[c & 1][i], kFirst ? from : t[j][i], 0, 0, 0);
         }
@@ -302,7 +335,8 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
       convert(c < 7 ? x : y, (c + 1) % 8);
       if constexpr (c == 2) sums_read(nxt);
       if constexpr (c == 3) sums_form();
-      if constexpr (c == 5) sums_write(nxt);
+      if constexpr (c == 5 && kOuter) sums_split(nxt);
+      if constexpr (c == 5 && !kOuter) sums_write(nxt);
       // a matrix instruction and others in turn
       if constexpr (!kFirst) {
         mx_unroll<0, MT * NS>([&](auto) __attribute__((always_inline)) {
@@ -327,8 +361,9 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
   step_barrier<ND>();
   sums_read(0u);
   sums_form();
-  sums_write(0u);
-  if constexpr (ZEROS) {  // "the step before" has sums of zero
+  if constexpr (kOuter) sums_split(0u);
+  else sums_write(0u);
+  if constexpr (kFolded) {  // "the step before" has sums of zero
     for (uint32_t i = threadIdx.x; i < NG * BM; i += 64u * kWaves) *reinterpret_cast<float *>(lds + 2u * kBuf + kSum + i * 4u) = 0.0f;
   }
   even = read_codes(0u);
@@ -343,8 +378,9 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
   };
   // Two steps an iteration: then no sums are copied from the registers that one step leaves
   // them in to those that the next expects (1000 x 5120, K = 17408: 225 -> 202 us; 1000 x
-  // 5120, K = 5120 71.5 -> 64.5). With zero points it gains nothing, and with groups of 32 the registers no longer suffice.
-  if constexpr (NG <= 2 && !ZEROS) {
+  // 5120, K = 5120 71.5 -> 64.5).  In groups of 32, and with zero points in groups of 64, the registers no
+  // longer suffice.
+  if constexpr (NG == 1 || (NG == 2 && !ZEROS)) {
     Codes odd;
     uint32_t s = 0;
     for (; s + 1u < kt; s += 2u) {
@@ -369,7 +405,7 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     f32x16_t z = {};
-    if constexpr (ZEROS) z = sums_of(prev, NG - 1, j);
+    if constexpr (kFolded) z = sums_of(prev, NG - 1, j);
 #pragma unroll
     for (int i = 0; i < NS; ++i) fold(j, i, z);
   }
