@@ -53,6 +53,13 @@ __device__ __forceinline__ double wave_sum(double x) {
   return x;
 }
 
+// Expert v of a lane, or the last one for those past it
+template <int V>
+__device__ __forceinline__ uint32_t held(uint32_t lane, int v, uint32_t E) {
+  const uint32_t e = lane * V + v;
+  return e < E ? e : E - 1u;
+}
+
 template <int V>
 __global__ __launch_bounds__(256) void moe_route_kernel(MoeRoute op) {
   extern __shared__ __attribute__((aligned(16))) double shared[];  // of a choice by groups: each wave's values
@@ -61,21 +68,28 @@ __global__ __launch_bounds__(256) void moe_route_kernel(MoeRoute op) {
   if (t >= op.T) return;  // no barriers below
 
   // An expert whose logit is NaN or minus infinity, or whose bias is, is never chosen.
+  // All values are asked for before one is used, and without a branch between.
   double p[V], key[V];
   double top = kNone;
+  uint32_t bits[V];
+  float bias[V];
+  const uint64_t row = (uint64_t)t * op.ld;
+  if (op.type == WQD_TYPE_FP32) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) bits[v] = static_cast<const uint32_t *>(op.logits)[row + held<V>(lane, v, op.E)];
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) bits[v] = static_cast<const uint16_t *>(op.logits)[row + held<V>(lane, v, op.E)];
+  }
+  if (op.bias) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) bias[v] = op.bias[held<V>(lane, v, op.E)];
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const uint32_t e = lane * V + v;
-    float x = __builtin_nanf("");
-    if (e < op.E) {
-      const uint64_t at = (uint64_t)t * op.ld + e;
-      if (op.type == WQD_TYPE_FP32)
-        x = static_cast<const float *>(op.logits)[at];
-      else if (op.type == WQD_TYPE_BF16)
-        x = __uint_as_float((uint32_t) static_cast<const uint16_t *>(op.logits)[at] << 16);
-      else
-        x = (float)static_cast<const _Float16 *>(op.logits)[at];
-    }
+    const float half = (float)__builtin_bit_cast(_Float16, (uint16_t)bits[v]);
+    float x = op.type == WQD_TYPE_FP32 ? __uint_as_float(bits[v]) : op.type == WQD_TYPE_BF16 ? __uint_as_float(bits[v] << 16) : half;
+    if (lane * V + v >= op.E) x = __builtin_nanf("");
     x = x > 3.402823466e38f ? 3.402823466e38f : x;  // an infinity is the largest value
     key[v] = x > -__builtin_inff() ? (double)x : kNone;
     top = __builtin_fmax(top, key[v]);
@@ -100,7 +114,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(MoeRoute op) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const uint32_t e = lane * V + v;
-      const double b = e < op.E ? (double)op.bias[e] : kNone;
+      const double b = e < op.E ? (double)bias[v] : kNone;
       key[v] = key[v] > kNone && b > kNone ? p[v] + b : kNone;
     }
   }
