@@ -247,31 +247,47 @@ __global__ __launch_bounds__(64 * kListWaves) void moe_lists_kernel(const int32_
 }
 
 // A thread adds four columns of a token's rows in slot order; slots without an
-// expert of these are passed over.
+// expert of these are passed over.  Rows of kSlots slots are in flight at once (33 tokens of
+// 8 slots, 2048 columns: with the products 27.0 -> 25.2 us; 2048 tokens: the same, 28
+// us for 142 MB).
+constexpr uint32_t kSlots = 8;
+
 __global__ __launch_bounds__(256) void moe_combine_kernel(I4Operands op, uint64_t from) {
   const uint32_t pieces = (op.N + 3u) / 4u;
   const uint64_t x = from + (uint64_t)blockIdx.x * 256u + threadIdx.x;
   const uint32_t t = (uint32_t)(x / pieces), n = (uint32_t)(x - (uint64_t)t * pieces) * 4u;
   if (x >= (uint64_t)op.T * pieces) return;
-  float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (uint32_t s = 0; s < op.top_k; ++s) {
-    const uint32_t p = t * op.top_k + s;
-    if ((uint32_t)op.ids[p] >= op.E) continue;
-    const float w = op.weights[p];
-    const float *y = op.Y + (uint64_t)p * op.N + n;
-    if (op.N % 4u == 0u) {
-      const f32x4_t v = *reinterpret_cast<const f32x4_t *>(y);
+  const bool whole = op.N % 4u == 0u;
+  f32x4_t c = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (uint32_t s0 = 0; s0 < op.top_k; s0 += kSlots) {
+    bool here[kSlots];
+    float w[kSlots];
+    f32x4_t y[kSlots];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(w, v[i], c[i]);
-    } else {
-#pragma unroll
-      for (uint32_t i = 0; i < 4; ++i)
-        if (n + i < op.N) c[i] = __builtin_fmaf(w, y[i], c[i]);
+    for (uint32_t i = 0; i < kSlots; ++i) {
+      const uint32_t s = s0 + i < op.top_k ? s0 + i : op.top_k - 1u, p = t * op.top_k + s;
+      here[i] = s0 + i < op.top_k && (uint32_t)op.ids[p] < op.E;
+      w[i] = op.weights[p];
     }
+#pragma unroll
+    for (uint32_t i = 0; i < kSlots; ++i) {
+      y[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      const float *row = op.Y + (uint64_t)(t * op.top_k + s0 + i) * op.N + n;
+      if (here[i] && whole) y[i] = *reinterpret_cast<const f32x4_t *>(row);
+      if (here[i] && !whole) {
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j)
+          if (n + j < op.N) y[i][j] = row[j];
+      }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kSlots; ++i)
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) c[j] = here[i] ? __builtin_fmaf(w[i], y[i][j], c[j]) : c[j];
   }
 #pragma unroll
-  for (uint32_t i = 0; i < 4; ++i)
-    if (n + i < op.N) op.C[(uint64_t)t * op.ldc + n + i] = (uint16_t)bf16x2_rne(c[i], 0.0f);
+  for (uint32_t j = 0; j < 4; ++j)
+    if (n + j < op.N) op.C[(uint64_t)t * op.ldc + n + j] = (uint16_t)bf16x2_rne(c[j], 0.0f);
 }
 
 }  // namespace
