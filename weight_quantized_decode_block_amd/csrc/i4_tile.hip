@@ -376,11 +376,29 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
     cur = nxt;
     nxt = free;
   };
-  // Two steps an iteration: then no sums are copied from the registers that one step leaves
-  // them in to those that the next expects (1000 x 5120, K = 17408: 225 -> 202 us; 1000 x
-  // 5120, K = 5120 71.5 -> 64.5).  In groups of 32, and with zero points in groups of 64, the registers no
-  // longer suffice.
-  if constexpr (NG == 1 || (NG == 2 && !ZEROS)) {
+  if ((WM == 2 && (ROWS == kLists || ZEROS)) && wm * (MT * 32u) >= rows) {
+    // Rows that are none of this wave's: it brings its share and forms its sums only, and leaves the SIMD to the
+    // other one there (512 tokens of 8 of 64 experts, 2048 outputs, K = 1024 56.1 -> 53 us, 300 x 17408, K = 5120 with
+    // zero points 77 -> 71.5).  Without lists and zero points the second loop costs more than it gives where tiles
+    // are full (1000 x 5120, K = 5120 64.2 -> 67.7; 300 x 17408, K = 5120 74.8 -> 68.9).
+    for (uint32_t s = 0; s < kt; ++s) {
+      step_barrier<0>();
+      sums_read(nxt);
+      sums_form();
+      if constexpr (kOuter) sums_split(nxt);
+      else sums_write(nxt);
+#pragma unroll
+      for (int i = 0; i < ND; ++i) issue(i, s + 2u, prev);
+      const uint32_t free = prev;
+      prev = cur;
+      cur = nxt;
+      nxt = free;
+    }
+  } else if constexpr (NG == 1 || (NG == 2 && !ZEROS)) {
+    // Two steps an iteration: then no sums are copied from the registers that one step leaves
+    // them in to those that the next expects (1000 x 5120, K = 17408: 225 -> 202 us; 1000 x
+    // 5120, K = 5120 71.5 -> 64.5).  In groups of 32, and with zero points in groups of 64, the registers no
+    // longer suffice.
     Codes odd;
     uint32_t s = 0;
     for (; s + 1u < kt; s += 2u) {
