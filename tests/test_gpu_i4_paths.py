@@ -13,7 +13,12 @@ from weight_quantized_decode_block_amd import wqd
 pytestmark = [pytest.mark.gpu, requires_gpu]
 
 CONFIGS = [(group, zeros, "bf16" if (group == 64) == zeros else "fp16") for group in (32, 64, 128) for zeros in (False, True)]
-# (M, N, K): chunks of 32 rows, tiles of 64 and of 128 rows; one to five steps
+# (M, N, K): tiles of 128 rows for whole rounds and the last outputs in chunks of 16, of 32 rows and tiles of 64
+PRODUCT_SPLIT = [(8248, 1808, 640), (4368, 1991, 640), (5435, 1747, 640)]
+GATED_SPLIT = [(3883, 2052, 384), (6211, 771, 384), (6793, 710, 384)]
+# tiles of 64 rows for whole rounds, and a prompt's
+GATED_LARGE = [(165, 16774, 5120), (500, 17408, 5120)]
+# chunks of 32 rows, tiles of 64 and of 128 rows; one to five steps
 PRODUCT = [(97, 5120, 128), (300, 1000, 256), (1000, 500, 384), (7043, 385, 128), (5864, 385, 256), (5864, 385, 640), (7698, 898, 128),
            (5471, 898, 256), (4947, 898, 384), (4685, 841, 640)]
 GATED = [(97, 5120, 128), (300, 1000, 256), (1000, 500, 384), (4554, 328, 128), (4554, 271, 256), (4554, 271, 640), (5733, 613, 128),
@@ -24,7 +29,7 @@ LISTS = [(2000, 4, 2, 257, 128), (900, 4, 2, 700, 384), (3000, 3, 2, 300, 256), 
 
 
 @pytest.mark.parametrize("group,zeros,scale", CONFIGS)
-@pytest.mark.parametrize("M,N,K", PRODUCT)
+@pytest.mark.parametrize("M,N,K", PRODUCT + PRODUCT_SPLIT)
 def test_product_exact(M, N, K, group, zeros, scale):
     """Integers times powers of two: every sum is exact in fp32, so the outputs are the rounded exact sums."""
     g = ref.generator(41, M, N, K, group)
@@ -37,7 +42,7 @@ def test_product_exact(M, N, K, group, zeros, scale):
 
 
 @pytest.mark.parametrize("group,zeros,scale", CONFIGS)
-@pytest.mark.parametrize("M,N,K", GATED)
+@pytest.mark.parametrize("M,N,K", GATED + GATED_SPLIT)
 def test_gated(M, N, K, group, zeros, scale):
     g = ref.generator(42, M, N, K, group)
     wg, wu = ref.Weights(g, 1, N, K, group, zeros, scale), ref.Weights(g, 1, N, K, group, zeros, scale)
@@ -47,6 +52,30 @@ def test_gated(M, N, K, group, zeros, scale):
     sums = [(a.double() @ w.values()[0].T, ref.sum_error(a.double().abs() @ w.size()[0].T, K)) for w in (wg, wu)]
     want, err = ref.gated(sums[0][0], sums[1][0], sums[0][1], sums[1][1])
     assert bool(((C[:M].cpu().double() - want).abs() <= ref.stored(want, err)).all()) and untouched(C, M, N)
+
+
+@pytest.mark.parametrize("group", [64, 128])
+@pytest.mark.parametrize("M,N,K", GATED_LARGE)
+def test_gated_by_parts(M, N, K, group):
+    """Bit for bit as its parts of 1040 outputs, which take other kernels: all sums are exact."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(51)
+    R = wqd.i4_packed_rows(N)
+
+    def weights():
+        codes = torch.randint(0, 256, (R, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+        s = torch.exp2(-torch.randint(6, 9, (R, K // group), generator=g, device="cuda").float()).half()
+        return codes, s, torch.randint(0, 16, (R, K // group), generator=g, device="cuda", dtype=torch.uint8)
+
+    G, U = weights(), weights()
+    A = torch.randint(-2, 3, (M, K), generator=g, device="cuda").to(BF)
+    C, D = out(M, N, N), out(M, N, N)
+    wqd.i4a16_gated(A, *G, *U, C, M, N, K, group)
+    for n in range(0, N, 1040):
+        m = min(1040, N - n)
+        part = lambda x: x[n:n + wqd.i4_packed_rows(m)]  # noqa: E731
+        wqd.i4a16_gated(A, *map(part, G), *map(part, U), D[:, n:], M, m, K, group, c_row_stride=N)
+    assert torch.equal(C, D) and untouched(C, M, N) and bool((C[:M] != 0).any())
 
 
 @pytest.mark.parametrize("group,zeros,scale", CONFIGS)

@@ -544,20 +544,37 @@ uint64_t cost_of(const Cost &c, uint64_t tiles, uint32_t steps) {
   return c.first + c.first_step * steps + (rounds > 1u ? (rounds - 1u) * (c.more + (uint64_t)c.more_step * steps) : 0u);
 }
 
-// Index of the least cost; chunks(bm): tiles of bm rows.
+// The least cost and its index; chunks(bm): tiles of bm rows.
+struct Choice {
+  uint32_t way;
+  uint64_t cost;
+};
 template <uint32_t COUNT, typename F>
-uint32_t least(const Cost (&costs)[COUNT], const I4Operands &op, F &&chunks) {
+Choice least(const Cost (&costs)[COUNT], const I4Operands &op, F &&chunks) {
   const uint32_t n = op.gated ? 2u * op.N : op.N;
-  uint64_t best = ~0ull;
-  uint32_t at = 0;
+  Choice best = {0u, ~0ull};
   for (uint32_t i = 0; i < COUNT; ++i) {
     const uint64_t x = cost_of(costs[i], chunks(costs[i].bm) * ((n + costs[i].bn - 1u) / costs[i].bn), op.K >> 7);
-    if (x < best) {
-      best = x;
-      at = i;
-    }
+    if (x < best.cost) best = {i, x};
   }
-  return at;
+  return best;
+}
+
+Choice least_product(const I4Operands &op) {
+  if (op.M <= 16u) return {0u, 0u};
+  return least(kCosts, op, [&](uint32_t bm) { return (uint64_t)((op.M + bm - 1u) / bm); });
+}
+
+hipError_t launch_way(const I4Operands &op, uint32_t way, hipStream_t stream) {
+  if (way < 2u) return launch_i4_skinny(op, way == 1u, stream);
+  if (way == 2u) return op.gated ? launch_dense<64, 1, true>(op, stream) : launch_dense<64, 1, false>(op, stream);
+  return op.gated ? launch_dense<128, 2, true>(op, stream) : launch_dense<128, 2, false>(op, stream);
+}
+
+// Outputs from n on (a whole number of weight tiles)
+I4Matrix from_row(const I4Matrix &m, const I4Operands &op, uint32_t n) {
+  const uint64_t values = (uint64_t)n * op.K;
+  return {m.W ? m.W + values / 2u : nullptr, m.S ? m.S + values / op.group : nullptr, m.Z ? m.Z + values / op.group : nullptr};
 }
 
 }  // namespace
@@ -566,11 +583,31 @@ uint32_t least(const Cost (&costs)[COUNT], const I4Operands &op, F &&chunks) {
 // with twice the weight rows, where its activations pass through fewer workgroups (96 x 5120, K = 5120 17.3 -> 12.3 us).
 // Tiles cost less per output and wait for each of their steps: 256 x 5120, K = 5120 30.5 us in chunks, 51 in tiles of 64
 // rows and 70 of 128; 1024 rows 143 in chunks of 16, 103 and 65 in tiles.
+//
+// A last round of tiles that leaves most compute units idle costs as much as a full one.  Where it is less, only as many
+// outputs as fill whole rounds are left to the tiles, and the others get the way that is best for them, in a
+// launch of their own (gated 500 x 17408, K = 5120 248 -> 205 us, 256 rows 153 -> 101; 2000 x 5120, K = 5120 138 -> 124).
 hipError_t launch_i4_product(const I4Operands &op, hipStream_t stream) {
-  const uint32_t way = op.M <= 16u ? 0u : least(kCosts, op, [&](uint32_t bm) { return (uint64_t)((op.M + bm - 1u) / bm); });
-  if (way < 2u) return launch_i4_skinny(op, way == 1u, stream);
-  if (way == 2u) return op.gated ? launch_dense<64, 1, true>(op, stream) : launch_dense<64, 1, false>(op, stream);
-  return op.gated ? launch_dense<128, 2, true>(op, stream) : launch_dense<128, 2, false>(op, stream);
+  const Choice whole = least_product(op);
+  if (whole.way >= 2u) {
+    const Cost &c = kCosts[whole.way];
+    const uint32_t each = op.gated ? c.bn / 2u : c.bn, tn = (op.N + each - 1u) / each;
+    const uint64_t tm = (op.M + c.bm - 1u) / c.bm, cols = tm * tn / 256u * 256u / tm;
+    if (cols > 0u && cols < tn) {
+      I4Operands first = op, rest = op;
+      first.N = (uint32_t)cols * each;
+      rest.N = op.N - first.N;
+      rest.w = from_row(op.w, op, first.N);
+      rest.up = from_row(op.up, op, first.N);
+      rest.C = op.C + first.N;
+      const Choice then = least_product(rest);
+      if (cost_of(c, tm * cols, op.K >> 7) + then.cost < whole.cost) {
+        const hipError_t e = launch_way(first, whole.way, stream);
+        return e == hipSuccess ? launch_way(rest, then.way, stream) : e;
+      }
+    }
+  }
+  return launch_way(op, whole.way, stream);
 }
 
 // Whether one launch of tiles of bm rows holds the lists' products.  Rows of more than 4 GB are beyond its offsets.
@@ -588,9 +625,9 @@ hipError_t launch_i4_experts(const I4Operands &op, hipStream_t stream) {
   uint32_t way = 0;
   if (op.order && i4_tiles_fit(op, 128u)) {
     way = least(kListCosts, op, [&](uint32_t bm) {
-      const uint64_t chunks = pairs / bm + busy / 4u;
-      return chunks > busy ? chunks : (uint64_t)busy;
-    });
+            const uint64_t chunks = pairs / bm + busy / 4u;
+            return chunks > busy ? chunks : (uint64_t)busy;
+          }).way;
     if ((way == 0u && !i4_experts_skinny_fit(op)) || (way == 1u && !i4_tiles_fit(op, 64u))) way = 2u;
   }
   if (way == 0u) return launch_i4_experts_skinny(op, stream);
