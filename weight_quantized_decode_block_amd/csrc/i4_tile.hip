@@ -20,9 +20,11 @@
 //   * All instructions of both waves of a SIMD share its issue: beside a 32 x 32 x 16
 //     matrix instruction (32 cycles) there is room for six others of its wave, beside a 16
 //     x 16 x 32 one for two.  Hence 32 x 32, and no more than two instructions for a pair of
-//     codes.  Of a step of 128 rows (1.45 us) the matrix instructions take 0.75; without the
-//     folds it would be 0.25 us shorter, without the sums 0.3, the transfers 0.24, the
-//     conversions 0.13.  4096 x 5120, K = 5120 213 us, 1.0 PFLOP/s.
+//     codes.  Of a step of 128 rows (1.45 us on 160 compute units) the matrix instructions
+//     take 0.9 at the highest clock; when it took 1.63 it was 0.25 us shorter without the
+//     folds, 0.3 without the sums, 0.24 without the transfers and 0.13 without the conversions.
+//     Where all compute units work the clock falls to about 2 GHz: 4096 x 5120, K = 5120 211
+//     us, 1.02 PFLOP/s, 16384 x 2048, K = 4096 1.14.
 //   * The sums of a group are a matrix accumulator of their own, which the scale
 //     adds to the output's in fp32: nothing but the output is rounded.
 #include <hip/hip_runtime.h>
