@@ -187,31 +187,49 @@ hipError_t launch_route(const MoeRoute &op, hipStream_t stream) {
   return hipGetLastError();
 }
 
-constexpr uint32_t kListWaves = 16, kBatch = 8;  // kBatch loads of a wave in flight
+// kBatch loads of 256 pairs of a wave in flight: up to 32768 pairs are read once only (4096 tokens of 8 of 64 experts in
+// loads of 64 pairs, read twice, 7.4 us, so 6.0; 1 token 2.7 and 2.9)
+constexpr uint32_t kListWaves = 16, kBatch = 8;
+
+typedef uint32_t ids_t __attribute__((ext_vector_type(4), aligned(4)));
 
 // Workgroup e < E writes expert e's list; workgroup E the lists' end and what is behind it.
 __global__ __launch_bounds__(64 * kListWaves) void moe_lists_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ order,
                                                                     int32_t *__restrict__ offsets, uint32_t pairs, uint32_t E) {
   __shared__ uint32_t counts[2][kListWaves];
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), e = blockIdx.x;
-  // each wave its own stretch of pairs, in whole rounds of 64
-  const uint32_t each = ((pairs + 63u) / 64u + kListWaves - 1u) / kListWaves * 64u;
+  // each wave its own stretch of pairs, in whole rounds of 256: four neighbours a lane
+  const uint32_t each = ((pairs + 255u) / 256u + kListWaves - 1u) / kListWaves * 256u;
   const uint32_t from = wave * each < pairs ? wave * each : pairs, to = pairs - from < each ? pairs : from + each;
-  uint32_t below = 0, own = 0;
-  for (uint32_t i0 = from + lane; i0 < to; i0 += 64u * kBatch) {
-    uint32_t id[kBatch];
-#pragma unroll
-    for (uint32_t b = 0; b < kBatch; ++b) id[b] = i0 + b * 64u < to ? (uint32_t)ids[i0 + b * 64u] : ~0u;
+  uint32_t id[kBatch][4];
+  auto load = [&](uint32_t i0) __attribute__((always_inline)) {
 #pragma unroll
     for (uint32_t b = 0; b < kBatch; ++b) {
-      below += id[b] < e ? 1u : 0u;
-      own += id[b] == e ? 1u : 0u;
-    }
-  }
+      const uint32_t p = i0 + b * 256u + lane * 4u;
+      ids_t v = {~0u, ~0u, ~0u, ~0u};
+      if (p + 3u < to) {
+        v = *reinterpret_cast<const ids_t *>(ids + p);
+      } else {
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    below += (uint32_t)__shfl_xor((int)below, d);
-    own += (uint32_t)__shfl_xor((int)own, d);
+        for (uint32_t j = 0; j < 3; ++j)
+          if (p + j < to) v[j] = (uint32_t)ids[p + j];
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) id[b][j] = v[j];
+    }
+  };
+  uint32_t below = 0, own = 0;
+  for (uint32_t i0 = from; i0 < to; i0 += 256u * kBatch) {
+    load(i0);
+#pragma unroll
+    for (uint32_t b = 0; b < kBatch; ++b) {
+      if (i0 + b * 256u >= to) break;
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) {
+        below += (uint32_t)__builtin_popcountll(__ballot(id[b][j] < e));
+        own += (uint32_t)__builtin_popcountll(__ballot(id[b][j] == e));
+      }
+    }
   }
   if (lane == 0u) {
     counts[0][wave] = below;
@@ -229,19 +247,23 @@ __global__ __launch_bounds__(64 * kListWaves) void moe_lists_kernel(const int32_
     return;
   }
   place += start;
-  for (uint32_t i0 = from; i0 < to; i0 += 64u * kBatch) {
-    uint32_t id[kBatch];
+  for (uint32_t i0 = from; i0 < to; i0 += 256u * kBatch) {
+    if (each > 256u * kBatch) load(i0);
 #pragma unroll
     for (uint32_t b = 0; b < kBatch; ++b) {
-      const uint32_t p = i0 + b * 64u + lane;
-      id[b] = p < to ? (uint32_t)ids[p] : ~0u;
-    }
+      if (i0 + b * 256u >= to) break;
+      uint32_t before = 0, count = 0;
 #pragma unroll
-    for (uint32_t b = 0; b < kBatch; ++b) {
-      const uint64_t set = __ballot(id[b] == e);
-      const uint32_t before = __builtin_amdgcn_mbcnt_hi((uint32_t)(set >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)set, 0u));
-      if (id[b] == e) order[place + before] = (int32_t)(i0 + b * 64u + lane);
-      place += (uint32_t)__builtin_popcountll(set);
+      for (uint32_t j = 0; j < 4; ++j) {
+        const uint64_t set = __ballot(id[b][j] == e);
+        before = __builtin_amdgcn_mbcnt_hi((uint32_t)(set >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)set, before));
+        count += (uint32_t)__builtin_popcountll(set);
+      }
+      int32_t *to_list = order + place + before;
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j)
+        if (id[b][j] == e) *to_list++ = (int32_t)(i0 + b * 256u + lane * 4u + j);
+      place += count;
     }
   }
 }
