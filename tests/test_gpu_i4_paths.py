@@ -78,6 +78,24 @@ def test_gated_by_parts(M, N, K, group):
     assert torch.equal(C, D) and untouched(C, M, N) and bool((C[:M] != 0).any())
 
 
+@pytest.mark.parametrize("M", [3, 40, 150])
+def test_the_most_outputs(M):
+    """2^24 outputs, the most there may be: bit for bit as parts of them."""
+    N, K, group = 1 << 24, 128, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(52)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.exp2(-torch.randint(6, 9, (N, K // group), generator=g, device="cuda").float()).bfloat16()
+    A = torch.randint(-2, 3, (M, K), generator=g, device="cuda").to(BF)
+    C = torch.full((M, N), CANARY, dtype=BF, device="cuda")
+    wqd.i4a16_gemm(A, codes, s, None, C, M, N, K, group)
+    D = out(M, 512, 512)
+    for n in (0, 1 << 20, (1 << 23) + 16, (1 << 24) - 4096 - 256, (1 << 24) - 512):
+        wqd.i4a16_gemm(A, codes[n:n + 512], s[n:n + 512], None, D, M, 512, K, group)
+        assert torch.equal(C[:, n:n + 512], D[:M])
+    assert not bool((C == CANARY).any())
+
+
 @pytest.mark.parametrize("group,zeros,scale", CONFIGS)
 @pytest.mark.parametrize("T,E,top_k,N,K", LISTS)
 def test_experts(T, E, top_k, N, K, group, zeros, scale):
