@@ -3,8 +3,9 @@
 // them.
 //
 // A workgroup of 8 waves owns BM rows and 256 weight rows (in the gated form
-// 128 of both matrices) and walks K in steps of 128.  The waves stand side by side
-// in n, so each converts its own weights only, once; all of them read all activations.
+// 128 of both matrices) and walks K in steps of 128.  With 64 rows the waves stand side
+// by side in n: each converts its own weights only, and all read all activations.  With
+// 128 they are four in n and two in m, which share a SIMD and convert the same weights.
 //
 //   * Staging.  Activations, codes, scales and zero points go straight from memory to
 //     LDS, two steps ahead of their use, into the third of three stages; a wave asks for
