@@ -346,18 +346,23 @@ int w4a4_gated(const void *A, const void *AS, const void *WG, const void *WGS, c
 
 /* ----------------------------------- 4-bit integer weights, routed experts */
 
+#define WQD_I4_BY_ROW  0x100  /* added to a scale type: scales and zero points row by row */
+
 /*
  * A matrix of 4-bit integer weights:
  *   w[n,k] = (q[n,k] - z[n,k/group]) * s[n,k/group],
  *   q  codes 0 .. 15;  s  FP16 or BF16 [N][K/group];  z  uint8 [N][K/group], or
  *   NULL: 8 everywhere;  group  32, 64 or 128.
- * The three are laid out once, by i4_pack, in tiles of 16 rows (padded with zeros
+ * The codes are laid out once, by i4_pack, in tiles of 16 rows (padded with zeros
  * to whole tiles) x 128 k, row tile by row tile:
  *   codes   uint8 [ceil(N/16)][K/128][1024]; byte 256 g + 16 n + 4 j + b of a tile (g, j,
  *           b 0 .. 3, n 0 .. 15) holds the codes of row n at k = 32 j + 8 g + i, for b = 0
  *           .. 3 of i = 0 and 2, 4 and 6, 1 and 3, 5 and 7, the first in the low nibble
- *   scales  [ceil(N/16)][K/128][16][128/group], zero points likewise (uint8)
- * Several matrices of one size (experts) lie one after another.
+ * The scales and zero points of a call are, all of them, either
+ *   in tiles    [ceil(N/16)][K/128][16][128/group], as i4_pack lays them out, or
+ *   row by row  [N][K/group], as above: WQD_I4_BY_ROW is added to the call's scale_type then.
+ * The library cannot tell the two apart: they are as many bytes where N is a multiple of
+ * 16.  Several matrices of one size (experts) lie one after another.
  *
  * i4_pack - `count` matrices, codes uint8 [count][N][K/2] with the even k in the low
  * nibble, scales and zero points [count][N][K/group], to that layout; the scales'
@@ -383,14 +388,17 @@ uint32_t i4_packed_rows(uint32_t N);
  * infinity or NaN has no finite output; which of the two it has is not defined.
  *
  *   A   device, BF16, row m at A + m * a_row_stride, 16-byte aligned
- *   W, WS, WZ  device, laid-out codes, scales and zero points (or NULL), 16-byte
- *       aligned; of a gated product both matrices have zero points or neither
+ *   W   device, laid-out codes, 16-byte aligned
+ *   WS, WZ  device, scales and zero points (or NULL); in tiles 16-byte aligned, row by
+ *       row to 256/group (scales) and 128/group bytes; of a gated product both matrices
+ *       have zero points or neither
  *   C   device, BF16, row m at C + m * c_row_stride, 2-byte aligned; only
  *       columns < N of rows < M are written
  *   M   rows, from one to a long prompt (0: nothing is launched), at most
  *       WQD_MX_MAX_ROWS;  N  1 .. WQD_MX_MAX_ROWS
  *   K   a positive multiple of 128, at most WQD_MX_MAX_K
- *   scale_type    WQD_TYPE_FP16 or WQD_TYPE_BF16
+ *   scale_type    WQD_TYPE_FP16 or WQD_TYPE_BF16, with scales and zero points row by
+ *       row plus WQD_I4_BY_ROW
  *   a_row_stride  >= K, a multiple of 8, at most WQD_MX_MAX_STRIDE;  c_row_stride >= N
  */
 int i4a16_gemm(const void *A, const void *W, const void *WS, const void *WZ, void *C,

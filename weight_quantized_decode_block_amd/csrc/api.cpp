@@ -192,7 +192,8 @@ wqd::MxOperands mx_operands(const void *A, const void *AS, const void *W, const 
 
 // Checks shared by the products with 4-bit integer weights: matrices (`both`:
 // two of them), their scales and zero points, and what the kernels' sizes assume.
-int validate_i4(const char *fn, const wqd::I4Operands &op, bool both, uint32_t scale_type) {
+int validate_i4(const char *fn, const wqd::I4Operands &op, bool both, uint32_t scales) {
+  const uint32_t scale_type = scales & ~(uint32_t)WQD_I4_BY_ROW;
   if (!op.w.W || !op.w.S || (both && (!op.up.W || !op.up.S)))
     return fail(WQD_ENULL, "%s: weights and scales must be non-NULL", fn);
   if (both && !op.w.Z != !op.up.Z)
@@ -213,16 +214,18 @@ int validate_i4(const char *fn, const wqd::I4Operands &op, bool both, uint32_t s
     return fail(WQD_EUNSUPPORTED, "%s: a_row_stride=%u above %u", fn, op.lda, (unsigned)WQD_MX_MAX_STRIDE);
   if (!aligned(op.A, 16)) return fail(WQD_EALIGN, "%s: activations must be 16-byte aligned", fn);
   if (!aligned(op.w.W, 16) || !aligned(op.up.W, 16)) return fail(WQD_EALIGN, "%s: weights must be 16-byte aligned", fn);
-  if (!aligned(op.w.S, 16) || !aligned(op.up.S, 16)) return fail(WQD_EALIGN, "%s: scales must be 16-byte aligned", fn);
-  if (!aligned(op.w.Z, 16) || !aligned(op.up.Z, 16))
-    return fail(WQD_EALIGN, "%s: zero points must be 16-byte aligned", fn);
+  // row by row what a row has for 128 k is one load
+  const uint32_t sa = op.by_row ? 256u / op.group : 16u, za = op.by_row ? 128u / op.group : 16u;
+  if (!aligned(op.w.S, sa) || !aligned(op.up.S, sa)) return fail(WQD_EALIGN, "%s: scales must be %u-byte aligned", fn, sa);
+  if (!aligned(op.w.Z, za) || !aligned(op.up.Z, za))
+    return fail(WQD_EALIGN, "%s: zero points must be %u-byte aligned", fn, za);
   if (!aligned(op.C, 2)) return fail(WQD_EALIGN, "%s: C must be 2-byte aligned", fn);
   return WQD_OK;
 }
 
-int run_i4_product(const char *fn, wqd::I4Operands op, uint32_t scale_type, hipStream_t stream) {
+int run_i4_product(const char *fn, const wqd::I4Operands &op, uint32_t scales, hipStream_t stream) {
   if (op.M && (!op.A || !op.C)) return fail(WQD_ENULL, "%s: A and C must be non-NULL", fn);
-  if (int rc = validate_i4(fn, op, op.gated, scale_type)) return rc;
+  if (int rc = validate_i4(fn, op, op.gated, scales)) return rc;
   if (op.M > WQD_MX_MAX_ROWS) return fail(WQD_EUNSUPPORTED, "%s: M=%u above %u", fn, op.M, (unsigned)WQD_MX_MAX_ROWS);
   if (op.M == 0) return WQD_OK;  // no rows: nothing to launch
   if (int rc = check_device(fn)) return rc;
@@ -241,13 +244,13 @@ int validate_routes(const char *fn, uint32_t T, uint32_t top_k, uint32_t E) {
   return WQD_OK;
 }
 
-int run_i4_experts(const char *fn, wqd::I4Operands op, uint32_t scale_type, hipStream_t stream) {
+int run_i4_experts(const char *fn, const wqd::I4Operands &op, uint32_t scales, hipStream_t stream) {
   if (op.T && (!op.A || !op.C || !op.ids || (!op.gated && !op.weights)))
     return fail(WQD_ENULL, "%s: activations, ids, weights and outputs must be non-NULL", fn);
   if (op.T && !op.order != !op.offsets) return fail(WQD_ENULL, "%s: order and offsets must both be given or both be NULL", fn);
   if (op.T && !op.gated && op.order && !op.Y) return fail(WQD_ENULL, "%s: Y must be non-NULL where lists are given", fn);
   if (int rc = validate_routes(fn, op.T, op.top_k, op.E)) return rc;
-  if (int rc = validate_i4(fn, op, op.gated, scale_type)) return rc;
+  if (int rc = validate_i4(fn, op, op.gated, scales)) return rc;
   if (!aligned(op.ids, 4) || !aligned(op.order, 4) || !aligned(op.offsets, 4) || !aligned(op.weights, 4))
     return fail(WQD_EALIGN, "%s: ids, weights and lists must be 4-byte aligned", fn);
   if (!aligned(op.Y, 16)) return fail(WQD_EALIGN, "%s: Y must be 16-byte aligned", fn);
@@ -258,6 +261,12 @@ int run_i4_experts(const char *fn, wqd::I4Operands op, uint32_t scale_type, hipS
   (void)hipGetLastError();
   if (int rc = check_launch(fn, wqd::launch_i4_experts(op, stream))) return rc;
   return !op.gated && op.order ? check_launch(fn, wqd::launch_moe_combine(op, stream)) : WQD_OK;
+}
+
+// How the scales of a call come (WQD_TYPE_* and WQD_I4_BY_ROW).
+void set_scales(wqd::I4Operands &op, uint32_t scales) {
+  op.scale_bf16 = (scales & ~(uint32_t)WQD_I4_BY_ROW) == WQD_TYPE_BF16;
+  op.by_row = scales & WQD_I4_BY_ROW;
 }
 
 wqd::I4Matrix i4_matrix(const void *W, const void *S, const void *Z) {
@@ -508,7 +517,7 @@ int i4a16_gemm(const void *A, const void *W, const void *WS, const void *WZ, voi
   op.w = i4_matrix(W, WS, WZ);
   op.C = static_cast<uint16_t *>(C);
   op.M = M, op.N = N, op.K = K, op.lda = a_row_stride, op.ldc = c_row_stride, op.group = group;
-  op.scale_bf16 = scale_type == WQD_TYPE_BF16;
+  set_scales(op, scale_type);
   return run_i4_product("i4a16_gemm", op, scale_type, stream);
 }
 
@@ -521,7 +530,7 @@ int i4a16_gated(const void *A, const void *WG, const void *WGS, const void *WGZ,
   op.up = i4_matrix(WU, WUS, WUZ);
   op.C = static_cast<uint16_t *>(C);
   op.M = M, op.N = N, op.K = K, op.lda = a_row_stride, op.ldc = c_row_stride, op.group = group;
-  op.scale_bf16 = scale_type == WQD_TYPE_BF16;
+  set_scales(op, scale_type);
   op.gated = true;
   return run_i4_product("i4a16_gated", op, scale_type, stream);
 }
@@ -577,7 +586,7 @@ int i4a16_experts_gated(const void *A, const int32_t *ids, const int32_t *order,
   op.C = static_cast<uint16_t *>(H);
   op.ids = ids, op.order = order, op.offsets = offsets;
   op.N = N, op.K = K, op.lda = a_row_stride, op.ldc = N, op.group = group;
-  op.scale_bf16 = scale_type == WQD_TYPE_BF16;
+  set_scales(op, scale_type);
   op.T = T, op.top_k = top_k, op.E = E;
   op.gated = true;
   return run_i4_experts("i4a16_experts_gated", op, scale_type, stream);
@@ -594,7 +603,7 @@ int i4a16_experts_down(const void *H, const int32_t *ids, const float *weights, 
   op.Y = Y;
   op.ids = ids, op.order = order, op.offsets = offsets, op.weights = weights;
   op.N = N, op.K = K, op.lda = K, op.ldc = c_row_stride, op.group = group;
-  op.scale_bf16 = scale_type == WQD_TYPE_BF16;
+  set_scales(op, scale_type);
   op.T = T, op.top_k = top_k, op.E = E;
   return run_i4_experts("i4a16_experts_down", op, scale_type, stream);
 }

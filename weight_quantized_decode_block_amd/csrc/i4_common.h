@@ -6,9 +6,11 @@
 // order: lane (n, g) = (lane % 16, lane / 16) has the 16 bytes at 16 * lane, and
 // dword j of them is k = 32 j + 8 g .. + 7 of row n.  Nibbles p and p + 4 of a
 // dword are elements 2p and 2p + 1, so that one shift and one mask give a pair.
-// A tile's scales and zero points are [16 rows][128/group]: one piece of memory
-// too.  Row by row, as they come, a load touches a line for each of 16 rows, and these
-// cost more than the codes: 1 x 5120, K = 5120 8.0 us, laid out so 6.4 (with the kernels of then).
+// Scales and zero points lie either
+//   in tiles: a tile's are [16 rows][128/group], one piece of memory too, or
+//   row by row ([N][K/group], as a checkpoint has them): a load then touches a line for each
+//     of 16 rows.
+// A call says which (I4Operands::by_row).
 #pragma once
 
 #include "mx_common.h"
@@ -37,16 +39,17 @@ __device__ __forceinline__ float i4_scale(uint32_t bits, bool bf) {
   return bf ? b : h;
 }
 
-// The scales (zero points) of a row of a tile: NG of them, one load.
+// The scales (zero points) of a row of a tile: NG of them, one load.  Rows are SROW scales and ZROW zero points
+// apart.
 template <int NG>
 struct I4Groups {
   uint32_t s[NG == 4 ? 2 : 1], z;
 };
-template <int NG, bool ZEROS>
+template <int NG, bool ZEROS, int SROW = NG, int ZROW = NG>
 __device__ __forceinline__ I4Groups<NG> i4_load_groups(const uint16_t *s, const uint8_t *z, uint32_t row) {
   I4Groups<NG> r;
-  s += row * NG;
-  z += row * NG;
+  s += row * SROW;
+  z += row * ZROW;
   if constexpr (NG == 4) {
     const u32x2_t v = *reinterpret_cast<const u32x2_t *>(s);
     r.s[0] = v.x;

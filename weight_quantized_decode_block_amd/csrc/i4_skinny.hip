@@ -47,10 +47,13 @@ struct Rest {
   uint32_t ldc, scale_bf16, top_k, E;
 };
 
+// BY_ROW: scales and zero points row by row: 16 lanes then touch 16 lines for them at each step, where those of a tile are
+// one or two (1 x 5120, K = 5120 6.0 us, in tiles 5.7; 16 x 5120, K = 17408 in groups of 64 with zero points 23.7 and
+// 15.9; 33 tokens' last products 27.2 and 23.0).
 // NT: 16-row weight tiles of a wave (of either matrix).  KS of the NW waves share K; NW / KS
 // such groups stand side by side.  DEPTH: steps in flight.  The arguments up to SU are in
 // registers when a wave starts.  M: rows, or tokens.
-template <int NW, int MMAX, int NT, int KS, int DEPTH, bool GATED, int NG, bool ZEROS, int ROWS>
+template <int NW, int MMAX, int NT, int KS, int DEPTH, bool GATED, int NG, bool ZEROS, bool BY_ROW, int ROWS>
 __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__restrict__ W, const uint16_t *__restrict__ S,
                                                             const uint16_t *__restrict__ A, uint32_t K, uint32_t N,
                                                             uint32_t M, uint32_t lda, const uint8_t *__restrict__ Z,
@@ -128,8 +131,17 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__res
       const uint32_t row = tile + j / G < tiles ? tile + j / G : tiles - 1u;
       const uint64_t at = ((uint64_t)e * tiles + row) * kt + t;
       const bool up = GATED && (j & 1);
+      // this step's scales of the tile's first row, and by how many steps' this lane's come later: of a row that there is
+      const uint64_t group = (BY_ROW ? ((uint64_t)e * N + row * 16u) * kt + t : at * 16u) * NG;
+      uint32_t own = r;
+      if constexpr (BY_ROW) {
+        uint32_t last = (N - 1u - row * 16u) * kt;
+        asm volatile("" : "+s"(last));  // formed here: kept from step to step they would not fit the registers
+        own = r * kt < last ? r * kt : last;
+        if (MMAX > 16) __builtin_amdgcn_sched_barrier(0);  // and of several tiles at once neither
+      }
       x.w[j] = *reinterpret_cast<const u32x4_t *>((up ? WU : W) + at * kI4Tile + lane * 16u);
-      x.s[j] = i4_load_groups<NG, ZEROS>((up ? SU : S) + at * (16u * NG), (up ? op.ZU : Z) + at * (16u * NG), r);
+      x.s[j] = i4_load_groups<NG, ZEROS>((up ? SU : S) + group, (up ? op.ZU : Z) + group, own);
     }
 #pragma unroll
     for (int i = 0; i < SA; ++i) x.a[i] = arow[i][a0 + t * 16u];
@@ -244,29 +256,32 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__res
   }
 }
 
-template <int MMAX, int NT, int KS, int DEPTH, bool GATED, int NG, bool ZEROS, int ROWS>
+template <int MMAX, int NT, int KS, int DEPTH, bool GATED, int NG, bool ZEROS, bool BY_ROW, int ROWS>
 hipError_t launch_kernel(const I4Operands &op, uint32_t count, hipStream_t stream) {
   constexpr int NW = KS > kWaves ? KS : kWaves;
   constexpr uint32_t kCols = 16 * NT * (NW / KS);
   const Rest rest = {op.up.Z, op.C, op.Y, op.ids, op.order, op.offsets, op.weights, op.ldc, op.scale_bf16, op.top_k, op.E};
-  hipLaunchKernelGGL((i4_skinny_kernel<NW, MMAX, NT, KS, DEPTH, GATED, NG, ZEROS, ROWS>), dim3((op.N + kCols - 1u) / kCols, count),
+  hipLaunchKernelGGL((i4_skinny_kernel<NW, MMAX, NT, KS, DEPTH, GATED, NG, ZEROS, BY_ROW, ROWS>), dim3((op.N + kCols - 1u) / kCols, count),
                      dim3(64 * NW), 0, stream, op.w.W, op.w.S, op.A, op.K, op.N, ROWS == kDense ? op.M : op.T, op.lda, op.w.Z,
                      op.up.W, op.up.S, rest);
   return hipGetLastError();
 }
 
+template <int MMAX, int NT, int KS, int DEPTH, bool GATED, int NG, int ROWS>
+hipError_t launch_group(const I4Operands &op, uint32_t count, hipStream_t stream) {
+  if (op.by_row)
+    return op.w.Z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, true, true, ROWS>(op, count, stream)
+                  : launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, false, true, ROWS>(op, count, stream);
+  return op.w.Z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, true, false, ROWS>(op, count, stream)
+                : launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, false, false, ROWS>(op, count, stream);
+}
+
 // `count`: chunks, pairs or tokens, the grid's second dimension
 template <int MMAX, int NT, int KS, int DEPTH, bool GATED, int ROWS>
 hipError_t launch_cfg(const I4Operands &op, uint32_t count, hipStream_t stream) {
-  const bool z = op.w.Z != nullptr;
-  if (op.group == 128u)
-    return z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, 1, true, ROWS>(op, count, stream)
-             : launch_kernel<MMAX, NT, KS, DEPTH, GATED, 1, false, ROWS>(op, count, stream);
-  if (op.group == 64u)
-    return z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, 2, true, ROWS>(op, count, stream)
-             : launch_kernel<MMAX, NT, KS, DEPTH, GATED, 2, false, ROWS>(op, count, stream);
-  return z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, 4, true, ROWS>(op, count, stream)
-           : launch_kernel<MMAX, NT, KS, DEPTH, GATED, 4, false, ROWS>(op, count, stream);
+  if (op.group == 128u) return launch_group<MMAX, NT, KS, DEPTH, GATED, 1, ROWS>(op, count, stream);
+  if (op.group == 64u) return launch_group<MMAX, NT, KS, DEPTH, GATED, 2, ROWS>(op, count, stream);
+  return launch_group<MMAX, NT, KS, DEPTH, GATED, 4, ROWS>(op, count, stream);
 }
 
 // Chunks (pairs, tokens) of one launch: the grid's second dimension holds 65535, and all its threads are half of 2^32

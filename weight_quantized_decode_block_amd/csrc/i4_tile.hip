@@ -58,13 +58,26 @@ __device__ __forceinline__ rsrc_t bytes_rsrc(const void *p, uint64_t offset, uin
 __device__ __forceinline__ void copy16_to_lds(uint32_t lds, rsrc_t r, uint32_t voff) {
   asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "{m0}"(lds), "v"(voff), "s"(r) : "memory");
 }
-// The same of 4 bytes for each of the first LANES lanes, where all 64 are active.
-template <int LANES>
-__device__ __forceinline__ void copy4_to_lds(uint32_t lds, rsrc_t r, uint32_t voff) {
-  asm volatile("s_mov_b64 exec, %3\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds\n\ts_mov_b64 exec, -1"
-               :
-               : "{m0}"(lds), "v"(voff), "s"(r), "s"((1ull << LANES) - 1ull)
-               : "memory");
+// BYTES (4, 2 or 1, in multiples of which voff is) for each of the first LANES lanes, where all 64 are
+// active, to LDS byte `lds` + 4 * lane; fewer than 4 are followed by zeros.
+template <int LANES, int BYTES = 4>
+__device__ __forceinline__ void copy_to_lds(uint32_t lds, rsrc_t r, uint32_t voff) {
+  constexpr uint64_t lanes = (1ull << LANES) - 1ull;
+  if constexpr (BYTES == 4)
+    asm volatile("s_mov_b64 exec, %3\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds\n\ts_mov_b64 exec, -1"
+                 :
+                 : "{m0}"(lds), "v"(voff), "s"(r), "s"(lanes)
+                 : "memory");
+  else if constexpr (BYTES == 2)
+    asm volatile("s_mov_b64 exec, %3\n\ts_nop 0\n\tbuffer_load_ushort %1, %2, 0 offen lds\n\ts_mov_b64 exec, -1"
+                 :
+                 : "{m0}"(lds), "v"(voff), "s"(r), "s"(lanes)
+                 : "memory");
+  else
+    asm volatile("s_mov_b64 exec, %3\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds\n\ts_mov_b64 exec, -1"
+                 :
+                 : "{m0}"(lds), "v"(voff), "s"(r), "s"(lanes)
+                 : "memory");
 }
 
 // Wait until at most N of this wave's transfers are in flight and its LDS
@@ -89,8 +102,9 @@ constexpr uint32_t kStage = BM * 256 + 16 * (kI4Tile + 128 + (ZEROS ? 64 : 0)) +
 template <int BM, int NG, bool ZEROS>
 constexpr uint32_t kLdsBytes = NBUF * kStage<BM, NG, ZEROS> + BM * 4;
 
-// WM: waves side by side in m; 8 / WM in n.
-template <int BM, int WM, bool GATED, int NG, bool ZEROS, int ROWS>
+// WM: waves side by side in m; 8 / WM in n.  BY_ROW: scales and zero points row by row; a transfer takes what a step
+// needs of each of 16 rows (4096 x 5120, K = 5120 212 us, in tiles 208; gated 500 x 17408, K = 5120 with zero points 210 and 205).
+template <int BM, int WM, bool GATED, int NG, bool ZEROS, bool BY_ROW, int ROWS>
 __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uint32_t tm) {
   static_assert(BM <= 128, "a wave forms the sums of 16 rows");
   constexpr int MT = BM / WM / 32, NS = WM, AU = BM / 32;  // 32 x 32 tiles of a wave; its transfers of activations
@@ -159,21 +173,35 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
     const uint32_t t = col * BNT + (GATED ? wave : wave * 2u + i);
     const uint64_t at = ((uint64_t)expert * tiles + (t < tiles ? t : tiles - 1u)) * kt;
     wr[i] = bytes_rsrc(m.W, at * kI4Tile, kt * kI4Tile);
-    sr[i] = bytes_rsrc(m.S, at * (32u * NG), kt * (32u * NG));
-    if constexpr (ZEROS) zr[i] = bytes_rsrc(m.Z, at * (16u * NG), kt * (16u * NG));
+    // the tile's scales: its row of tiles', or the rows that there are
+    const uint32_t row = (t < tiles ? t : tiles - 1u) * 16u, left = op.N - row;
+    const uint64_t groups = BY_ROW ? ((uint64_t)expert * op.N + row) * kt * NG : at * (16u * NG);
+    const uint32_t count = (BY_ROW && left < 16u ? left : 16u) * kt * NG;
+    sr[i] = bytes_rsrc(m.S, groups * 2u, count * 2u);
+    if constexpr (ZEROS) zr[i] = bytes_rsrc(m.Z, groups, count);
   }
+  // Row by row a lane brings its row's piece, 4 bytes at most: rows of scales lie kSRow and of zero points kZRow
+  // elements apart in LDS then
+  constexpr int kSRow = BY_ROW && NG == 1 ? 2 : NG, kZRow = BY_ROW ? 4 : NG;
+  constexpr int kSBytes = NG == 1 ? 2 : 4, kZBytes = NG;
+  const uint32_t srow = NG == 4 ? (lane >> 1) * (kt * 8u) + (lane & 1u) * 4u : lane * (kt * (2u * NG)), zrow = lane * (kt * NG);
   // Transfer i of step s to its stage.  Past the last step it comes once more.
-  // Scales and zero points beyond a tile's row of them are read as zeros and not used.
+  // Scales and zero points beyond a tile's are read as zeros and not used.
   auto issue = [&](int i, uint32_t s, uint32_t stage) __attribute__((always_inline)) {
     const uint32_t t = s < kt ? s : kt - 1u, h = (i - AU) & 1, to = lds0 + stage;
     if (i < AU)
       copy16_to_lds(to + (wave + i * kWaves) * 1024u, ar, aoff[i] + t * 256u);
     else if (i < AU + 2)
       copy16_to_lds(to + kW + (wave * 2u + h) * kI4Tile, wr[h], t * kI4Tile + lane * 16u);
-    else if (i < AU + 4)
-      copy4_to_lds<32>(to + kS + (wave * 2u + h) * 128u, sr[h], t * (32u * NG) + lane * 4u);
+    else if (i < AU + 4) {
+      if constexpr (BY_ROW)
+        copy_to_lds<NG == 4 ? 32 : 16, kSBytes>(to + kS + (wave * 2u + h) * 128u, sr[h], t * (2u * NG) + srow);
+      else
+        copy_to_lds<32>(to + kS + (wave * 2u + h) * 128u, sr[h], t * (32u * NG) + lane * 4u);
+    } else if constexpr (BY_ROW)
+      copy_to_lds<16, kZBytes>(to + kZ + (wave * 2u + h) * 64u, zr[h], t * NG + zrow);
     else
-      copy4_to_lds<16>(to + kZ + (wave * 2u + h) * 64u, zr[h], t * (16u * NG) + lane * 4u);
+      copy_to_lds<16>(to + kZ + (wave * 2u + h) * 64u, zr[h], t * (16u * NG) + lane * 4u);
   };
 
   f32x16_t acc[MT][NS];
@@ -201,7 +229,7 @@ __global__ __launch_bounds__(64 * kWaves) void i4_tile_kernel(I4Operands op, uin
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h)
         x.w[i][h] = *reinterpret_cast<const u32x4_t *>(p + kW + t * kI4Tile + (2u * h + kk) * 256u + r * 16u);
-      x.s[i] = i4_load_groups<NG, ZEROS>(reinterpret_cast<const uint16_t *>(p + kS + t * 128u), p + kZ + t * 64u, r);
+      x.s[i] = i4_load_groups<NG, ZEROS, kSRow, kZRow>(reinterpret_cast<const uint16_t *>(p + kS + t * 128u), p + kZ + t * 64u, r);
     }
     return x;
   };
@@ -490,9 +518,9 @@ hipError_t allow_lds(const void *kern, std::atomic<uint64_t> &ready) {
   return e;
 }
 
-template <int BM, int WM, bool GATED, int NG, bool ZEROS, int ROWS>
+template <int BM, int WM, bool GATED, int NG, bool ZEROS, bool BY_ROW, int ROWS>
 hipError_t launch_kernel(const I4Operands &op, uint32_t tm, hipStream_t stream) {
-  const auto kern = i4_tile_kernel<BM, WM, GATED, NG, ZEROS, ROWS>;
+  const auto kern = i4_tile_kernel<BM, WM, GATED, NG, ZEROS, BY_ROW, ROWS>;
   constexpr uint32_t kLds = kLdsBytes<BM, NG, ZEROS>;
   static_assert(kLds <= 160 * 1024, "one workgroup's LDS");
   static std::atomic<uint64_t> ready;  // devices on which the kernel may use that much LDS
@@ -503,14 +531,20 @@ hipError_t launch_kernel(const I4Operands &op, uint32_t tm, hipStream_t stream) 
   return hipGetLastError();
 }
 
+template <int BM, int WM, bool GATED, int NG, int ROWS>
+hipError_t launch_group(const I4Operands &op, uint32_t tm, hipStream_t stream) {
+  if (op.by_row)
+    return op.w.Z ? launch_kernel<BM, WM, GATED, NG, true, true, ROWS>(op, tm, stream)
+                  : launch_kernel<BM, WM, GATED, NG, false, true, ROWS>(op, tm, stream);
+  return op.w.Z ? launch_kernel<BM, WM, GATED, NG, true, false, ROWS>(op, tm, stream)
+                : launch_kernel<BM, WM, GATED, NG, false, false, ROWS>(op, tm, stream);
+}
+
 template <int BM, int WM, bool GATED, int ROWS>
 hipError_t launch_cfg(const I4Operands &op, uint32_t tm, hipStream_t stream) {
-  const bool z = op.w.Z != nullptr;
-  if (op.group == 128u)
-    return z ? launch_kernel<BM, WM, GATED, 1, true, ROWS>(op, tm, stream) : launch_kernel<BM, WM, GATED, 1, false, ROWS>(op, tm, stream);
-  if (op.group == 64u)
-    return z ? launch_kernel<BM, WM, GATED, 2, true, ROWS>(op, tm, stream) : launch_kernel<BM, WM, GATED, 2, false, ROWS>(op, tm, stream);
-  return z ? launch_kernel<BM, WM, GATED, 4, true, ROWS>(op, tm, stream) : launch_kernel<BM, WM, GATED, 4, false, ROWS>(op, tm, stream);
+  if (op.group == 128u) return launch_group<BM, WM, GATED, 1, ROWS>(op, tm, stream);
+  if (op.group == 64u) return launch_group<BM, WM, GATED, 2, ROWS>(op, tm, stream);
+  return launch_group<BM, WM, GATED, 4, ROWS>(op, tm, stream);
 }
 
 template <int BM, int WM, bool GATED>
@@ -574,7 +608,7 @@ hipError_t launch_way(const I4Operands &op, uint32_t way, hipStream_t stream) {
   return op.gated ? launch_dense<128, 2, true>(op, stream) : launch_dense<128, 2, false>(op, stream);
 }
 
-// Outputs from n on (a whole number of weight tiles)
+// Outputs from n on (a whole number of weight tiles): rows of scales in tiles and row by row are as long
 I4Matrix from_row(const I4Matrix &m, const I4Operands &op, uint32_t n) {
   const uint64_t values = (uint64_t)n * op.K;
   return {m.W ? m.W + values / 2u : nullptr, m.S ? m.S + values / op.group : nullptr, m.Z ? m.Z + values / op.group : nullptr};

@@ -99,8 +99,8 @@ hipError_t launch_mx_dequantize(const void *Q, const void *S, bool fp4, void *Y,
 hipError_t launch_add_rmsnorm_mx8(const void *X, const void *R, const void *G, void *H, void *Y, void *Q, void *S,
                                   uint32_t M, uint32_t K, uint32_t ldx, uint32_t ldr, float eps, hipStream_t stream);
 
-// A matrix of 4-bit integer weights (or several, one after another), laid out in
-// tiles: codes, scales in FP16 or BF16, zero points or null.
+// A matrix of 4-bit integer weights (or several, one after another): codes in
+// tiles, scales in FP16 or BF16 and zero points (or null) in tiles or row by row.
 struct I4Matrix {
   const uint8_t *W;
   const uint16_t *S;
@@ -121,6 +121,7 @@ struct I4Operands {
   uint32_t M, N, K, lda, ldc, group, scale_bf16;
   uint32_t T, top_k, E;
   bool gated;
+  bool by_row;  // scales and zero points [E][N][K/group], not in tiles
 };
 
 // Enqueue a dense product (i4_tile.hip chooses the kernel; launch_i4_skinny is

@@ -26,6 +26,7 @@ Q2_0_BATCHM_MAX_M = 8
 W8A16_MAX_M = 16
 MXFP4, MXFP8 = 4, 8  # WQD_MXFP4, WQD_MXFP8
 TYPE_BF16, TYPE_FP16, TYPE_FP32 = range(3)  # WQD_TYPE_*
+I4_BY_ROW = 0x100  # WQD_I4_BY_ROW
 MOE_SOFTMAX, MOE_SIGMOID = range(2)  # WQD_MOE_*
 Q2_0_TIER_WIDTHS = (1, 2, 4, 6, 8)  # WQD_Q2_0_TIER_WIDTHS, narrowest first
 
@@ -432,24 +433,58 @@ def _i4_sizes(fn: str, bits: int, K: int, group: int) -> None:
         raise WqdError(fn, WQD_EINVAL, f"{fn}: group={group} is not 32, 64 or 128")
 
 
-def _i4_scale_type(fn: str, given: int | None, *scales) -> int:
-    """WQD_TYPE_* of the scales (an address comes with its type, FP16 unless told)."""
-    t = given
-    for s in scales:
-        if s is None or isinstance(s, int):
-            continue
-        own = _types.get(s.dtype)
-        if own not in (TYPE_FP16, TYPE_BF16) or t not in (None, own):
-            raise ValueError(f"{fn}: scales must all be FP16 or all BF16, as their tensors are ({str(s.dtype)[6:]})")
-        t = own
-    return TYPE_FP16 if t is None else t
+def _i4_by_row(shape, E: int, N: int, K: int, group: int) -> bool | None:
+    """Whether scales or zero points of E matrices lie row by row and not in tiles.  Both are as many bytes where N is a multiple
+    of 16, so the shape has to tell: [N, K / group] ([E, N, K / group], or with the first two as one) is row by row; flat
+    memory, whole matrices that are flat and [..., K / 128, 16, 128 / group] are tiles.  None: neither."""
+    n = len(shape)
+    if n < 2:
+        return False
+    last, g = shape[-1], K // group
+    if n > 2 and shape[-2] == 16 and last * group == 128 and shape[-3] * 128 == K:
+        return False
+    if last == g and (E == 1 or shape[-2] == (N if n > 2 else E * N)):
+        return True
+    return None if last % ((N + 15 & -16) * g or 1) else False
 
 
-def _i4_matrix(fn: str, name: str, W, S, Z, E: int, N: int, K: int, group: int, d: int) -> tuple:
-    """Addresses of E laid-out matrices' codes, scales and zero points."""
+def _i4_scales(fn: str, given: int | None, E: int, N: int, K: int, group: int, *matrices) -> int:
+    """scale_type of a call: `matrices` are the names, scales and zero points of each.  An address comes with its type, FP16
+    and in tiles unless told (TYPE_*, plus I4_BY_ROW where it is row by row)."""
+    t = by_row = seen = None
+    if given is not None:
+        t, by_row = given & ~I4_BY_ROW, True if given & I4_BY_ROW else None
+    for name, s, z in matrices:
+        if not (s is None or isinstance(s, int)):
+            own = _types.get(s.dtype)
+            if own != t:
+                if t is not None or own not in (TYPE_FP16, TYPE_BF16):
+                    raise ValueError(f"{fn}: scales must all be FP16 or all BF16, as their tensors are ({str(s.dtype)[6:]})")
+                t = own
+        for x in (s, z):
+            if x is None or isinstance(x, int):
+                continue
+            shape = x.shape
+            if shape == seen:
+                continue
+            seen, rows = shape, _i4_by_row(shape, E, N, K, group)
+            if rows is None:
+                raise ValueError(f"{fn}: {name}{'S' if x is s else 'Z'} of shape {list(shape)} is neither row by row, "
+                                 f"{[E, N, K // group]}, nor in tiles as i4_pack writes them, flat or [..., {K // 128}, 16, {128 // group}]")
+            if rows is not by_row:
+                if by_row is not None:
+                    raise ValueError(f"{fn}: scales and zero points must all lie row by row or all in tiles, and not "
+                                     f"{name}{'S' if x is s else 'Z'} alone")
+                by_row = rows
+    return (TYPE_FP16 if t is None else t) | (I4_BY_ROW if by_row else 0)
+
+
+def _i4_matrix(fn: str, name: str, W, S, Z, E: int, N: int, K: int, group: int, d: int, by_row: int = 0) -> tuple:
+    """Addresses of E matrices' laid-out codes, scales and zero points."""
     n = E * (N + 15 & -16) * K
-    return (_arg(fn, name, W, n // 2, d, _BYTES), _arg(fn, name + "S", S, n // group * 2, d, _I4_SCALES),
-            _arg(fn, name + "Z", Z, n // group, d, _BYTES))
+    m, g = (E * N * K // group, K // group) if by_row else (n // group, 0)
+    return (_arg(fn, name, W, n // 2, d, _BYTES), _arg(fn, name + "S", S, m * 2, d, _I4_SCALES, g),
+            None if Z is None else _arg(fn, name + "Z", Z, m, d, _BYTES, g))
 
 
 def i4_packed_rows(N: int) -> int:
@@ -459,13 +494,17 @@ def i4_packed_rows(N: int) -> int:
 
 def i4_pack(Q, S, Z, W, WS, WZ, N: int, K: int, group: int, count: int = 1, stream=None) -> None:
     """`count` matrices to the layout that the products read: codes Q, two a byte with
-    the even k in the low nibble, scales S and zero points Z (or None, and WZ too)."""
+    the even k in the low nibble, scales S and zero points Z (or None, and WZ too).  WS and
+    WZ are tiles, and their shape says so: flat, or [..., K / 128, 16, 128 / group]."""
     fn = "i4_pack"
     _i4_sizes(fn, N | K | count, K, group)
     d, st = _here(fn, stream)
     n, g = count * N * K, K // group
     if not isinstance(S, int) and not isinstance(WS, int) and S is not None and WS is not None and S.dtype != WS.dtype:
         raise ValueError(f"{fn}: S and WS must have the same type")
+    for name, x in ("WS", WS), ("WZ", WZ):
+        if x is not None and not isinstance(x, int) and _i4_by_row(x.shape, count, N, K, group) is not False:
+            raise ValueError(f"{fn}: {name} of shape {list(x.shape)} is not in tiles: make it flat")
     _check(fn, (_lib or lib()).i4_pack(_arg(fn, "Q", Q, n // 2, d, _BYTES, K // 2), _arg(fn, "S", S, n // group * 2, d, _I4_SCALES, g),
                                        _arg(fn, "Z", Z, n // group, d, _BYTES, g),
                                        *_i4_matrix(fn, "W", W, WS, WZ, count, N, K, group, d), N, K, group, count, st))
@@ -473,28 +512,30 @@ def i4_pack(Q, S, Z, W, WS, WZ, N: int, K: int, group: int, count: int = 1, stre
 
 def i4a16_gemm(A, W, WS, WZ, C, M: int, N: int, K: int, group: int, a_row_stride: int | None = None,
                c_row_stride: int | None = None, scale_type: int | None = None, stream=None) -> None:
-    """C = A W^T, W in laid-out codes W, scales WS and zero points WZ (None: 8)."""
+    """C = A W^T, W in laid-out codes W, scales WS and zero points WZ (None: 8).  Scales and
+    zero points lie in tiles, as i4_pack writes them, or row by row, [N, K / group]: their
+    tensors' shape tells (_i4_by_row); with addresses pass `scale_type`, for rows plus I4_BY_ROW."""
     fn = "i4a16_gemm"
     lda, ldc = K if a_row_stride is None else a_row_stride, N if c_row_stride is None else c_row_stride
     _i4_sizes(fn, M | N | K | lda | ldc, K, group)
     d, st = _here(fn, stream)
-    t = _i4_scale_type(fn, scale_type, WS)
+    t = _i4_scales(fn, scale_type, 1, N, K, group, ("W", WS, WZ))
     _check(fn, (_lib or lib()).i4a16_gemm(_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda),
-                                          *_i4_matrix(fn, "W", W, WS, WZ, 1, N, K, group, d),
+                                          *_i4_matrix(fn, "W", W, WS, WZ, 1, N, K, group, d, t & I4_BY_ROW),
                                           _arg(fn, "C", C, _span(M, ldc, N, 2), d, _BF16, ldc), M, N, K, group, t, lda, ldc, st))
 
 
 def i4a16_gated(A, WG, WGS, WGZ, WU, WUS, WUZ, C, M: int, N: int, K: int, group: int, a_row_stride: int | None = None,
                 c_row_stride: int | None = None, scale_type: int | None = None, stream=None) -> None:
-    """C = silu(A WG^T) * (A WU^T)."""
+    """C = silu(A WG^T) * (A WU^T); scales and zero points as for i4a16_gemm."""
     fn = "i4a16_gated"
     lda, ldc = K if a_row_stride is None else a_row_stride, N if c_row_stride is None else c_row_stride
     _i4_sizes(fn, M | N | K | lda | ldc, K, group)
     d, st = _here(fn, stream)
-    t = _i4_scale_type(fn, scale_type, WGS, WUS)
+    t = _i4_scales(fn, scale_type, 1, N, K, group, ("WG", WGS, WGZ), ("WU", WUS, WUZ))
     _check(fn, (_lib or lib()).i4a16_gated(_arg(fn, "A", A, _span(M, lda, K, 2), d, _BF16, lda),
-                                           *_i4_matrix(fn, "WG", WG, WGS, WGZ, 1, N, K, group, d),
-                                           *_i4_matrix(fn, "WU", WU, WUS, WUZ, 1, N, K, group, d),
+                                           *_i4_matrix(fn, "WG", WG, WGS, WGZ, 1, N, K, group, d, t & I4_BY_ROW),
+                                           *_i4_matrix(fn, "WU", WU, WUS, WUZ, 1, N, K, group, d, t & I4_BY_ROW),
                                            _arg(fn, "C", C, _span(M, ldc, N, 2), d, _BF16, ldc), M, N, K, group, t, lda, ldc, st))
 
 
@@ -539,12 +580,13 @@ def i4a16_experts_gated(A, ids, order, offsets, WG, WGS, WGZ, WU, WUS, WUZ, H, T
     fn, lda = "i4a16_experts_gated", K if a_row_stride is None else a_row_stride
     _i4_sizes(fn, T | top_k | E | N | K | lda, K, group)
     d, st = _here(fn, stream)
-    t = _i4_scale_type(fn, scale_type, WGS, WUS)
+    t = _i4_scales(fn, scale_type, E, N, K, group, ("WG", WGS, WGZ), ("WU", WUS, WUZ))
     pairs = T * top_k
     _check(fn, (_lib or lib()).i4a16_experts_gated(
         _arg(fn, "A", A, _span(T, lda, K, 2), d, _BF16, lda), _arg(fn, "ids", ids, 4 * pairs, d, _INT32, top_k),
         _arg(fn, "order", order, 4 * pairs, d, _INT32), _arg(fn, "offsets", offsets, 4 * (E + 1), d, _INT32),
-        *_i4_matrix(fn, "WG", WG, WGS, WGZ, E, N, K, group, d), *_i4_matrix(fn, "WU", WU, WUS, WUZ, E, N, K, group, d),
+        *_i4_matrix(fn, "WG", WG, WGS, WGZ, E, N, K, group, d, t & I4_BY_ROW),
+        *_i4_matrix(fn, "WU", WU, WUS, WUZ, E, N, K, group, d, t & I4_BY_ROW),
         _arg(fn, "H", H, 2 * pairs * N, d, _BF16, N), T, top_k, E, N, K, group, t, lda, st))
 
 
@@ -555,12 +597,12 @@ def i4a16_experts_down(H, ids, weights, order, offsets, W, WS, WZ, Y, C, T: int,
     fn, ldc = "i4a16_experts_down", N if c_row_stride is None else c_row_stride
     _i4_sizes(fn, T | top_k | E | N | K | ldc, K, group)
     d, st = _here(fn, stream)
-    t = _i4_scale_type(fn, scale_type, WS)
+    t = _i4_scales(fn, scale_type, E, N, K, group, ("W", WS, WZ))
     pairs = T * top_k
     _check(fn, (_lib or lib()).i4a16_experts_down(
         _arg(fn, "H", H, 2 * pairs * K, d, _BF16, K), _arg(fn, "ids", ids, 4 * pairs, d, _INT32, top_k),
         _arg(fn, "weights", weights, 4 * pairs, d, _FP32, top_k), _arg(fn, "order", order, 4 * pairs, d, _INT32),
-        _arg(fn, "offsets", offsets, 4 * (E + 1), d, _INT32), *_i4_matrix(fn, "W", W, WS, WZ, E, N, K, group, d),
+        _arg(fn, "offsets", offsets, 4 * (E + 1), d, _INT32), *_i4_matrix(fn, "W", W, WS, WZ, E, N, K, group, d, t & I4_BY_ROW),
         _arg(fn, "Y", Y, 4 * pairs * N, d, _FP32, N), _arg(fn, "C", C, _span(T, ldc, N, 2), d, _BF16, ldc),
         T, top_k, E, N, K, group, t, ldc, st))
 
