@@ -87,25 +87,23 @@ def _rows(g, m, k):
     return (_normal(g, m, k) * gain).to(torch.bfloat16)
 
 
-def _laid_out(codes, s, z):
-    """Weights as the library takes them. Codes: tiles of 16 rows x 128 k, 1024 bytes each, row tile by row tile. Byte 256 g +
+def _laid_out(codes):
+    """Codes as the library takes them: tiles of 16 rows x 128 k, 1024 bytes each, row tile by row tile. Byte 256 g +
     16 n + 4 j + b of a tile holds two codes of row n, k = 32 j + 8 g + (0, 2, 4, 6, 1, 3, 5, 7)[2 b] and [2 b + 1], the
-    first in the low nibble. Scales and zero points: [row tile][K / 128][16][128 / group]. Rows past the last one hold zeros."""
+    first in the low nibble. Rows past the last one hold zeros."""
     e, n, k = codes.shape
-    rows = lambda x: torch.nn.functional.pad(x, (0, 0, 0, -n % 16))  # noqa: E731
-    q = rows(codes).view(e, -1, 16, k // 128, 4, 4, 4, 2).permute(0, 1, 3, 5, 2, 4, 7, 6)
+    q = torch.nn.functional.pad(codes, (0, 0, 0, -n % 16)).view(e, -1, 16, k // 128, 4, 4, 4, 2).permute(0, 1, 3, 5, 2, 4, 7, 6)
     q = q.reshape(e, -1, 4, 2)  # pairs (0, 2), (4, 6), (1, 3), (5, 7) of each 8
-    tiles = lambda x: rows(x).view(e, -1, 16, k // 128, x.shape[-1] * 128 // k).transpose(2, 3).contiguous()  # noqa: E731
-    return (q[..., 0] | q[..., 1] << 4).view(e, -1, k // 2), tiles(s), None if z is None else tiles(z)
+    return (q[..., 0] | q[..., 1] << 4).view(e, -1, k // 2)
 
 
 def _weights(g, e, n, k, c):
-    """Codes [e, n, k], scales and zero points [e, n, k / group] (None: 8 everywhere), and the three as laid out."""
+    """Codes [e, n, k], scales and zero points [e, n, k / group] (None: 8 everywhere), and the same with the codes laid out."""
     z = torch.randint(5, 12, (e, n, k // c["group"]), generator=g, device=DEVICE, dtype=torch.uint8) if c["zeros"] else None
     q = (_normal(g, e, n, k // c["group"], c["group"]) * 2.5).round_()
     codes = q.add_(8.0 if z is None else z.unsqueeze(-1)).clamp_(0, 15).flatten(2).to(torch.uint8)
     s = ((0.5 + torch.rand(e, n, k // c["group"], generator=g, device=DEVICE)) * (0.4 * k ** -0.5)).to(SCALES[c["scale"]])
-    return (codes, s, z), _laid_out(codes, s, z)
+    return (codes, s, z), (_laid_out(codes), s, z)
 
 
 def _lists(ids, e):
