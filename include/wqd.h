@@ -367,7 +367,8 @@ int w4a4_gated(const void *A, const void *AS, const void *WG, const void *WGS, c
  * i4_pack - `count` matrices, codes uint8 [count][N][K/2] with the even k in the low
  * nibble, scales and zero points [count][N][K/group], to that layout; the scales'
  * type does not matter here.
- *   Q, S, Z     device, 4-, 2- and 1-byte aligned; Z and WZ may both be NULL
+ *   Q, S, Z     device, 4-, 2- and 1-byte aligned; Z and WZ may both be NULL, and S and
+ *               WS too: the codes alone, where the others are to stay row by row
  *   W, WS, WZ   device, 16-byte aligned; count * i4_packed_rows(N) rows of K/2 bytes, K/group
  *               scales and K/group bytes; not the inputs
  *   K  a positive multiple of 128, at most WQD_MX_MAX_K;  N  1 .. WQD_MX_MAX_ROWS;

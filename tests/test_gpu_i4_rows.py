@@ -122,6 +122,18 @@ def test_experts_exact(T, E, top_k, N, K, group, zeros, scale):
         assert torch.equal(C[:T].cpu(), want) and untouched(C, T, N)
 
 
+@pytest.mark.parametrize("E,N,K,group", [(1, 1, 128, 128), (3, 17, 384, 32), (2, 100, 1152, 64)])
+def test_pack_of_codes_alone(E, N, K, group):
+    w = ref.Weights(ref.generator(73, E, N, K), E, N, K, group, True, "fp16", exact=True)
+    W = torch.full((E * wqd.i4_packed_rows(N) * K // 2 + 32,), 0xA5, dtype=torch.uint8, device="cuda")
+    wqd.i4_pack(ref.rows_of_pairs(w.codes).cuda(), None, None, W, None, None, N, K, group, E)
+    assert torch.equal(W[:-32].cpu(), ref.laid_out(w.codes).flatten()) and bool((W[-32:] == 0xA5).all())
+    a, A = rows(ref.generator(74, N), 3, K, exact=True)
+    C = out(3, N, N)
+    wqd.i4a16_gemm(A, W[:-32], w.s.cuda(), w.z.cuda(), C, 3, N, K, group)
+    assert torch.equal(C[:3].cpu(), (a.double() @ w.values()[0].T).to(BF)) and untouched(C, 3, N)
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_every_scale_of_a_slice(M):
     """Rows that begin anywhere: scales and zero points of rows 1 .. of a larger matrix, aligned to their own loads only."""

@@ -3,7 +3,7 @@ shapes say, and shapes that say neither, or both, are refused before the library
 import pytest
 import torch
 
-from test_i4_abi import EALIGN, EINVAL, PRODUCTS, P, refused
+from test_i4_abi import EALIGN, EINVAL, ENULL, PRODUCTS, P, refused
 from test_i4_binding import BF, E, F16, G, K, M, N, PAD, T, U8, library, operands, run, z  # noqa: F401  (library: a fixture)
 from weight_quantized_decode_block_amd import wqd
 
@@ -117,3 +117,13 @@ def test_the_library_checks_rows(fn):
                 EALIGN, "C must" if "gemm" in fn or fn == "i4a16_gated" else "ids")
     for t in (2 | row, 3 | row, 0x200, 0x300, row << 1):
         refused(fn, dict(t=t), EINVAL, "scale type")
+
+
+def test_pack_of_codes_alone(library):  # noqa: F811
+    run("i4_pack", operands()["i4_pack"] | dict(S=None, Z=None, WS=None, WZ=None))
+    assert [library.calls[-1][1][i] for i in (1, 2, 4, 5)] == [None] * 4
+
+
+@pytest.mark.parametrize("change", [dict(S=None), dict(WS=None), dict(S=None, Z=None, WZ=None), dict(WS=None, Z=None, WZ=None)])
+def test_pack_of_half_the_scales(change):
+    refused("i4_pack", change, ENULL, "S and WS must both be non-NULL")

@@ -489,7 +489,8 @@ int w4a4_gated(const void *A, const void *AS, const void *WG, const void *WGS, c
 int i4_pack(const void *Q, const void *S, const void *Z, void *W, void *WS, void *WZ, uint32_t N, uint32_t K,
             uint32_t group, uint32_t count, hipStream_t stream) {
   static const char fn[] = "i4_pack";
-  if (count && (!Q || !S || !W || !WS)) return fail(WQD_ENULL, "%s: Q, S, W and WS must be non-NULL", fn);
+  if (count && (!Q || !W)) return fail(WQD_ENULL, "%s: Q and W must be non-NULL", fn);
+  if (count && !S != !WS) return fail(WQD_ENULL, "%s: S and WS must both be non-NULL or both be NULL", fn);
   if (count && !Z != !WZ) return fail(WQD_ENULL, "%s: Z and WZ must both be given or both be NULL", fn);
   if (N == 0) return fail(WQD_EINVAL, "%s: N must be >= 1", fn);
   if (K == 0 || K % 128u != 0) return fail(WQD_EINVAL, "%s: K=%u is not a positive multiple of 128", fn, K);

@@ -1,8 +1,8 @@
 // Layout of 4-bit integer weights for gfx950 (MI355X): rows of codes, two a
 // byte, to the tiles that the products read (i4_common.h).  Done once per
 // matrix.  A thread gathers the 16 bytes of one lane of a tile from four dwords
-// of its row, and a scale and a zero point; rows past the matrix are written as
-// zeros.
+// of its row, and a scale and a zero point, where they are to be in tiles too; rows past the
+// matrix are written as zeros.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -40,7 +40,7 @@ __global__ __launch_bounds__(256) void i4_pack_kernel(const uint32_t *__restrict
   reinterpret_cast<u32x4_t *>(const_cast<uint8_t *>(to.W))[x] = v;
   if (g < groups) {  // lane (n, g): group g of row n
     const uint64_t at = (tile * 16u + n) * groups + g;
-    const_cast<uint16_t *>(to.S)[at] = row < N ? S[from * groups + g] : (uint16_t)0;
+    if (S) const_cast<uint16_t *>(to.S)[at] = row < N ? S[from * groups + g] : (uint16_t)0;
     if (Z) const_cast<uint8_t *>(to.Z)[at] = row < N ? Z[from * groups + g] : (uint8_t)0;
   }
 }

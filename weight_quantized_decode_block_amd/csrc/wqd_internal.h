@@ -137,7 +137,7 @@ hipError_t launch_i4_experts(const I4Operands &op, hipStream_t stream);
 hipError_t launch_i4_experts_skinny(const I4Operands &op, hipStream_t stream);
 
 // Enqueue the layout of `count` matrices: rows of codes, scales and zero points
-// (or null) to `to`, which is written.
+// (or null, either) to `to`, which is written.
 hipError_t launch_i4_pack(const void *Q, const I4Matrix &to, const void *S, const void *Z, uint32_t N, uint32_t K,
                           uint32_t group, uint32_t count, hipStream_t stream);
 

@@ -494,8 +494,9 @@ def i4_packed_rows(N: int) -> int:
 
 def i4_pack(Q, S, Z, W, WS, WZ, N: int, K: int, group: int, count: int = 1, stream=None) -> None:
     """`count` matrices to the layout that the products read: codes Q, two a byte with
-    the even k in the low nibble, scales S and zero points Z (or None, and WZ too).  WS and
-    WZ are tiles, and their shape says so: flat, or [..., K / 128, 16, 128 / group]."""
+    the even k in the low nibble, scales S and zero points Z (or None, and WZ too; S, Z, WS
+    and WZ None lays out the codes alone, and scales and zero points stay row by row).  WS
+    and WZ are tiles, and their shape says so: flat, or [..., K / 128, 16, 128 / group]."""
     fn = "i4_pack"
     _i4_sizes(fn, N | K | count, K, group)
     d, st = _here(fn, stream)
