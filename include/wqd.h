@@ -415,6 +415,7 @@ int i4a16_gated(const void *A, const void *WG, const void *WGS, const void *WGZ,
 #define WQD_MOE_MAX_EXPERTS  1024        /* largest E */
 #define WQD_MOE_MAX_TOP_K    32          /* largest top_k */
 #define WQD_MOE_MAX_PAIRS    (1u << 24)  /* largest T * top_k */
+#define WQD_MOE_MAX_VALUES   (1ull << 38) /* largest T * top_k * N of the experts' products */
 
 /*
  * moe_route - each token's experts and their weights.
@@ -475,10 +476,11 @@ int moe_lists(const int32_t *ids, int32_t *order, int32_t *offsets, uint32_t T, 
  *   Y    device, fp32 [T * top_k][N], 16-byte aligned: scratch, used with lists only
  *        (NULL without); two calls that may run at once need one each
  *   C    device, BF16, row t at C + t * c_row_stride
- *   The rest is as for the products and moe_route.  WQD_EUNSUPPORTED where no launch holds
- *   the call: without lists above 65535 pairs (the gated product) or tokens (the last one),
- *   or 2^21 / ceil(N/16) of them; with lists, T * top_k * N from about 2^29 on where the input
- *   has 4 GB or more, and from about 2^35 where not.
+ *   The rest is as for the products and moe_route.  WQD_EUNSUPPORTED with lists where
+ *   T * top_k * N is above WQD_MOE_MAX_VALUES, without above 65535 pairs (the gated
+ *   product) or tokens (the last one), or 2^21 / ceil(N/16) of them.  With lists a call may
+ *   take several launches; inputs of 4 GB or more take the kernel for few rows, which is
+ *   slower for many.
  */
 int i4a16_experts_gated(const void *A, const int32_t *ids, const int32_t *order, const int32_t *offsets,
                         const void *WG, const void *WGS, const void *WGZ,

@@ -45,6 +45,7 @@ struct Rest {
   const int32_t *ids, *order, *offsets;
   const float *weights;
   uint32_t ldc, scale_bf16, top_k, E;
+  uint32_t chunk;  // the first of this launch
 };
 
 // BY_ROW: scales and zero points row by row: 16 lanes then touch 16 lines for them at each step, where those of a tile are
@@ -76,7 +77,7 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__res
     first *= MMAX;
     rows = M - first < (uint32_t)MMAX ? M - first : (uint32_t)MMAX;
   } else if constexpr (ROWS == kLists) {
-    if (!i4_find_chunk<MMAX>(op.offsets, op.E, M * op.top_k, blockIdx.y, lane, expert, first, rows)) return;
+    if (!i4_find_chunk<MMAX>(op.offsets, op.E, M * op.top_k, op.chunk + blockIdx.y, lane, expert, first, rows)) return;
   } else if constexpr (ROWS == kPairs) {
     expert = (uint32_t)op.ids[first];
     if (expert >= op.E) return;
@@ -257,10 +258,10 @@ __global__ __launch_bounds__(64 * NW) void i4_skinny_kernel(const uint8_t *__res
 }
 
 template <int MMAX, int NT, int KS, int DEPTH, bool GATED, int NG, bool ZEROS, bool BY_ROW, int ROWS>
-hipError_t launch_kernel(const I4Operands &op, uint32_t count, hipStream_t stream) {
+hipError_t launch_kernel(const I4Operands &op, uint32_t count, uint32_t chunk, hipStream_t stream) {
   constexpr int NW = KS > kWaves ? KS : kWaves;
   constexpr uint32_t kCols = 16 * NT * (NW / KS);
-  const Rest rest = {op.up.Z, op.C, op.Y, op.ids, op.order, op.offsets, op.weights, op.ldc, op.scale_bf16, op.top_k, op.E};
+  const Rest rest = {op.up.Z, op.C, op.Y, op.ids, op.order, op.offsets, op.weights, op.ldc, op.scale_bf16, op.top_k, op.E, chunk};
   hipLaunchKernelGGL((i4_skinny_kernel<NW, MMAX, NT, KS, DEPTH, GATED, NG, ZEROS, BY_ROW, ROWS>), dim3((op.N + kCols - 1u) / kCols, count),
                      dim3(64 * NW), 0, stream, op.w.W, op.w.S, op.A, op.K, op.N, ROWS == kDense ? op.M : op.T, op.lda, op.w.Z,
                      op.up.W, op.up.S, rest);
@@ -268,20 +269,20 @@ hipError_t launch_kernel(const I4Operands &op, uint32_t count, hipStream_t strea
 }
 
 template <int MMAX, int NT, int KS, int DEPTH, bool GATED, int NG, int ROWS>
-hipError_t launch_group(const I4Operands &op, uint32_t count, hipStream_t stream) {
+hipError_t launch_group(const I4Operands &op, uint32_t count, uint32_t chunk, hipStream_t stream) {
   if (op.by_row)
-    return op.w.Z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, true, true, ROWS>(op, count, stream)
-                  : launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, false, true, ROWS>(op, count, stream);
-  return op.w.Z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, true, false, ROWS>(op, count, stream)
-                : launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, false, false, ROWS>(op, count, stream);
+    return op.w.Z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, true, true, ROWS>(op, count, chunk, stream)
+                  : launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, false, true, ROWS>(op, count, chunk, stream);
+  return op.w.Z ? launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, true, false, ROWS>(op, count, chunk, stream)
+                : launch_kernel<MMAX, NT, KS, DEPTH, GATED, NG, false, false, ROWS>(op, count, chunk, stream);
 }
 
-// `count`: chunks, pairs or tokens, the grid's second dimension
+// `count`: chunks, pairs or tokens, the grid's second dimension; `chunk`: the first of them, of chunks
 template <int MMAX, int NT, int KS, int DEPTH, bool GATED, int ROWS>
-hipError_t launch_cfg(const I4Operands &op, uint32_t count, hipStream_t stream) {
-  if (op.group == 128u) return launch_group<MMAX, NT, KS, DEPTH, GATED, 1, ROWS>(op, count, stream);
-  if (op.group == 64u) return launch_group<MMAX, NT, KS, DEPTH, GATED, 2, ROWS>(op, count, stream);
-  return launch_group<MMAX, NT, KS, DEPTH, GATED, 4, ROWS>(op, count, stream);
+hipError_t launch_cfg(const I4Operands &op, uint32_t count, hipStream_t stream, uint32_t chunk = 0) {
+  if (op.group == 128u) return launch_group<MMAX, NT, KS, DEPTH, GATED, 1, ROWS>(op, count, chunk, stream);
+  if (op.group == 64u) return launch_group<MMAX, NT, KS, DEPTH, GATED, 2, ROWS>(op, count, chunk, stream);
+  return launch_group<MMAX, NT, KS, DEPTH, GATED, 4, ROWS>(op, count, chunk, stream);
 }
 
 // Chunks (pairs, tokens) of one launch: the grid's second dimension holds 65535, and all its threads are half of 2^32
@@ -336,8 +337,14 @@ bool i4_experts_skinny_fit(const I4Operands &op) {
 hipError_t launch_i4_experts_skinny(const I4Operands &op, hipStream_t stream) {
   const uint32_t pairs = op.T * op.top_k;
   if (op.order) {
-    const uint32_t chunks = (uint32_t)i4_chunks(pairs, op.E, 16u);
-    return op.gated ? launch_cfg<16, 1, 2, 2, true, kLists>(op, chunks, stream) : launch_cfg<16, 2, 2, 2, false, kLists>(op, chunks, stream);
+    const uint32_t chunks = (uint32_t)i4_chunks(pairs, op.E, 16u), most = most_of(op);
+    for (uint32_t c = 0; c < chunks; c += most) {
+      const uint32_t count = chunks - c < most ? chunks - c : most;
+      const hipError_t e = op.gated ? launch_cfg<16, 1, 2, 2, true, kLists>(op, count, stream, c)
+                                    : launch_cfg<16, 2, 2, 2, false, kLists>(op, count, stream, c);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   }
   if (op.gated)
     return op.K < 4096u ? launch_cfg<4, 1, 4, 2, true, kPairs>(op, pairs, stream) : launch_cfg<4, 1, 8, 2, true, kPairs>(op, pairs, stream);

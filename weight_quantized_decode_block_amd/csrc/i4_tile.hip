@@ -654,7 +654,10 @@ static bool i4_tiles_fit(const I4Operands &op, uint32_t bm) {
          i4_chunks(pairs, op.E, bm) * ((op.N + cols - 1u) / cols) <= mx_max_grid(64 * kWaves);
 }
 
-bool i4_experts_fit(const I4Operands &op) { return i4_experts_skinny_fit(op) || (op.order && i4_tiles_fit(op, 128u)); }
+// With lists the few-row kernel takes what no launch of tiles holds, in several launches if need be.
+bool i4_experts_fit(const I4Operands &op) {
+  return op.order ? (uint64_t)op.T * op.top_k * op.N <= WQD_MOE_MAX_VALUES : i4_experts_skinny_fit(op);
+}
 
 // The lists' lengths are on the GPU: every expert is taken to have the mean of rows, and a quarter of them a chunk more.
 hipError_t launch_i4_experts(const I4Operands &op, hipStream_t stream) {

@@ -131,8 +131,8 @@ hipError_t launch_i4_skinny(const I4Operands &op, bool wide, hipStream_t stream)
 
 // Enqueue the experts' products: gated (C gets a row per pair), or the last ones
 // (with lists: Y gets a row per pair; without: C gets each token's weighted sum).
-bool i4_experts_fit(const I4Operands &op);  // whether one launch holds them
-bool i4_experts_skinny_fit(const I4Operands &op);
+bool i4_experts_fit(const I4Operands &op);         // whether there are not too many
+bool i4_experts_skinny_fit(const I4Operands &op);  // whether one launch for few rows holds them
 hipError_t launch_i4_experts(const I4Operands &op, hipStream_t stream);
 hipError_t launch_i4_experts_skinny(const I4Operands &op, hipStream_t stream);
 
