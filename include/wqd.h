@@ -384,9 +384,11 @@ uint32_t i4_packed_rows(uint32_t N);
  * i4a16_gemm, i4a16_gated - products with 4-bit integer weights:
  *   C[m,n] = bf16( sum_k a[m,k] * w[n,k] ),
  *   C[m,n] = bf16( silu(sum_k a[m,k] wg[n,k]) * sum_k a[m,k] wu[n,k] ).
- * Products are exact and sums fp32; up to a group's scale, sums of a * (16 + q)
- * and of a are formed, so activations from 2^116 on may overflow.  A row that holds an
- * infinity or NaN has no finite output; which of the two it has is not defined.
+ * Products are exact and sums fp32; up to a group's scale, sums of a * (16 + q) are
+ * formed, and (16 + z) times those of a, which is taken from them.  Outputs may be
+ * infinities or NaN where group * |a| * (16 + z) or group * |a| * 31 reaches 2^128: with
+ * zero points up to 15 from activations of 2^116 on, with any from 2^112 on.  A row that
+ * holds an infinity or NaN has no finite output; which of the two it has is not defined.
  *
  *   A   device, BF16, row m at A + m * a_row_stride, 16-byte aligned
  *   W   device, laid-out codes, 16-byte aligned
