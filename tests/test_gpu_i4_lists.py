@@ -53,3 +53,35 @@ def test_gated_products_of_4_gb_of_rows():
     want, err = ref.gated(gate, up, eg, eu)
     assert bool(((H.cpu()[some].double() - want).abs() <= ref.stored(want, err)).all()) and untouched(H, T, N)
     assert bool(torch.isfinite(H).all())
+
+
+# (T, E, top_k, N, K): the kernel for few rows, tiles of 64 and of 128 rows
+ROUTED = [(40, 8, 2, 65, 640), (2000, 4, 2, 257, 128), (2000, 5, 3, 513, 640)]
+
+
+@pytest.mark.parametrize("T,E,top_k,N,K", ROUTED)
+def test_lists_that_point_elsewhere_stay_inside(T, E, top_k, N, K):
+    """Lists that are not moe_lists' of any ids are read and written within the operands all the same, in every kernel."""
+    g, pairs, group, guard = ref.generator(87, T), T * top_k, 64, 64
+    wg, wu, wd = (ref.Weights(g, E, N, K, group, True, "fp16").operands() for _ in range(3))
+    ids = moe.choice(g, T, E, top_k).cuda()
+    a, h = torch.randn(T, K, generator=g).to(BF).cuda(), torch.randn(pairs, K, generator=g).to(BF).cuda()
+    weights = torch.rand(T, top_k, generator=g).cuda()
+    some = torch.randint(-(1 << 31), (1 << 31) - 1, (pairs,), generator=g)
+    for offsets in ([0] + [pairs] * E, [pairs] * (E + 1), [-1] * (E + 1), [1 << 30, -5, 3, pairs + 1, 100, 7, 0, -(1 << 31), 1 << 30][:E + 1],
+                    [0, pairs] * (E // 2 + 1)):
+        for order in (torch.full((pairs,), 1 << 30), torch.full((pairs,), -1), torch.full((pairs,), pairs - 1), some):
+            lists = order.to(torch.int32).cuda(), torch.tensor(offsets[:E + 1], dtype=torch.int32).cuda()
+            H = torch.full((pairs + 2 * guard, N), moe.CANARY, dtype=BF, device="cuda")
+            Y = torch.full((pairs + 2 * guard, N), moe.CANARY, device="cuda")
+            C = torch.full((T + 2 * guard, N), moe.CANARY, dtype=BF, device="cuda")
+            wqd.i4a16_experts_gated(a, ids, *lists, *wg, *wu, H[guard:-guard], T, top_k, E, N, K, group)
+            wqd.i4a16_experts_down(h, ids, weights, *lists, *wd, Y[guard:-guard], C[guard:-guard], T, top_k, E, N, K, group)
+            for x in (H, Y, C):
+                assert bool((x[:guard] == moe.CANARY).all() and (x[-guard:] == moe.CANARY).all())
+
+
+@pytest.mark.parametrize("T", [600, 2000, 8000])
+def test_routed_block_in_tiles(T):
+    """As for few tokens: eagerly, captured and replayed, each step against its definition."""
+    moe.test_routed_block(T)

@@ -3,6 +3,11 @@ every check (and ends at the missing GPU), and what is beyond it is refused."""
 import pytest
 import torch
 
+import test_gpu_i4_lists as gpu_lists
+import test_gpu_i4_paths as gpu_paths
+import test_gpu_i4_range as gpu_range
+import test_gpu_moe as gpu_moe
+import test_i4_paths as paths
 from test_i4_abi import CALLS, EXPERTS, EUNSUPPORTED, call, refused
 from weight_quantized_decode_block_amd import wqd
 
@@ -34,3 +39,39 @@ def test_without_lists_launches_are_the_limit():
     refused("i4a16_experts_gated", few | dict(T=65536, top_k=1), EUNSUPPORTED, "too many")
     refused("i4a16_experts_down", few | dict(T=65536, top_k=1), EUNSUPPORTED, "too many")
     refused("i4a16_experts_gated", few | dict(T=(1 << 21) // 320 + 1, top_k=1, N=5120), EUNSUPPORTED, "too many")
+
+
+# ---------------------------------------------------- the kernels that lists take
+def fit(T, E, top_k, N, lda, gated, bm):
+    """Chunks of bm rows that a call may have, and whether a launch of tiles of them holds it."""
+    pairs, busy = T * top_k, min(T * top_k, E)
+    chunks = (pairs + busy * (bm - 1)) // bm
+    return chunks, (T if gated else pairs) * lda * 2 < 1 << 32 and chunks * -(-N // (128 if gated else 256)) <= 1 << 22
+
+
+def launch(T, E, top_k, N, K, gated, lda=None):
+    """(kernel, launches) of a call with lists: 0 the one for few rows, 1 and 2 tiles of 64 and 128 rows."""
+    lda, pairs, busy = lda or K, T * top_k, min(T * top_k, E)
+    most = min((1 << 21) // -(-N // 16), 65535)
+    launches = -(-fit(T, E, top_k, N, lda, gated, 16)[0] // most)
+    if not fit(T, E, top_k, N, lda, gated, 128)[1]:
+        return 0, launches
+    way = paths.cheapest(paths.costs("kListCosts"), lambda bm: max(pairs // bm + busy // 4, busy), N, K, gated)[0]
+    if way == 0 and launches > 1 or way == 1 and not fit(T, E, top_k, N, lda, gated, 64)[1]:
+        way = 2
+    return way, launches if way == 0 else 1
+
+
+def test_the_tests_take_the_kernels_that_they_name():
+    for gated in (False, True):
+        for sizes, ways in ((gpu_lists.ROUTED, (0, 1, 2)), (gpu_range.ROUTED, (0, 0, 1, 2))):
+            assert [launch(*x, gated) for x in sizes] == [(w, 1) for w in ways]
+        taken = {launch(*x, gated) for x in gpu_paths.LISTS + gpu_moe.EXPERTS}
+        assert taken == {(0, 1), (1, 1), (2, 1)}  # what the costs say, always
+        assert launch(200000, 8, 8, 24, 128, gated) == (2, 1)  # more chunks than a launch for few rows holds
+    assert launch(131072, 64, 8, 64, 2048, False) == (0, 2) and launch(1 << 20, 300, 1, 17, 2048, False) == (0, 2)
+    assert launch(1100000, 6, 1, 32, 256, True, lda=2048) == (0, 2)
+    assert {launch(T, 16, 4, 384, 256, True)[0] for T in (600, 2000, 8000)} == {1, 2}
+    assert {launch(T, 16, 4, 256, 384, False)[0] for T in (600, 2000, 8000)} == {0, 1, 2}
+    product = {i: paths.product(paths.costs("kCosts"), *x, False) for i, x in enumerate(gpu_range.SIZES)}
+    assert product == {0: (0,), 1: (0,), 2: (0,), 3: (1,), 4: (1,), 5: (2,), 6: (3,)}
