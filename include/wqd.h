@@ -425,7 +425,7 @@ int i4a16_gated(const void *A, const void *WG, const void *WGS, const void *WGZ,
  *   score + bias[e], or without a bias the logit itself.  With groups > 1 the experts
  *   are `groups` equal runs, and only those of the top_groups best are chosen
  *   from; a group's value is the sum of its group_top (1 or 2) largest score (+
- *   bias) values.  The top_k largest choice values win, in falling order; among equals
+ *   bias) values, without a bias and with group_top 1 its largest logit.  The top_k largest choice values win, in falling order; among equals
  *   the lowest index (of experts, and of groups) comes first.  weight = score
  *   (without the bias), over the sum of the chosen scores if `renormalize`, times scale.
  * Scores and choice values are 64-bit.  An expert whose logit, or bias, is NaN or minus

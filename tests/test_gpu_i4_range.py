@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import i4_reference as ref
+import test_gpu_moe as moe
 from parity import requires_gpu
 from test_gpu_i4 import BF, out, untouched
 from weight_quantized_decode_block_amd import wqd
@@ -31,6 +32,21 @@ def test_the_largest_activations(M, N, K, group, top):
     wqd.i4a16_gemm(A.cuda(), *w.operands(), C, M, N, K, group)
     want = (A[:2].double() @ w.values()[0].T).to(BF)
     assert bool(torch.isfinite(want).all()) and torch.equal(C[:M].cpu(), want[torch.arange(M) % 2]) and untouched(C, M, N)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_groups_whose_scores_are_equal_in_64_bits(scoring):
+    """Logits of 800 and more: sigmoids are all 1, and softmax has zeros.  Without a bias the largest logit decides between groups
+    (group_top 1), and between experts; the sum of two scores leaves equal groups to the lowest index."""
+    x = torch.full((1, 16), -900.0)
+    x[0, [1, 6, 9, 10, 14]] = torch.tensor([800.0, 850.0, 900.0, 2.0, 1700.0])
+    one, _ = moe.route(x, None, 2, scoring=scoring, groups=4, top_groups=2, group_top=1)
+    two, _ = moe.route(x, None, 2, scoring=scoring, groups=4, top_groups=2, group_top=2)
+    assert one.tolist() == [[14, 9]]  # groups 3 and 2
+    # softmax: group 3 and, of those with zeros, 0; sigmoid: group 2 with 1 + 0.88 and, of those with 1 + 0, 0
+    assert two.tolist() == ([[14, 1]] if scoring == "softmax" else [[9, 1]])
+    for group_top in (1, 2):
+        moe.check_route(x, None, 2, scoring=scoring, groups=4, top_groups=2, group_top=group_top)
 
 
 def both(fn, operands, into, a, at, bad):
