@@ -22,12 +22,12 @@
 //     matrix instruction (32 cycles) there is room for six others of its wave, beside a 16
 //     x 16 x 32 one for two.  Hence 32 x 32, and no more than two instructions for a pair of
 //     codes.  Of a step of 128 rows (1.45 us on 160 compute units) the matrix instructions
-//     take 0.9 at the highest clock; when it took 1.63 it was 0.25 us shorter without the
-//     folds, 0.3 without the sums, 0.24 without the transfers and 0.13 without the conversions.
-//     Where all compute units work the clock falls to about 2 GHz: 4096 x 5120, K = 5120 211
-//     us, 1.02 PFLOP/s, 16384 x 2048, K = 4096 1.14.
+//     take 0.9 at the highest clock.
+//     Where all compute units work the clock falls to about 2 GHz: 4096 x 5120, K = 5120 208 - 214
+//     us, 1.0 PFLOP/s, 16384 x 2048, K = 4096 267 us, 1.03.
 //   * The sums of a group are a matrix accumulator of their own, which the scale
-//     adds to the output's in fp32: nothing but the output is rounded.
+//     adds to the output's, all in fp32.  What is rounded in them are sums of a (16 + q) and their
+//     remainder after (16 + z) times those of a, which may be a few times the sum that is meant.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -564,7 +564,8 @@ hipError_t launch_dense(const I4Operands &op, hipStream_t stream) {
 
 // What a way to multiply takes, in ns: one round of its tiles over 256 compute units (`first` and
 // `first_step` for each 128 k), and every further one.  Measured at 24 to 1024 rows times 512, 5120 and 17408 outputs,
-// K = 512 to 17408 (MI355X, weights from memory).
+// K = 512 to 17408 (MI355X, weights from memory).  Several full rounds, where the clock falls, take up to a third longer than
+// these say (4096 x 4096, K = 5120 160 us, here 127).
 struct Cost {
   uint32_t bm, bn;  // outputs of a tile, half as many in the gated form
   uint32_t first, first_step, more, more_step;
