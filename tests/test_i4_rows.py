@@ -69,6 +69,17 @@ def test_shapes_that_are_neither(library, name):  # noqa: F811
     assert not library.calls
 
 
+@pytest.mark.parametrize("shape,E,N,K,group,by_row", [
+    ((1, 64, 16), 1, 64, 2048, 128, True), ((64, 16), 1, 64, 2048, 128, True), ((80, 16), 1, 70, 2048, 128, True),
+    ((1, 4, 16, 16), 1, 64, 2048, 128, None), ((4, 16, 16), 1, 64, 2048, 128, None),  # [row tile][group][row], [row tile][row][group]
+    ((1, 4, 16, 16, 1), 1, 64, 2048, 128, False), ((16, 16, 1), 1, 16, 2048, 128, False), ((16, 64), 1, 64, 2048, 128, None),
+    ((3, 64, 16), 3, 64, 2048, 128, True), ((192, 16), 3, 64, 2048, 128, True), ((3, 80, 16), 3, 70, 2048, 128, None), ((240, 16), 3, 70, 2048, 128, None),
+    ((3, 1024), 3, 64, 2048, 128, False), ((4096,), 4, 64, 2048, 128, False), ((3, 70, 4), 3, 70, 128, 32, True), ((3, 5, 1, 16, 4), 3, 70, 128, 32, False),
+])
+def test_shapes(shape, E, N, K, group, by_row):
+    assert wqd._i4_by_row(torch.Size(shape), E, N, K, group) is by_row
+
+
 @pytest.mark.parametrize("name", list(AT))
 def test_rows_that_are_too_few_or_elsewhere(library, name):  # noqa: F811
     own, by_row = operands()[name], rows(name)

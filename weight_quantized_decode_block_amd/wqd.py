@@ -443,7 +443,7 @@ def _i4_by_row(shape, E: int, N: int, K: int, group: int) -> bool | None:
     last, g = shape[-1], K // group
     if n > 2 and shape[-2] == 16 and last * group == 128 and shape[-3] * 128 == K:
         return False
-    if last == g and (E == 1 or shape[-2] == (N if n > 2 else E * N)):
+    if last == g and (shape[-2] >= N if E == 1 else shape[-2] == (N if n > 2 else E * N)):
         return True
     return None if last % ((N + 15 & -16) * g or 1) else False
 
